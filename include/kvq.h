@@ -15,6 +15,14 @@
  *                    a sequence's codes and scales out of / into the pool
  *   kvq_stream_plan / kvq_stream_fetch
  *                    a resident window of device blocks over a host copy
+ *   kvq_plan_step    block tables and slot maps of a step from the requests'
+ *                    lengths, on the device
+ *   kvq_bound_blocks bounds of each block's keys
+ *   kvq_select_blocks
+ *                    the blocks each query token and KV head attends to,
+ *                    chosen by those bounds
+ *   kvq_sparse_decode_attn
+ *                    decode attention over such lists of blocks
  *
  * Sources (page title, section):
  *   [kv-q8 PR]  "#3084 qwen35: FP16 K/V cache by default, int8 with --kv-q8
@@ -445,6 +453,151 @@ kvq_status kvq_decode_attn_static(const kvq_cache *cache, const float *q, int n_
                                   int n_q, const int32_t *ctx_lens, int max_ctx,
                                   const int32_t *block_table, int max_blocks_per_seq,
                                   float sm_scale, float *out, void *stream);
+
+/*
+ * One serving step's block tables and slot maps, built on the device from
+ * the requests' lengths: what kvq_append (tok_seq, tok_pos, the table) and
+ * the attention calls (the lengths) take, without a copy to the host.
+ *
+ *   ctx_in        device int32 [n_seq]: cells each sequence holds
+ *   n_new         device int32 [n_seq]: tokens it gets this step (0: none);
+ *                 negative: the sequence ends and gives its blocks back
+ *   block_table   device int32 [n_seq][max_blocks_per_seq], updated in
+ *                 place: new entries follow the old ones (a released row
+ *                 keeps its entries, which its length of 0 leaves unread)
+ *   free_list     device int32 [n_blocks], updated in place: a stack of
+ *                 free block ids, its top at index *free_count_in - 1
+ *   free_count_in device int32 [1]
+ *   max_tok       host int: capacity of the token arrays
+ *   ctx_out       device int32 [n_seq]: ctx_in + n_new, 0 for a released one
+ *   tok_start     device int32 [n_seq + 1]: each sequence's first token
+ *   tok_seq, tok_pos, slots
+ *                 device int32 [max_tok], 16-byte aligned: each token's
+ *                 sequence, its position, and its cell in the pool (block *
+ *                 block_size + offset; slots may be NULL), the sequences in
+ *                 order; -1 past the last token, which kvq_append skips, so a
+ *                 captured graph can append all max_tok rows
+ *   free_count_out device int32 [1]
+ *   info          device int32 [4], 16-byte aligned: tokens, blocks handed
+ *                 out, blocks given back, status
+ *
+ * Blocks given back are pushed in (sequence, column) order, then the new
+ * ones are popped in (sequence, column) order, so a step may hand out what
+ * it got back.  A step that cannot be placed leaves lengths, tables, list
+ * and count as they were, places no token (tok_start 0, the token arrays
+ * -1, info 0, 0, 0, status) and says why in status, a sum of:
+ */
+#define KVQ_PLAN_TOKENS 1 /* more than max_tok tokens                        */
+#define KVQ_PLAN_ROW 2    /* a sequence longer than its row, or ctx_in < 0   */
+#define KVQ_PLAN_BLOCKS 4 /* not enough free blocks                          */
+#define KVQ_PLAN_LIST 8   /* free_count_in outside [0, n_blocks], or more    */
+                          /* blocks given back than the list holds           */
+/*
+ * Output arrays must not overlap one another or an input (KVQ_ERR_ARG): a
+ * step reads one set of lengths and count and writes another.  n_seq <=
+ * 16384 and max_tok <= 2^30, else KVQ_ERR_UNSUPPORTED; n_blocks * block_size
+ * and max_blocks_per_seq * block_size < 2^31; block_size as in kvq_cache.
+ * Table and list entries read must be block ids the caller owns; they are
+ * copied, not followed.  One launch, no workspace.
+ */
+kvq_status kvq_plan_step(const int32_t *ctx_in, const int32_t *n_new, int n_seq, int block_size,
+                         int n_blocks, int32_t *block_table, int max_blocks_per_seq,
+                         int32_t *free_list, const int32_t *free_count_in, int max_tok,
+                         int32_t *ctx_out, int32_t *tok_start, int32_t *tok_seq, int32_t *tok_pos,
+                         int32_t *slots, int32_t *free_count_out, int32_t *info, void *stream);
+
+/*
+ * Bounds of the keys of every block that cells [ctx_start[b], ctx_lens[b])
+ * touch (after the append that wrote them): per KV head and dim the smallest
+ * and largest dequantised K over the block's cells below ctx_lens[b], as
+ * int8 codes rounded outwards.
+ *
+ *   ctx_start    device int32 [n_seq]: first cell that changed (NULL: 0,
+ *                all blocks)
+ *   ctx_lens     device int32 [n_seq]
+ *   max_new      host int: an upper bound of ctx_lens - ctx_start; blocks
+ *                beyond what it covers keep their old bounds
+ *   bounds       device int8 [n_blocks][n_kv_heads][2][head_dim], 256-byte
+ *                aligned: lo codes, then hi codes
+ *   bound_scales device fp32 [n_blocks][n_kv_heads][head_dim / 64]
+ *
+ * Per 64 dims the scale is 2^e, e in [-24, 16] the smallest with 127 * 2^e
+ * >= max(|lo|, |hi|); the codes are floor(lo / 2^e) and ceil(hi / 2^e).  The
+ * result is bit-identical to that definition for finite keys; NaN keys are
+ * passed over (a dim with nothing else gets 0), infinite ones give codes of
+ * +-127 at e = 16.  Bounds belong to the physical block: blocks shared by
+ * several rows need one call, and a block that is refilled needs a new one.
+ * Sequences with ctx_start >= ctx_lens and blocks with an id out of range
+ * are skipped.  max_new == 0 is a no-op.
+ */
+kvq_status kvq_bound_blocks(const kvq_cache *cache, const int32_t *block_table, int n_seq,
+                            int max_blocks_per_seq, const int32_t *ctx_start,
+                            const int32_t *ctx_lens, int max_new, void *bounds,
+                            float *bound_scales, void *stream);
+
+/*
+ * The blocks each query token attends to, chosen per KV head by an upper
+ * bound of its logits over each block.
+ *
+ *   q          device fp32 [n_seq][W][n_q][head_dim], 16-byte aligned, as
+ *              kvq_decode_attn takes it (token w sees cells [0, ctx_lens[b]
+ *              - W + w]); any W >= 1
+ *   max_ctx    host int: an upper bound of ctx_lens
+ *   n_sel      blocks per list, of which the first n_first and the last
+ *              n_last visible blocks are always kept (n_first + n_last <=
+ *              n_sel)
+ *   sel_blocks device int32 [n_seq][W][n_kv_heads][n_sel]: pool block ids, in
+ *              ascending order of the blocks' place in the sequence, -1 past
+ *              the list's end
+ *   sel_index  the same entries as indexes into the sequence's row, or NULL
+ *   sel_lens   device int32 [n_seq][W][n_kv_heads]: cells the list holds (the
+ *              last visible block, if chosen, counts its visible cells)
+ *
+ * Only cache's geometry is read.  Score of a block: per 64 dims of a query
+ * row, the scale 2^f is the smallest (f in [-60, 60]) with 127 * 2^f >=
+ * max|q| and the codes are c = rint(q / 2^f), half to even (NaN: 0); S =
+ * sum over the dims of max(c, 0) hi + min(c, 0) lo over the bounds' codes, a
+ * whole number; t = S * 2^f * bound_scale, exact in fp32 for the scales
+ * kvq_bound_blocks writes; the score is t0, t0 + t1, or (t0 + t1) + (t2 +
+ * t3) in fp32, and the largest over the KV head's n_q / n_kv_heads query
+ * heads counts.  The n_sel highest visible blocks are taken, ties to the
+ * lower index; blocks whose id is out of range never are.  The result is
+ * bit-identical to that definition.
+ *
+ * n_q / n_kv_heads <= 32, ceil(max_ctx / block_size) <= 32768, n_seq * W *
+ * n_kv_heads <= 2^24, n_sel * block_size < 2^30, else KVQ_ERR_UNSUPPORTED.
+ * One launch, no workspace.
+ */
+kvq_status kvq_select_blocks(const kvq_cache *cache, const void *bounds, const float *bound_scales,
+                             const float *q, int n_seq, int W, int n_q, const int32_t *ctx_lens,
+                             int max_ctx, const int32_t *block_table, int max_blocks_per_seq,
+                             int n_sel, int n_first, int n_last, int32_t *sel_blocks,
+                             int32_t *sel_index, int32_t *sel_lens, void *stream);
+
+/*
+ * kvq_decode_attn over a list of blocks for each (sequence, query token, KV
+ * head), as kvq_select_blocks writes them (any lists will do).
+ *
+ *   q, out     device fp32 [n_seq][W][n_q][head_dim], 16-byte aligned; any
+ *              W >= 1
+ *   sel_blocks device int32 [n_seq][W][n_kv_heads][n_sel]: pool block ids
+ *   sel_lens   device int32 [n_seq][W][n_kv_heads]: cells of each list: the
+ *              first sel_lens of its blocks' cells, block by block, are
+ *              attended to (clamped to [0, n_sel * block_size]; 0 gives 0)
+ *   workspace  at least kvq_sparse_workspace_bytes(), 256-byte aligned, under
+ *              kvq_decode_attn's rules
+ *
+ * Cells of a block whose id is out of range are masked.  Precision, formats,
+ * checks and errors as kvq_decode_attn; n_q / n_kv_heads <= 32, n_seq * W *
+ * n_kv_heads <= 2^24 and n_sel * block_size < 2^30, else
+ * KVQ_ERR_UNSUPPORTED.  kvq_sparse_workspace_bytes returns 0 for invalid
+ * arguments.
+ */
+size_t kvq_sparse_workspace_bytes(const kvq_cache *cache, int n_seq, int W, int n_q, int n_sel);
+kvq_status kvq_sparse_decode_attn(const kvq_cache *cache, const float *q, int n_seq, int W, int n_q,
+                                  const int32_t *sel_blocks, const int32_t *sel_lens, int n_sel,
+                                  float sm_scale, float *out, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 /* Static, human-readable name of a status code. */
 const char *kvq_status_string(int status);

@@ -29,6 +29,12 @@ KVQ_ERR_UNSUPPORTED = 2
 KVQ_ERR_WORKSPACE = 3
 KVQ_ERR_CUDA = 4
 
+# kvq_plan_step's status (info[3]): why a step was not placed
+KVQ_PLAN_TOKENS = 1
+KVQ_PLAN_ROW = 2
+KVQ_PLAN_BLOCKS = 4
+KVQ_PLAN_LIST = 8
+
 # Every symbol the C header declares, in the order it declares them.
 EXPORTED_SYMBOLS = (
     "kvq_block_bytes",
@@ -44,6 +50,11 @@ EXPORTED_SYMBOLS = (
     "kvq_stream_plan",
     "kvq_stream_fetch",
     "kvq_decode_attn_static",
+    "kvq_plan_step",
+    "kvq_bound_blocks",
+    "kvq_select_blocks",
+    "kvq_sparse_workspace_bytes",
+    "kvq_sparse_decode_attn",
     "kvq_status_string",
 )
 
@@ -118,6 +129,16 @@ def load_library(path: Optional[str] = None):
     lib.kvq_stream_fetch.argtypes = [CP, CP, P, P, I, P]
     lib.kvq_decode_attn_static.restype = I
     lib.kvq_decode_attn_static.argtypes = [CP, P, I, I, I, P, I, P, I, ctypes.c_float, P, P]
+    lib.kvq_plan_step.restype = I
+    lib.kvq_plan_step.argtypes = [P, P, I, I, I, P, I, P, P, I, P, P, P, P, P, P, P, P]
+    lib.kvq_bound_blocks.restype = I
+    lib.kvq_bound_blocks.argtypes = [CP, P, I, I, P, P, I, P, P, P]
+    lib.kvq_select_blocks.restype = I
+    lib.kvq_select_blocks.argtypes = [CP, P, P, P, I, I, I, P, I, P, I, I, I, I, P, P, P, P]
+    lib.kvq_sparse_workspace_bytes.restype = Z
+    lib.kvq_sparse_workspace_bytes.argtypes = [CP, I, I, I, I]
+    lib.kvq_sparse_decode_attn.restype = I
+    lib.kvq_sparse_decode_attn.argtypes = [CP, P, I, I, I, P, P, I, ctypes.c_float, P, P, Z, P]
     lib.kvq_status_string.restype = ctypes.c_char_p
     lib.kvq_status_string.argtypes = [I]
     if path is None:
@@ -267,6 +288,45 @@ def kvq_decode_attn_lost_wait_test(cache: kvq_cache, q, n_seq: int, W: int, n_q:
         ctypes.byref(cache), _ptr(q), n_seq, W, n_q, _ptr(ctx_lens), max_ctx, _ptr(block_table),
         max_blocks_per_seq, float(sm_scale), _ptr(out), _ptr(workspace), workspace_bytes,
         wait_limit, extra_tx_bytes, _stream(stream))
+
+
+def kvq_plan_step(ctx_in, n_new, n_seq: int, block_size: int, n_blocks: int, block_table,
+                  max_blocks_per_seq: int, free_list, free_count_in, max_tok: int, ctx_out,
+                  tok_start, tok_seq, tok_pos, slots, free_count_out, info, stream=None) -> int:
+    return load_library().kvq_plan_step(
+        _ptr(ctx_in), _ptr(n_new), n_seq, block_size, n_blocks, _ptr(block_table),
+        max_blocks_per_seq, _ptr(free_list), _ptr(free_count_in), max_tok, _ptr(ctx_out),
+        _ptr(tok_start), _ptr(tok_seq), _ptr(tok_pos), _ptr(slots), _ptr(free_count_out),
+        _ptr(info), _stream(stream))
+
+
+def kvq_bound_blocks(cache: kvq_cache, block_table, n_seq: int, max_blocks_per_seq: int, ctx_start,
+                     ctx_lens, max_new: int, bounds, bound_scales, stream=None) -> int:
+    return load_library().kvq_bound_blocks(
+        ctypes.byref(cache), _ptr(block_table), n_seq, max_blocks_per_seq, _ptr(ctx_start),
+        _ptr(ctx_lens), max_new, _ptr(bounds), _ptr(bound_scales), _stream(stream))
+
+
+def kvq_select_blocks(cache: kvq_cache, bounds, bound_scales, q, n_seq: int, W: int, n_q: int,
+                      ctx_lens, max_ctx: int, block_table, max_blocks_per_seq: int, n_sel: int,
+                      n_first: int, n_last: int, sel_blocks, sel_index, sel_lens,
+                      stream=None) -> int:
+    return load_library().kvq_select_blocks(
+        ctypes.byref(cache), _ptr(bounds), _ptr(bound_scales), _ptr(q), n_seq, W, n_q,
+        _ptr(ctx_lens), max_ctx, _ptr(block_table), max_blocks_per_seq, n_sel, n_first, n_last,
+        _ptr(sel_blocks), _ptr(sel_index), _ptr(sel_lens), _stream(stream))
+
+
+def kvq_sparse_workspace_bytes(cache: kvq_cache, n_seq: int, W: int, n_q: int, n_sel: int) -> int:
+    return int(load_library().kvq_sparse_workspace_bytes(ctypes.byref(cache), n_seq, W, n_q, n_sel))
+
+
+def kvq_sparse_decode_attn(cache: kvq_cache, q, n_seq: int, W: int, n_q: int, sel_blocks, sel_lens,
+                           n_sel: int, sm_scale: float, out, workspace, workspace_bytes: int,
+                           stream=None) -> int:
+    return load_library().kvq_sparse_decode_attn(
+        ctypes.byref(cache), _ptr(q), n_seq, W, n_q, _ptr(sel_blocks), _ptr(sel_lens), n_sel,
+        float(sm_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream))
 
 
 def kvq_status_string(status: int) -> str:

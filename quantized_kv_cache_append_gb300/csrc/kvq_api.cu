@@ -67,6 +67,11 @@ int sm_count() {
 
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// Block lists are about equally long, so one wave of splits (attention over
+// 4096 cells, 1 / 2 / 4 waves: one sequence 9.2 / 11.7 / 11.7 us, 16 int8
+// sequences 35.0 / 37.0 / 41.4 us, 64 FP16 sequences 170 / 170 / 181 us).
+constexpr int kListWaves = 1;
+
 // Split plan: one wave of partial CTAs (as many as are resident per SM, on
 // every SM; four times that for batches, whose ragged lengths need short
 // splits to fill the tail of the launch) over all (sequence, KV head, row
@@ -75,14 +80,16 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // With max_bytes set, the split count is lowered until the workspace fits
 // (false if even one split per pair does not).  use_mma is 0 when the
 // kernel's one-time setup failed.
+// Block lists (lists): the plan of their own kernels, kListWaves waves.
 bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, DecodePlan* p,
-                 size_t max_bytes = SIZE_MAX) {
+                 size_t max_bytes = SIZE_MAX, bool lists = false) {
   const int G = n_q / c->n_kv_heads;
   p->rows = G * W;
   const int cta_rows = mma_rows_per_cta(c->head_dim);
   p->rt_rows = p->rows < cta_rows ? p->rows : cta_rows;
   p->n_rt = (p->rows + p->rt_rows - 1) / p->rt_rows;
-  int per_sm = mma_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows);
+  int per_sm = lists ? lists_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows)
+                     : mma_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows);
   p->use_mma = per_sm > 0;
   if (!p->use_mma) per_sm = 1;   // still a plan (and a workspace size); the launch is refused
   const int tile = mma_cell_tile();
@@ -91,7 +98,7 @@ bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, Dec
   int sms = sm_count();
   if (sms <= 0) sms = 148;
   const long long capacity = (long long)per_sm * sms;
-  const long long target = capacity * (n_seq > 1 ? 4 : 1);
+  const long long target = capacity * (lists ? kListWaves : n_seq > 1 ? 4 : 1);
   long long ns = target / units;
   if (ns < 1) ns = 1;
   if (ns > tiles) ns = tiles;
@@ -233,6 +240,9 @@ kvq_status decode_impl(const kvq_cache* cache, const float* q, int n_seq, int W,
   a.n_q = n_q;
   a.G = n_q / cache->n_kv_heads;
   a.g_magic = (0x100000000ull + (unsigned long long)a.G - 1) / (unsigned long long)a.G;
+  a.n_kv = cache->n_kv_heads;
+  a.div_heads = make_fastdiv(1);
+  a.div_nseq = make_fastdiv(1);
   a.div_nkv = make_fastdiv((unsigned)cache->n_kv_heads);
   a.div_nrt = make_fastdiv((unsigned)plan.n_rt);
   a.div_split = make_fastdiv((unsigned)plan.split_cells);
@@ -275,6 +285,252 @@ KVQ_API kvq_status kvq_decode_attn_lost_wait_test(const kvq_cache* cache, const 
   return kvq::decode_impl(cache, q, n_seq, W, n_q, ctx_lens, max_ctx, block_table,
                           max_blocks_per_seq, sm_scale, out, workspace, workspace_bytes, stream,
                           false, wait_limit, extra_tx_bytes);
+}
+
+namespace kvq {
+namespace {
+
+// Block lists as the decode plan sees them: each (sequence, token, KV head)
+// is a "sequence" of its own with one KV head, G = n_q / n_kv_heads query
+// rows and up to n_sel blocks of context.
+struct ListShape {
+  kvq_cache one;   // the cache's geometry with one KV head
+  int n_lists, G, max_ctx;
+};
+
+kvq_status check_lists(const kvq_cache* c, int n_seq, int W, int n_q, int n_sel, ListShape* out) {
+  if (n_seq <= 0 || W <= 0 || n_q <= 0 || n_sel <= 0) return KVQ_ERR_ARG;
+  if (n_q % c->n_kv_heads != 0) return KVQ_ERR_ARG;
+  const long long lists = (long long)n_seq * W * c->n_kv_heads, cells = (long long)n_sel * c->block_size;
+  const int G = n_q / c->n_kv_heads;
+  if (lists > (1 << 24) || cells >= (1LL << 30)) return KVQ_ERR_UNSUPPORTED;
+  if (!mma_decode_supported(c->fmt, c->head_dim, G)) return KVQ_ERR_UNSUPPORTED;
+  out->one = *c;
+  out->one.n_kv_heads = 1;
+  out->n_lists = (int)lists;
+  out->G = G;
+  out->max_ctx = (int)cells;
+  return KVQ_OK;
+}
+
+}  // namespace
+}  // namespace kvq
+
+KVQ_API size_t kvq_sparse_workspace_bytes(const kvq_cache* cache, int n_seq, int W, int n_q, int n_sel) {
+  if (check_cache(cache) != KVQ_OK) return 0;
+  ListShape ls;
+  if (check_lists(cache, n_seq, W, n_q, n_sel, &ls) != KVQ_OK) return 0;
+  DecodePlan p;
+  if (!plan_decode(&ls.one, ls.n_lists, 1, ls.G, ls.max_ctx, &p, SIZE_MAX, true)) return 0;
+  return p.bytes;
+}
+
+KVQ_API kvq_status kvq_sparse_decode_attn(const kvq_cache* cache, const float* q, int n_seq, int W,
+                                          int n_q, const int32_t* sel_blocks,
+                                          const int32_t* sel_lens, int n_sel, float sm_scale,
+                                          float* out, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  ListShape ls;
+  st = check_lists(cache, n_seq, W, n_q, n_sel, &ls);
+  if (st != KVQ_OK) return st;
+  if (q == nullptr || out == nullptr || sel_blocks == nullptr || sel_lens == nullptr) return KVQ_ERR_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(sel_blocks, 4) || !aligned(sel_lens, 4))
+    return KVQ_ERR_ARG;
+  if (!(sm_scale == sm_scale) || isinf(sm_scale)) return KVQ_ERR_ARG;
+  if (workspace == nullptr || !aligned(workspace, 256)) return KVQ_ERR_WORKSPACE;
+  DecodePlan plan;
+  if (!plan_decode(&ls.one, ls.n_lists, 1, ls.G, ls.max_ctx, &plan, SIZE_MAX, true)) return KVQ_ERR_ARG;
+  if (workspace_bytes < plan.bytes) return KVQ_ERR_WORKSPACE;
+  if (!plan.use_mma) return KVQ_ERR_CUDA;
+  DecodeArgs a;
+  a.pool = make_pool(cache);
+  a.n_kv = 1;
+  a.div_heads = make_fastdiv((unsigned)cache->n_kv_heads);
+  a.div_nseq = make_fastdiv((unsigned)ls.n_lists);
+  a.q = q;
+  a.out = out;
+  a.ctx_lens = sel_lens;
+  a.block_table = sel_blocks;
+  a.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.off_o);
+  a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.off_ml);
+  a.n_seq = ls.n_lists;
+  a.W = 1;
+  a.n_q = ls.G;
+  a.G = ls.G;
+  a.g_magic = (0x100000000ull + (unsigned long long)a.G - 1) / (unsigned long long)a.G;
+  a.div_nkv = make_fastdiv(1);
+  a.div_nrt = make_fastdiv((unsigned)plan.n_rt);
+  a.div_split = make_fastdiv((unsigned)plan.split_cells);
+  a.R = plan.rows;
+  a.RT = plan.rt_rows;
+  a.n_rt = plan.n_rt;
+  a.max_blocks = n_sel;
+  a.split_cells = plan.split_cells;
+  a.nsplit = plan.nsplit;
+  a.qscale = sm_scale * 1.4426950408889634f;  // log2(e)
+  a.wait_limit = kDefaultWaitLimit;
+  a.extra_tx = 0;
+  const cudaError_t e =
+      launch_decode_lists(cache->fmt, cache->head_dim, plan, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+namespace kvq {
+namespace {
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a != nullptr && b != nullptr && x < y + bn && y < x + an;
+}
+
+}  // namespace
+}  // namespace kvq
+
+KVQ_API kvq_status kvq_plan_step(const int32_t* ctx_in, const int32_t* n_new, int n_seq, int block_size,
+                                 int n_blocks, int32_t* block_table, int max_blocks_per_seq,
+                                 int32_t* free_list, const int32_t* free_count_in, int max_tok,
+                                 int32_t* ctx_out, int32_t* tok_start, int32_t* tok_seq,
+                                 int32_t* tok_pos, int32_t* slots, int32_t* free_count_out,
+                                 int32_t* info, void* stream) {
+  if (n_seq <= 0 || n_blocks <= 0 || max_blocks_per_seq <= 0 || max_tok < 0) return KVQ_ERR_ARG;
+  if (block_size < 16 || block_size > 1024 || log2_exact(block_size) < 0) return KVQ_ERR_ARG;
+  if ((long long)n_blocks * block_size >= (1LL << 31) ||
+      (long long)max_blocks_per_seq * block_size >= (1LL << 31))
+    return KVQ_ERR_ARG;
+  if (ctx_in == nullptr || n_new == nullptr || block_table == nullptr || free_list == nullptr ||
+      free_count_in == nullptr || ctx_out == nullptr || tok_start == nullptr ||
+      free_count_out == nullptr || info == nullptr)
+    return KVQ_ERR_ARG;
+  if (max_tok > 0 && (tok_seq == nullptr || tok_pos == nullptr)) return KVQ_ERR_ARG;
+  if (!aligned(ctx_in, 4) || !aligned(n_new, 4) || !aligned(block_table, 4) || !aligned(free_list, 4) ||
+      !aligned(free_count_in, 4) || !aligned(ctx_out, 4) || !aligned(tok_start, 4) ||
+      !aligned(free_count_out, 4) || !aligned(tok_seq, 16) || !aligned(tok_pos, 16) ||
+      !aligned(slots, 16) || !aligned(info, 16))
+    return KVQ_ERR_ARG;
+  // what is read is not written in the same call (but for the table and the
+  // free list, whose entries are either read or written)
+  const struct { const void* p; size_t n; } in[] = {
+      {ctx_in, 4ull * n_seq}, {n_new, 4ull * n_seq}, {free_count_in, 4},
+      {block_table, 4ull * n_seq * max_blocks_per_seq}, {free_list, 4ull * n_blocks}};
+  const struct { const void* p; size_t n; } out[] = {
+      {ctx_out, 4ull * n_seq}, {tok_start, 4ull * (n_seq + 1)}, {tok_seq, 4ull * max_tok},
+      {tok_pos, 4ull * max_tok}, {slots, 4ull * max_tok}, {free_count_out, 4}, {info, 16},
+      {block_table, 4ull * n_seq * max_blocks_per_seq}, {free_list, 4ull * n_blocks}};
+  for (const auto& o : out) {
+    for (const auto& i : in)
+      if (i.p != o.p || (o.p != block_table && o.p != free_list))
+        if (overlap(i.p, i.n, o.p, o.n)) return KVQ_ERR_ARG;
+    for (const auto& p : out)
+      if (&p != &o && overlap(p.p, p.n, o.p, o.n)) return KVQ_ERR_ARG;
+  }
+  if (n_seq > kPlanMaxSeq || max_tok > (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+  PlanArgs a;
+  a.ctx_in = ctx_in;
+  a.n_new = n_new;
+  a.block_table = a.block_table_out = block_table;
+  a.free_list = a.free_list_out = free_list;
+  a.free_count_in = free_count_in;
+  a.ctx_out = ctx_out;
+  a.tok_start = tok_start;
+  a.tok_seq = tok_seq;
+  a.tok_pos = tok_pos;
+  a.slots = slots;
+  a.free_count_out = free_count_out;
+  a.info = info;
+  a.n_seq = n_seq;
+  a.max_blocks = max_blocks_per_seq;
+  a.bs_log2 = log2_exact(block_size);
+  a.n_blocks = n_blocks;
+  a.max_tok = max_tok;
+  const int sms = sm_count();
+  const cudaError_t e = launch_plan_step(a, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+KVQ_API kvq_status kvq_bound_blocks(const kvq_cache* cache, const int32_t* block_table, int n_seq,
+                                    int max_blocks_per_seq, const int32_t* ctx_start,
+                                    const int32_t* ctx_lens, int max_new, void* bounds,
+                                    float* bound_scales, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (n_seq <= 0 || max_blocks_per_seq <= 0 || max_new < 0) return KVQ_ERR_ARG;
+  if (max_new == 0) return KVQ_OK;
+  if (block_table == nullptr || ctx_lens == nullptr || bounds == nullptr || bound_scales == nullptr)
+    return KVQ_ERR_ARG;
+  if (!aligned(block_table, 4) || !aligned(ctx_start, 4) || !aligned(ctx_lens, 4) ||
+      !aligned(bounds, 256) || !aligned(bound_scales, 16))
+    return KVQ_ERR_ARG;
+  if ((long long)max_new > (long long)max_blocks_per_seq * cache->block_size) return KVQ_ERR_ARG;
+  BoundArgs a;
+  a.pool = make_pool(cache);
+  a.block_table = block_table;
+  a.ctx_start = ctx_start;
+  a.ctx_lens = ctx_lens;
+  a.bounds = static_cast<int8_t*>(bounds);
+  a.scales = bound_scales;
+  a.n_seq = n_seq;
+  a.max_blocks = max_blocks_per_seq;
+  // max_new cells that start anywhere in a block
+  const long long bs = cache->block_size;
+  long long touched = ctx_start == nullptr ? (max_new + bs - 1) / bs : (max_new + bs - 2) / bs + 1;
+  if (touched > max_blocks_per_seq) touched = max_blocks_per_seq;
+  a.touched = (int)touched;
+  if ((long long)n_seq * touched * cache->n_kv_heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
+  const cudaError_t e =
+      launch_bound_blocks(cache->fmt, cache->head_dim, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+KVQ_API kvq_status kvq_select_blocks(const kvq_cache* cache, const void* bounds,
+                                     const float* bound_scales, const float* q, int n_seq, int W,
+                                     int n_q, const int32_t* ctx_lens, int max_ctx,
+                                     const int32_t* block_table, int max_blocks_per_seq, int n_sel,
+                                     int n_first, int n_last, int32_t* sel_blocks,
+                                     int32_t* sel_index, int32_t* sel_lens, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (n_seq <= 0 || W <= 0 || n_q <= 0 || max_ctx <= 0 || max_blocks_per_seq <= 0) return KVQ_ERR_ARG;
+  if (n_q % cache->n_kv_heads != 0) return KVQ_ERR_ARG;
+  if ((long long)max_ctx > (long long)max_blocks_per_seq * cache->block_size) return KVQ_ERR_ARG;
+  if (n_sel <= 0 || n_first < 0 || n_last < 0 || (long long)n_first + n_last > n_sel) return KVQ_ERR_ARG;
+  if (bounds == nullptr || bound_scales == nullptr || q == nullptr || ctx_lens == nullptr ||
+      block_table == nullptr || sel_blocks == nullptr || sel_lens == nullptr)
+    return KVQ_ERR_ARG;
+  if (!aligned(bounds, 256) || !aligned(bound_scales, 16) || !aligned(q, 16) || !aligned(ctx_lens, 4) ||
+      !aligned(block_table, 4) || !aligned(sel_blocks, 4) || !aligned(sel_index, 4) ||
+      !aligned(sel_lens, 4))
+    return KVQ_ERR_ARG;
+  SelectArgs a;
+  a.bounds = static_cast<const int8_t*>(bounds);
+  a.scales = bound_scales;
+  a.q = q;
+  a.ctx_lens = ctx_lens;
+  a.block_table = block_table;
+  a.sel_blocks = sel_blocks;
+  a.sel_index = sel_index;
+  a.sel_lens = sel_lens;
+  a.n_seq = n_seq;
+  a.W = W;
+  a.n_q = n_q;
+  a.n_kv = cache->n_kv_heads;
+  a.G = n_q / cache->n_kv_heads;
+  a.bs_log2 = log2_exact(cache->block_size);
+  a.n_blocks = cache->n_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.n_cap = (max_ctx + cache->block_size - 1) / cache->block_size;
+  a.n_sel = n_sel;
+  a.n_first = n_first;
+  a.n_last = n_last;
+  if (a.G > 32 || a.n_cap > kSelMaxBlocks || (long long)n_sel * cache->block_size >= (1LL << 30) ||
+      (long long)n_seq * W * cache->n_kv_heads > (1 << 24))
+    return KVQ_ERR_UNSUPPORTED;
+  const int sms = sm_count();
+  if (!plan_select(cache->head_dim, sms > 0 ? sms : 148, &a)) return KVQ_ERR_UNSUPPORTED;
+  const cudaError_t e = launch_select_blocks(cache->head_dim, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
 KVQ_API kvq_status kvq_compact_f16(const kvq_cache* cache, const int32_t* block_table_row,

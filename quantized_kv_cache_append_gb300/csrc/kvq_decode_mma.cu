@@ -54,15 +54,31 @@
 #include "kvq_internal.cuh"
 #include "kvq_ptx.cuh"
 
+// This file is compiled twice.  As it stands it is the dense decode; included
+// by kvq_decode_lists.cu with KVQ_DECODE_LISTS set it is the decode over block
+// lists (kvq_sparse_decode_attn), whose work items are described at
+// DecodeArgs.
+#ifndef KVQ_DECODE_LISTS
+#define KVQ_DECODE_LISTS 0
+#endif
+
 namespace kvq {
 namespace {
 
+constexpr bool kLists = KVQ_DECODE_LISTS != 0;
 constexpr int kConsumerWarps = 4;
 constexpr int kThreads = kConsumerWarps * 32;  // thread 0 also issues the copies
 constexpr int kTC = 64;                      // cells per pipeline stage (a piece index is
                                              // split by shifts: 64 = 2^6)
 constexpr int kCellsPerWarp = kTC / kConsumerWarps;
 constexpr float kTau = 8.0f;                 // lazy rescale threshold (log2 units)
+// A raised reference maximum lies this far below the row's own (log2 units),
+// so p runs up to 2^kTau.  Dense: 0.  Block lists: kTau, which keeps the fp16
+// lo halves of p (times the V scale, often below 0.05) clear of fp16's
+// subnormals (int8 cache, 16 ragged lists of 4096 cells: relative output
+// error 3.2e-6 without, below 1e-6 with it) at the price of a rescale
+// whenever the maximum rises at all.
+constexpr float kBelowMax = kLists ? kTau : 0.0f;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int FMT, int HD, int NT>
@@ -134,6 +150,13 @@ struct TmaMaps {
 constexpr uint32_t kMagic = 0x64646464u;
 constexpr uint32_t kBias = 0x64806480u;  // fp16 1152 in both halves
 
+// int8 K in q.k.  Dense: as 1152 + code, the 1152 * sum(q) taken off through
+// the accumulator's start (no subtraction per element).  The sums then run
+// at 1152 times the codes' weight and leave a logit error of up to about
+// 1e-5; block lists subtract first (4 HSUB2 more per 16 x 16 tile) and keep
+// it at the FP16 cache's 1e-6.
+constexpr bool kCodesExact = kLists;
+
 // Swizzled shared-memory byte offset of logical byte `b` of cell `c` (0..63)
 // in a K or V tile laid out [span][cell][SWB]: every TMA box (one piece of
 // cells, one span) is placed at its [span][first cell] slot, so the layout
@@ -182,7 +205,7 @@ __device__ __forceinline__ int block_of(const DecodeArgs& a, const int32_t* bt, 
 // warp-wide scan over 32 sequences at a time.  Returns false past the end.
 __device__ __forceinline__ bool item_of(const DecodeArgs& a, int c, int& b, int& kvh, int& split) {
   const int lane = threadIdx.x & 31;
-  const int S = a.split_cells, nkv = a.pool.n_kv;
+  const int S = a.split_cells, nkv = a.n_kv;
   for (int pass = 0; pass < 2; ++pass) {   // 0: full splits, 1: last partial splits
     for (int b0 = 0; b0 < a.n_seq; b0 += 32) {
       const int bb = b0 + lane;
@@ -259,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     // ids read here may still change before the wait below (the copies
     // read them again after the wait), and a prefetch of the wrong rows
     // costs bandwidth, nothing else.
-    if (a.n_seq == 1 && a.n_rt == 1) {
-      const int split0 = (int)fdiv(blockIdx.x, a.div_nkv), kvh0 = (int)blockIdx.x - split0 * a.pool.n_kv;
+    if (a.n_seq == 1 && a.n_rt == 1 && !kLists) {
+      const int split0 = (int)fdiv(blockIdx.x, a.div_nkv), kvh0 = (int)blockIdx.x - split0 * a.n_kv;
       const int c0 = split0 * a.split_cells;
       const int pcl = a.pool.bs_log2 < 6 ? a.pool.bs_log2 : 6;
       const int cap = clamp_len_mma(INT_MAX, a);   // cells the table row can address
@@ -306,12 +329,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   if (single) {
     b = 0;
     split = (int)fdiv((unsigned)item, a.div_nkv);
-    kvh = item - split * a.pool.n_kv;
+    kvh = item - split * a.n_kv;
     L_raw = __ldg(a.ctx_lens);
+  } else if (kLists) {
+    // block lists: split-major, no search (the lists are about equally long)
+    split = (int)fdiv((unsigned)item, a.div_nseq);
+    b = item - split * a.n_seq;
+    kvh = 0;
+    L_raw = __ldg(a.ctx_lens + b);
+    if (split * a.split_cells >= clamp_len_mma(L_raw, a)) return;
   } else {
     if (!item_of(a, item, b, kvh, split)) return;
     L_raw = __ldg(a.ctx_lens + b);
   }
+  // the KV head's place in the pool
+  const int pool_h = kLists ? b - (int)fdiv((unsigned)b, a.div_heads) * a.pool.n_kv : kvh;
   const int c_begin = split * a.split_cells;
   // until the length is known (one sequence), copies stay inside the split
   // and the block table
@@ -356,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       const int blk = blks[p];
       const int c = c0 + (p << pc_log2);
       rows[p] = (p < n_pieces && blk >= 0 && blk < a.pool.n_blocks)
-                    ? (blk * a.pool.n_kv + kvh) * bsz + (c & (bsz - 1))
+                    ? (blk * a.pool.n_kv + pool_h) * bsz + (c & (bsz - 1))
                     : -1;
       if (rows[p] >= 0) bytes += (uint32_t)pc * (C::ROWB + C::VROWB + (C::KI8 ? (C::NG + C::VNS) * 2 : 0));
     }
@@ -480,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     if (n_tiles == 0) {
       // a split past the context: its slots tell the combine "no cells"
       if (producer && n_first > 0) (void)mbar_wait(bar_full, 0, a.wait_limit);
-      const size_t slot0 = (((size_t)b * a.pool.n_kv + kvh) * a.nsplit + split) * a.R;
+      const size_t slot0 = (((size_t)b * a.n_kv + kvh) * a.nsplit + split) * a.R;
       if (threadIdx.x < a.R)
         *reinterpret_cast<float2*>(a.ws_ml + (slot0 + threadIdx.x) * 2) = make_float2(-INFINITY, 0.f);
       return;
@@ -689,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       float acc[2][NT][4];  // hi chain (starts at -1152 sum q), lo chain
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        acc[0][nt][0] = acc[0][nt][2] = qcorr[gq][nt][0];
-        acc[0][nt][1] = acc[0][nt][3] = qcorr[gq][nt][1];
+        acc[0][nt][0] = acc[0][nt][2] = kCodesExact ? 0.f : qcorr[gq][nt][0];
+        acc[0][nt][1] = acc[0][nt][3] = kCodesExact ? 0.f : qcorr[gq][nt][1];
       }
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
@@ -699,6 +731,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
         af[2] = prmt(w[kk][0], kMagic, 0x4342u);
         af[1] = prmt(w[kk][1], kMagic, 0x4140u);
         af[3] = prmt(w[kk][1], kMagic, 0x4342u);
+        if constexpr (kCodesExact) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) af[i] = hsub2(af[i], kBias);
+        }
         if constexpr (HL) {
           // one chain: columns 0-3 hi (start at -1152 sum q), 4-7 lo (at 0)
           mma16816(acc[0][0], af, qreg[gq * 4 + kk][0], qreg[gq * 4 + kk][1]);
@@ -786,8 +822,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 8));
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 16));
         if (tmax > m[nt][j] + kTau) {
-          const float alpha = fast_exp2(m[nt][j] - tmax);  // 0 from the finite start
-          m[nt][j] = tmax;
+          const float top = tmax - kBelowMax;
+          const float alpha = fast_exp2(m[nt][j] - top);  // 0 from the finite start
+          m[nt][j] = top;
           l[nt][j] *= alpha;
 #pragma unroll
           for (int mt = 0; mt < KS; ++mt) {
@@ -1119,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     }
   __syncthreads();
   // this CTA's rows of the split's partial
-  const size_t row0 = (((size_t)b * a.pool.n_kv + kvh) * a.nsplit + split) * a.R + r0;
+  const size_t row0 = (((size_t)b * a.n_kv + kvh) * a.nsplit + split) * a.R + r0;
   if constexpr (C::V4) {
     // K8V4: the merged rows are in the rotated basis; one warp per row sums
     // the slabs, rotates the row back (Walsh-Hadamard, divided by HD) and
@@ -1207,7 +1244,8 @@ __global__ void __launch_bounds__(kCombineThreads, 4) combine_partials(DecodeArg
   __shared__ float4 s_wacc[NW][DV];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int kvh = blockIdx.x, b = blockIdx.y;
+  // (block lists: the grid's x runs over the lists, which may exceed y's limit)
+  const int kvh = kLists ? 0 : blockIdx.x, b = kLists ? blockIdx.x : blockIdx.y;
   const int r = blockIdx.z / CHUNKS, d0 = (blockIdx.z % CHUNKS) * DV * 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int dv = tid % DV, js = tid / DV;
@@ -1218,7 +1256,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) combine_partials(DecodeArg
                                  : (int)fdiv((unsigned)(clamp_len_mma(__ldg(a.ctx_lens + b), a) +
                                                         a.split_cells - 1),
                                              a.div_split);
-  const size_t base0 = ((size_t)b * a.pool.n_kv + kvh) * a.nsplit;
+  const size_t base0 = ((size_t)b * a.n_kv + kvh) * a.nsplit;
 
   float M = kNegInf, lsum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1326,7 +1364,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) combine_partials(DecodeArg
 template <int HD, int DV>
 cudaError_t launch_combine_dv(const DecodeArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cc = {};
-  cc.gridDim = dim3(a.pool.n_kv, a.n_seq, a.R * (HD / 4 / DV));
+  cc.gridDim = kLists ? dim3(a.n_seq, 1, a.R * (HD / 4 / DV)) : dim3(a.n_kv, a.n_seq, a.R * (HD / 4 / DV));
   cc.blockDim = dim3(kCombineThreads);
   cc.stream = s;
   cudaLaunchAttribute pdl[1];
@@ -1411,7 +1449,7 @@ cudaError_t launch_impl(const DecodePlan& p, const DecodeArgs& a, cudaStream_t s
   for (int sp = 0; sp < C::VNCH; ++sp)
     if (!make_map(&maps.v[sp], a.pool.v, C::VSWB, C::VROWB, sp, rows, piece)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  const long long items = (long long)p.nsplit * a.pool.n_kv * a.n_seq * a.n_rt;
+  const long long items = (long long)p.nsplit * a.n_kv * a.n_seq * a.n_rt;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   cfg.gridDim = dim3((unsigned)items);
   cfg.blockDim = dim3(kThreads);
@@ -1454,6 +1492,8 @@ cudaError_t launch_hd(int code, const DecodePlan& p, const DecodeArgs& a, cudaSt
 }
 
 }  // namespace
+
+#if !KVQ_DECODE_LISTS
 
 void* tensor_map_encoder() {
   static void* fn = nullptr;
@@ -1510,7 +1550,17 @@ int mma_rows_per_cta(int hd) { return 8 * (256 / hd); }
 
 int mma_cell_tile() { return kTC; }
 
-int mma_ctas_per_sm(int fmt, int hd, int rows) {
+#endif  // !KVQ_DECODE_LISTS
+
+#if KVQ_DECODE_LISTS
+#define KVQ_CTAS_PER_SM lists_ctas_per_sm
+#define KVQ_LAUNCH launch_decode_lists
+#else
+#define KVQ_CTAS_PER_SM mma_ctas_per_sm
+#define KVQ_LAUNCH launch_decode_mma_partial
+#endif
+
+int KVQ_CTAS_PER_SM(int fmt, int hd, int rows) {
   const int nt = tile_code(rows);
   if (fmt == KVQ_F16) {
     if (hd == 64) return ctas_per_sm_hd<KVQ_F16, 64>(nt);
@@ -1527,8 +1577,7 @@ int mma_ctas_per_sm(int fmt, int hd, int rows) {
   return ctas_per_sm_hd<KVQ_K8V4, 256>(nt);
 }
 
-cudaError_t launch_decode_mma_partial(int fmt, int hd, const DecodePlan& p, const DecodeArgs& a,
-                                      cudaStream_t s) {
+cudaError_t KVQ_LAUNCH(int fmt, int hd, const DecodePlan& p, const DecodeArgs& a, cudaStream_t s) {
   const int nt = tile_code(p.rt_rows);
   if (fmt == KVQ_F16) {
     if (hd == 64) return launch_hd<KVQ_F16, 64>(nt, p, a, s);

@@ -155,6 +155,13 @@ __device__ __forceinline__ unsigned fdiv(unsigned x, const FastDiv& f) {
 
 struct DecodeArgs {
   Pool pool;
+  // The work items' "sequences" and their KV heads.  Dense decode: the
+  // batch's sequences with the pool's KV heads each.  Block lists
+  // (kvq_sparse_decode_attn): one "sequence" per (sequence, token, KV head)
+  // with a block table row and a length of its own and one KV head, whose
+  // place in the pool is the sequence's index mod the pool's KV heads.
+  int n_kv;            // KV heads per "sequence": pool.n_kv, or 1
+  FastDiv div_heads, div_nseq;  // pool.n_kv, n_seq (block lists)
   const float* q;      // [n_seq][W][n_q][hd]
   float* out;          // [n_seq][W][n_q][hd]
   const int32_t* ctx_lens;
@@ -195,9 +202,67 @@ struct PersistArgs {
   __half* scales_v;        // (K8V4: [n_cells][n_kv][hd/32])
 };
 
+// One step's block tables and slot maps (kvq_plan.cu).
+struct PlanArgs {
+  const int32_t* ctx_in;       // [n_seq]
+  const int32_t* n_new;        // [n_seq]: tokens to append, < 0: release the sequence
+  const int32_t* block_table;  // [n_seq][max_blocks], read at old entries ...
+  int32_t* block_table_out;    // ... written at new ones (the same array)
+  const int32_t* free_list;    // [n_blocks], read below the old top ...
+  int32_t* free_list_out;      // ... written above it (the same array)
+  const int32_t* free_count_in;
+  int32_t* ctx_out;            // [n_seq]
+  int32_t* tok_start;          // [n_seq + 1]
+  int32_t* tok_seq;            // [max_tok]
+  int32_t* tok_pos;            // [max_tok]
+  int32_t* slots;              // [max_tok] or null
+  int32_t* free_count_out;
+  int32_t* info;               // [4]
+  int n_seq, max_blocks, bs_log2, n_blocks, max_tok;
+};
+constexpr int kPlanMaxSeq = 16384;   // three prefixes of it fit a CTA's shared memory
+constexpr int plan_smem_bytes(int n_seq) { return 3 * (n_seq + 1) * 4; }
+
+// Bounds of the touched blocks' keys (kvq_bounds.cu).
+struct BoundArgs {
+  Pool pool;
+  const int32_t* block_table;  // [n_seq][max_blocks]
+  const int32_t* ctx_start;    // [n_seq] or null (0): first cell that changed
+  const int32_t* ctx_lens;     // [n_seq]
+  int8_t* bounds;              // [n_blocks][n_kv][2][hd]: lo codes, hi codes
+  float* scales;               // [n_blocks][n_kv][hd / 64]
+  int n_seq, max_blocks;
+  int touched;                 // blocks per sequence the launch covers
+};
+
+// Block selection (kvq_select.cu).
+struct SelectArgs {
+  const int8_t* bounds;
+  const float* scales;
+  const float* q;              // [n_seq][W][n_q][hd]
+  const int32_t* ctx_lens;
+  const int32_t* block_table;
+  int32_t* sel_blocks;         // [n_seq][W][n_kv][n_sel]: pool blocks, -1 past the list
+  int32_t* sel_index;          // the same entries as block indexes of the sequence, or null
+  int32_t* sel_lens;           // [n_seq][W][n_kv]: cells of the list
+  int n_seq, W, n_q, n_kv, G, bs_log2, n_blocks, max_blocks;
+  int n_cap;                   // blocks of the longest context: ceil(max_ctx / block size)
+  int n_sel, n_first, n_last;
+  int wg_tok, n_wg;            // tokens per cluster, clusters per (sequence, KV head)
+  int cluster, lead_rows;      // CTAs per cluster, tokens each of them leads
+};
+constexpr int kSelMaxBlocks = 32768;       // keys of one token: 128 KB of shared memory
+constexpr int kSelMaxSmem = 200 * 1024;
+
 // Launchers (host side, one per translation unit).  They return the launch
 // status from the runtime.
 cudaError_t launch_append(int fmt, int hd, const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_bound_blocks(int fmt, int hd, const BoundArgs& a, cudaStream_t s);
+// Fills in the launch shape (wg_tok, n_wg, cluster, lead_rows); false if the
+// keys of one token do not fit the shared memory.
+bool plan_select(int hd, int sms, SelectArgs* a);
+cudaError_t launch_select_blocks(int hd, const SelectArgs& a, cudaStream_t s);
 cudaError_t launch_compact(int fmt, int hd, const CompactArgs& a, cudaStream_t s);
 cudaError_t launch_persist(int fmt, int hd, bool gather, const PersistArgs& a, cudaStream_t s);
 
@@ -210,6 +275,9 @@ int mma_rows_per_cta(int hd);
 int mma_ctas_per_sm(int fmt, int hd, int rows);
 cudaError_t launch_decode_mma_partial(int fmt, int hd, const DecodePlan& p, const DecodeArgs& a,
                                       cudaStream_t s);
+// The same over block lists (kvq_decode_lists.cu).
+int lists_ctas_per_sm(int fmt, int hd, int rows);
+cudaError_t launch_decode_lists(int fmt, int hd, const DecodePlan& p, const DecodeArgs& a, cudaStream_t s);
 
 // The driver's cuTensorMapEncodeTiled (version 12000), looked up once; null
 // if the driver does not provide it.

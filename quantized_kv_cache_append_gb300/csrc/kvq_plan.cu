@@ -1,0 +1,245 @@
+// kvq_plan.cu -- block tables and slot maps of one serving step, built on
+// the GPU from the requests' lengths (kvq_plan_step).
+//
+// Sequence b holds ceil(ctx_in[b] / block_size) blocks.  With n_new[b] >= 0
+// it grows to ceil((ctx_in[b] + n_new[b]) / block_size); with n_new[b] < 0
+// it ends and gives its blocks back.  Three exclusive prefix sums over the
+// sequences (tokens, blocks handed out, blocks given back) place everything:
+//
+//   given back  j = 0 .. P-1   row entries of the released sequences, in
+//                              (sequence, column) order, pushed on the stack
+//   handed out  i = 0 .. A-1   popped off its top, to the growing sequences
+//                              in (sequence, column) order: pushed[P - 1 - i]
+//                              while i < P, then free_list[count - 1 - (i - P)]
+//   token       t = 0 .. T-1   its sequence by a binary search in the token
+//                              prefix, its position, and its cell
+//
+// One launch, no workspace: every CTA computes the prefixes of all sequences
+// into its own shared memory (a few KB read from L2) and then writes its
+// share of the tokens, table entries and list entries.  Nothing one CTA
+// writes is read by another: new table entries lie past the old ones, a
+// given-back block is either handed out again or stored above the old stack
+// top by the thread that reads it, pops below the old top read entries nobody
+// writes, and the lengths and the count are not updated in place (the call
+// refuses overlapping arrays).
+#include <stdint.h>
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr unsigned kFullMask = 0xffffffffu;
+
+struct Three {
+  unsigned long long tok, grow, back;
+};
+
+__device__ __forceinline__ Three operator+(const Three& a, const Three& b) {
+  return {a.tok + b.tok, a.grow + b.grow, a.back + b.back};
+}
+
+__device__ __forceinline__ Three shfl_up(const Three& a, int d) {
+  return {__shfl_up_sync(kFullMask, a.tok, d), __shfl_up_sync(kFullMask, a.grow, d),
+          __shfl_up_sync(kFullMask, a.back, d)};
+}
+
+// What one sequence adds to the three sums (64-bit: lengths come from the
+// device and may be anything); bad: it does not fit its row of the table.
+__device__ __forceinline__ Three of_sequence(const PlanArgs& a, int b, bool& bad) {
+  const long long ctx = __ldg(a.ctx_in + b), n = __ldg(a.n_new + b);
+  const long long cap = (long long)a.max_blocks << a.bs_log2, up = (1 << a.bs_log2) - 1;
+  const long long add = n > 0 ? n : 0;
+  bad |= ctx < 0 || ctx + add > cap;
+  const long long have = (ctx + up) >> a.bs_log2;
+  Three t = {0, 0, 0};
+  if (ctx < 0) return t;
+  if (n < 0) {
+    t.back = have;
+  } else {
+    t.tok = add;
+    t.grow = ((ctx + add + up) >> a.bs_log2) - have;
+  }
+  return t;
+}
+
+// First sequence whose inclusive prefix end[] is above x (x < end[n - 1]).
+__device__ __forceinline__ int owner_of(const uint32_t* end, int n, uint32_t x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(PlanArgs a) {
+  // inclusive prefixes over the sequences, shifted by one: end[b] at [b + 1]
+  extern __shared__ uint32_t s_pref[];
+  const int n = a.n_seq;
+  uint32_t* s_tok = s_pref;
+  uint32_t* s_grow = s_pref + (n + 1);
+  uint32_t* s_back = s_pref + 2 * (n + 1);
+  __shared__ Three s_warp[kPlanWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // each thread sums a run of consecutive sequences, the runs are scanned
+  const int per = (n + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
+  Three sum = {0, 0, 0};
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) sum = sum + of_sequence(a, b, bad);
+  Three incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Three y = shfl_up(incl, d);
+    if (lane >= d) incl = incl + y;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  const long long count = __ldg(a.free_count_in);
+  const bool any_bad = __syncthreads_or(bad);
+  Three base = {0, 0, 0}, total = {0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) {
+    if (w < warp) base = base + s_warp[w];
+    total = total + s_warp[w];
+  }
+  int status = 0;
+  if (total.tok > (unsigned long long)a.max_tok) status |= KVQ_PLAN_TOKENS;
+  if (any_bad) status |= KVQ_PLAN_ROW;
+  if ((long long)total.grow > count + (long long)total.back) status |= KVQ_PLAN_BLOCKS;
+  if (count < 0 || count + (long long)total.back > a.n_blocks) status |= KVQ_PLAN_LIST;
+  const bool ok = status == 0;
+  const int gtid = blockIdx.x * kPlanThreads + tid, gthreads = gridDim.x * kPlanThreads;
+
+  if (!ok) {  // nothing changes: the lengths stay, no token is placed
+    for (int b = gtid; b < n; b += gthreads) a.ctx_out[b] = __ldg(a.ctx_in + b);
+    for (int b = gtid; b < n + 1; b += gthreads) a.tok_start[b] = 0;
+    for (int t = gtid; t < a.max_tok; t += gthreads) {
+      a.tok_seq[t] = -1;
+      a.tok_pos[t] = -1;
+      if (a.slots != nullptr) a.slots[t] = -1;
+    }
+    if (gtid == 0) {
+      *a.free_count_out = (int32_t)count;
+      *reinterpret_cast<int4*>(a.info) = make_int4(0, 0, 0, status);
+    }
+    return;
+  }
+
+  // all sums fit 32 bits from here on
+  Three run = base + incl;
+  run = {run.tok - sum.tok, run.grow - sum.grow, run.back - sum.back};
+  if (tid == 0) s_tok[0] = s_grow[0] = s_back[0] = 0;
+  bool unused = false;
+  for (int b = b0; b < b1; ++b) {
+    run = run + of_sequence(a, b, unused);
+    s_tok[b + 1] = (uint32_t)run.tok;
+    s_grow[b + 1] = (uint32_t)run.grow;
+    s_back[b + 1] = (uint32_t)run.back;
+  }
+  __syncthreads();
+  const uint32_t T = (uint32_t)total.tok, A = (uint32_t)total.grow, P = (uint32_t)total.back;
+  const int bs_mask = (1 << a.bs_log2) - 1;
+
+  auto pushed = [&](uint32_t j) -> int32_t {   // j-th block given back
+    const int b = owner_of(s_back + 1, n, j);
+    return __ldg(a.block_table + (size_t)b * a.max_blocks + (j - s_back[b]));
+  };
+  auto handed = [&](uint32_t i) -> int32_t {   // i-th block handed out
+    return i < P ? pushed(P - 1 - i) : __ldg(a.free_list + ((uint32_t)count - 1 - (i - P)));
+  };
+
+  // lengths, token starts, totals
+  for (int b = gtid; b < n + 1; b += gthreads) {
+    a.tok_start[b] = (int32_t)s_tok[b];
+    if (b < n) {
+      const int nn = __ldg(a.n_new + b);
+      a.ctx_out[b] = nn < 0 ? 0 : __ldg(a.ctx_in + b) + nn;
+    }
+  }
+  if (gtid == 0) {
+    *a.free_count_out = (int32_t)((uint32_t)count + P - A);
+    *reinterpret_cast<int4*>(a.info) = make_int4((int)T, (int)A, (int)P, 0);
+  }
+  // the new table entries, and what stays on the stack above its old top
+  for (uint32_t i = gtid; i < A; i += gthreads) {
+    const int b = owner_of(s_grow + 1, n, i);
+    const int have = (__ldg(a.ctx_in + b) + bs_mask) >> a.bs_log2;
+    a.block_table_out[(size_t)b * a.max_blocks + have + (i - s_grow[b])] = handed(i);
+  }
+  if (P > A)
+    for (uint32_t j = gtid; j < P - A; j += gthreads) a.free_list_out[(uint32_t)count + j] = pushed(j);
+
+  // tokens: 4 consecutive ones a thread, one search, then a walk
+  for (long long t4 = 4LL * gtid; t4 < a.max_tok; t4 += 4LL * gthreads) {
+    int32_t seq[4], pos[4], slot[4];
+    int b = t4 < T ? owner_of(s_tok + 1, n, (uint32_t)t4) : 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const long long t = t4 + u;
+      seq[u] = pos[u] = slot[u] = -1;
+      if (t < T) {
+        while (s_tok[b + 1] <= (uint32_t)t) ++b;
+        const int ctx = __ldg(a.ctx_in + b);
+        seq[u] = b;
+        pos[u] = ctx + (int)((uint32_t)t - s_tok[b]);
+        if (a.slots != nullptr) {
+          const int c = pos[u] >> a.bs_log2, have = (ctx + bs_mask) >> a.bs_log2;
+          const int blk = c < have ? __ldg(a.block_table + (size_t)b * a.max_blocks + c)
+                                   : handed(s_grow[b] + (uint32_t)(c - have));
+          slot[u] = (blk << a.bs_log2) | (pos[u] & bs_mask);
+        }
+      }
+    }
+    if (t4 + 4 <= a.max_tok) {
+      *reinterpret_cast<int4*>(a.tok_seq + t4) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+      *reinterpret_cast<int4*>(a.tok_pos + t4) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      if (a.slots != nullptr)
+        *reinterpret_cast<int4*>(a.slots + t4) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (t4 + u < a.max_tok) {
+          a.tok_seq[t4 + u] = seq[u];
+          a.tok_pos[t4 + u] = pos[u];
+          if (a.slots != nullptr) a.slots[t4 + u] = slot[u];
+        }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t s) {
+  static ContextCache<int> cache;
+  int ready = 0;
+  if (!per_context(cache, &ready, [](int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(plan_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    plan_smem_bytes(kPlanMaxSeq)) == cudaSuccess;
+      }))
+    return cudaErrorInvalidConfiguration;
+  const long long per_cta = 4LL * kPlanThreads;
+  long long ctas = (a.max_tok + per_cta - 1) / per_cta;
+  if (ctas < 1) ctas = 1;
+  if (ctas > sms) ctas = sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = plan_smem_bytes(a.n_seq);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, plan_step_kernel, a);
+}
+
+}  // namespace kvq

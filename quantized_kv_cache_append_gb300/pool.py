@@ -11,7 +11,8 @@ import contextlib
 import torch
 
 from . import (KVQ_F16, KVQ_GROUP, KVQ_K8V4, KVQ_Q4_BLOCK, KVQ_Q8, check, kvq_append,
-               kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes, make_cache)
+               kvq_bound_blocks, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
+               kvq_select_blocks, kvq_sparse_decode_attn, kvq_sparse_workspace_bytes, make_cache)
 
 
 def on_stream(stream):
@@ -37,6 +38,18 @@ def row_layout(fmt: int, head_dim: int):
         return (torch.int8, head_dim, torch.uint8, head_dim // 2, head_dim // KVQ_GROUP,
                 head_dim // KVQ_Q4_BLOCK)
     raise ValueError(f"unknown cache format {fmt}")
+
+
+class BlockBounds:
+    """Bounds of a pool's keys, a block and KV head at a time: int8 codes
+    [n_blocks][n_kv][2][hd] (lo, hi) and fp32 scales [n_blocks][n_kv][hd/64]."""
+
+    def __init__(self, pool: "PagedPool"):
+        dev = pool.k.device
+        self.codes = torch.zeros((pool.n_blocks, pool.n_kv, 2, pool.head_dim), dtype=torch.int8,
+                                 device=dev)
+        self.scales = torch.zeros((pool.n_blocks, pool.n_kv, pool.head_dim // KVQ_GROUP),
+                                  dtype=torch.float32, device=dev)
 
 
 class PagedPool:
@@ -99,3 +112,44 @@ class PagedPool:
             check(kvq_compact_f16(self.cache, block_table_row, n_cells, out_k, out_v, stream),
                   "kvq_compact_f16")
         return out_k, out_v
+
+    def bound(self, bounds: BlockBounds, block_table, ctx_lens, max_new: int, ctx_start=None,
+              stream=None) -> None:
+        """Bounds of the blocks that cells [ctx_start, ctx_lens) touch (None: from 0)."""
+        check(kvq_bound_blocks(self.cache, block_table, int(block_table.shape[0]),
+                               int(block_table.shape[1]), ctx_start, ctx_lens, max_new,
+                               bounds.codes, bounds.scales, stream), "kvq_bound_blocks")
+
+    def select(self, bounds: BlockBounds, q, ctx_lens, max_ctx: int, block_table, n_sel: int,
+               n_first: int = 1, n_last: int = 1, out=None, stream=None):
+        """The blocks each (token, KV head) of q attends to: (pool block ids,
+        their indexes in the sequence) [n_seq][W][n_kv][n_sel] and the lists'
+        cells [n_seq][W][n_kv]."""
+        n_seq, W, n_q, hd = q.shape
+        with on_stream(stream):
+            if out is None:
+                new = lambda *s: torch.empty(s, dtype=torch.int32, device=q.device)
+                out = (new(n_seq, W, self.n_kv, n_sel), new(n_seq, W, self.n_kv, n_sel),
+                       new(n_seq, W, self.n_kv))
+            blocks, index, lens = out
+            check(kvq_select_blocks(self.cache, bounds.codes, bounds.scales, q, n_seq, W, n_q,
+                                    ctx_lens, max_ctx, block_table, int(block_table.shape[1]),
+                                    n_sel, n_first, n_last, blocks, index, lens, stream),
+                  "kvq_select_blocks")
+        return out
+
+    def decode_selected(self, q, sel_blocks, sel_lens, sm_scale: float, out=None, workspace=None,
+                        stream=None):
+        """decode over a list of blocks for each (token, KV head)."""
+        n_seq, W, n_q, hd = q.shape
+        n_sel = int(sel_blocks.shape[-1])
+        with on_stream(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                need = kvq_sparse_workspace_bytes(self.cache, n_seq, W, n_q, n_sel)
+                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+            check(kvq_sparse_decode_attn(self.cache, q, n_seq, W, n_q, sel_blocks, sel_lens, n_sel,
+                                         sm_scale, out, workspace, workspace.numel(), stream),
+                  "kvq_sparse_decode_attn")
+        return out

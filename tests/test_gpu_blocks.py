@@ -1,0 +1,478 @@
+"""GPU: kvq_bound_blocks and kvq_select_blocks bit for bit, and
+kvq_sparse_decode_attn within a derived tolerance, against the plain 64-bit
+forms of tests/plain_blocks.py; and the whole step together."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_kv_cache_append_gb300 as kvq
+from quantized_kv_cache_append_gb300.pool import BlockBounds, PagedPool
+from quantized_kv_cache_append_gb300.steps import StepPlanner
+from tests import plain_blocks as plain
+
+pytestmark = pytest.mark.gpu
+
+FMT = {"f16": kvq.KVQ_F16, "q8": kvq.KVQ_Q8, "k8v4": kvq.KVQ_K8V4}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not torch.cuda.is_available():
+        pytest.fail("the GPU suite needs a CUDA device")
+    kvq.build()
+    kvq.load_library()
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def i32(a):
+    return dev(np.asarray(a, np.int32))
+
+
+def tables(rng, lens, bs, spare=3):
+    nb = [-(-int(L) // bs) for L in lens]
+    perm = rng.permutation(sum(nb) + spare).astype(np.int32)
+    t = np.full((len(lens), max(nb + [1])), -1, np.int32)
+    at = 0
+    for b, n in enumerate(nb):
+        t[b, :n] = perm[at:at + n]
+        at += n
+    return t, sum(nb) + spare
+
+
+def fill_pool(rng, fmt, n_blocks, n_kv, bs, hd):
+    """A pool of random contents, written directly (host arrays returned too)."""
+    p = PagedPool(FMT[fmt], n_kv, hd, bs, n_blocks)
+    shape = (n_blocks, n_kv, bs)
+    gain = np.where(rng.random(hd) < 0.05, 6.0, 1.0)
+    h = {"vs": None, "ks": None}
+    if fmt == "f16":
+        h["k"] = (rng.standard_normal(shape + (hd,)) * gain).astype(np.float16)
+        h["v"] = rng.standard_normal(shape + (hd,)).astype(np.float16)
+    else:
+        h["k"] = rng.integers(-127, 128, shape + (hd,)).astype(np.int8)
+        h["ks"] = (rng.random(shape + (hd // 64,)) * 0.03 + 0.003).astype(np.float16)
+        if fmt == "q8":
+            h["v"] = rng.integers(-127, 128, shape + (hd,)).astype(np.int8)
+            h["vs"] = (rng.random(shape + (hd // 64,)) * 0.03 + 0.003).astype(np.float16)
+        else:
+            h["v"] = rng.integers(0, 256, shape + (hd // 2,)).astype(np.uint8)
+            h["vs"] = ((rng.random(shape + (hd // 32,)) - 0.5) * 4).astype(np.float16)
+    for name in ("k", "v", "ks", "vs"):
+        if h[name] is not None:
+            getattr(p, name).copy_(dev(h[name]))
+    return p, h
+
+
+# ---------------------------------------------------------------- bounds
+def plain_bounds(fmt, h, bounds, scales, table, start, lens, bs):
+    with np.errstate(invalid="ignore", over="ignore"):
+        K = h["k"].astype(np.float64)
+        if fmt != "f16":
+            K = K * np.repeat(h["ks"].astype(np.float64), 64, -1)
+    codes, sc = bounds.copy(), scales.copy()
+    for b in range(len(lens)):
+        L = min(int(lens[b]), table.shape[1] * bs)
+        if int(start[b]) >= L:
+            continue
+        for j in range(max(int(start[b]), 0) // bs, -(-L // bs)):
+            blk = table[b, j]
+            if 0 <= blk < len(codes):
+                for n in range(K.shape[1]):
+                    codes[blk, n], sc[blk, n] = plain.bounds_of(K[blk, n, :min(bs, L - j * bs)])
+    return codes, sc
+
+
+def check_bounds(rng, fmt, p, h, table, start, lens, use_start=True, max_new=None):
+    n_blocks, n_kv, bs, hd = p.n_blocks, p.n_kv, p.block_size, p.head_dim
+    bb = BlockBounds(p)
+    old = rng.integers(-128, 128, bb.codes.shape).astype(np.int8)
+    old_s = rng.random(bb.scales.shape).astype(np.float32)
+    bb.codes.copy_(dev(old))
+    bb.scales.copy_(dev(old_s))
+    start, lens = np.asarray(start), np.asarray(lens)
+    if max_new is None:
+        max_new = int(max((lens - (start if use_start else 0)).max(), 0))
+    p.bound(bb, i32(table), i32(lens), max_new, i32(start) if use_start else None)
+    torch.cuda.synchronize()
+    want = plain_bounds(fmt, h, old, old_s, table, start if use_start else np.zeros_like(lens), lens, bs)
+    assert np.array_equal(bb.codes.cpu().numpy(), want[0])
+    assert np.array_equal(bb.scales.cpu().numpy(), want[1])
+    return want
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8", "k8v4"])
+@pytest.mark.parametrize("n_kv,hd,bs", [(2, 64, 16), (1, 64, 1024), (3, 128, 16), (2, 128, 64), (1, 128, 256),
+                                        (1, 256, 16), (2, 256, 32), (1, 256, 128)])
+def test_bounds_of_ragged_sequences(fmt, n_kv, hd, bs):
+    rng = np.random.default_rng(hd + bs)
+    lens = np.array([1, bs - 1, bs, bs + 1, 0, 3 * bs + 5])
+    table, n_blocks = tables(rng, lens, bs)
+    p, h = fill_pool(rng, fmt, n_blocks, n_kv, bs, hd)
+    check_bounds(rng, fmt, p, h, table, np.zeros(6, int), lens, use_start=False)
+    # the newest cells alone: mid-block, on a border, none, several blocks
+    check_bounds(rng, fmt, p, h, table, [0, bs - 2, bs - 1, bs, 0, bs - 1], lens)
+    check_bounds(rng, fmt, p, h, table, [1, bs - 1, bs, bs + 1, 0, 3 * bs + 5], lens, max_new=4)   # nothing new
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8"])
+def test_bounds_of_special_values(fmt):
+    rng = np.random.default_rng(2)
+    n_kv, hd, bs = 1, 128, 16
+    table, n_blocks = tables(rng, [16 * 7], bs, spare=0)
+    p, h = fill_pool(rng, fmt, n_blocks, n_kv, bs, hd)
+    blk = table[0]
+    if fmt == "f16":
+        k = h["k"]
+        k[blk[0]] = 0
+        k[blk[1], 0, 3, :40] = np.nan                 # passed over
+        k[blk[2], 0, :, 5] = np.nan                   # nothing left: 0
+        k[blk[3], 0, 2, 7], k[blk[3], 0, 4, 70] = np.inf, -np.inf
+        k[blk[4]] = np.float16(2.0 ** -24)            # the smallest subnormal
+        k[blk[5]] = np.float16(-65504)
+        k[blk[6], 0, :, :64] = np.float16(127 / 128)  # on the border of two scales
+        k[blk[6], 0, :, 64:] = np.nextafter(np.float16(127 / 128), np.float16(2))
+        k[blk[6], 0, 0, 3] = -0.0
+    else:
+        s = h["ks"]
+        s[blk[0]] = 0
+        s[blk[1]] = 65504                             # dequantised up to 8.3 million
+        s[blk[2]] = np.float16(2.0 ** -24)
+        h["k"][blk[3]] = 0
+        s[blk[4]] = np.float16(2.0 ** -7)             # 127 * 2^-7: on the border
+        h["k"][blk[4], 0, 0, :] = 127
+        h["k"][blk[5]] = -127
+    for name in ("k", "ks"):
+        if h[name] is not None:
+            getattr(p, name).copy_(dev(h[name]))
+    check_bounds(rng, fmt, p, h, table, [0], [16 * 7], use_start=False)
+
+
+def test_bounds_skip_foreign_ids_and_clamp_lengths():
+    rng = np.random.default_rng(4)
+    bs = 16
+    table, n_blocks = tables(rng, [64, 64], bs)
+    p, h = fill_pool(rng, "f16", n_blocks, 2, bs, 64)
+    table[0, 1], table[0, 3], table[1, 2] = -1, n_blocks, 1 << 30
+    check_bounds(rng, "f16", p, h, table, [0, 0], [64, 64])
+    check_bounds(rng, "f16", p, h, table, [-5, 60], [1000, 64], max_new=64)       # past the row: clamped
+
+
+# ---------------------------------------------------------------- selection
+def random_bounds(rng, n_blocks, n_kv, hd):
+    hi = np.clip(np.rint(rng.normal(60, 30, (n_blocks, n_kv, 2, hd))), -127, 127).astype(np.int8)
+    hi[:, :, 0] = np.minimum(hi[:, :, 1], np.clip(np.rint(rng.normal(-60, 30, hi[:, :, 0].shape)), -127, 127))
+    scales = (2.0 ** rng.integers(-9, -3, (n_blocks, n_kv, hd // 64))).astype(np.float32)
+    return hi, scales
+
+
+def check_select(codes, scales, q, ctx, table, bs, n_blocks, n_sel, n_first, n_last, max_ctx=None, index=True):
+    n_seq, W, n_q, hd = q.shape
+    n_kv = codes.shape[1]
+    p = PagedPool(kvq.KVQ_F16, n_kv, hd, bs, n_blocks)
+    mk = lambda *s: torch.full(s, 77777, dtype=torch.int32, device="cuda")
+    blocks, idx, lens = mk(n_seq, W, n_kv, n_sel), mk(n_seq, W, n_kv, n_sel), mk(n_seq, W, n_kv)
+    st = kvq.kvq_select_blocks(p.cache, dev(codes), dev(scales), dev(q), n_seq, W, n_q, i32(ctx),
+                               int(max(ctx)) if max_ctx is None else max_ctx, i32(table), table.shape[1],
+                               n_sel, n_first, n_last, blocks, idx if index else None, lens)
+    assert st == kvq.KVQ_OK, kvq.kvq_status_string(st)
+    torch.cuda.synchronize()
+    want = plain.select(codes, scales, q, ctx, table, bs, n_blocks, n_sel, n_first, n_last)
+    assert np.array_equal(lens.cpu().numpy(), want[2])
+    assert np.array_equal(blocks.cpu().numpy(), want[0])
+    if index:
+        assert np.array_equal(idx.cpu().numpy(), want[1])
+    return want
+
+
+def queries(rng, *shape):
+    return rng.standard_normal(shape).astype(np.float32)
+
+
+@pytest.mark.parametrize("n_seq,W,n_kv,G,hd,bs,hi,n_sel,first,last", [
+    (1, 1, 1, 1, 64, 16, 16, 1, 0, 0), (1, 1, 8, 4, 128, 64, 32768, 64, 1, 2),
+    (3, 1, 2, 2, 64, 16, 5000, 31, 1, 1), (2, 3, 3, 3, 128, 32, 4001, 17, 0, 3),
+    (1, 4, 2, 8, 256, 16, 20011, 100, 2, 4), (2, 1, 1, 32, 256, 16, 3001, 9, 0, 0),
+    (2, 17, 1, 5, 64, 16, 1500, 11, 1, 1), (1, 2, 1, 16, 128, 1024, 70000, 8, 1, 1),
+    (40, 1, 8, 4, 128, 16, 900, 12, 1, 2), (2, 9, 2, 7, 128, 16, 1200, 30, 1, 2),
+    (1, 1, 2, 1, 256, 16, 131072, 700, 0, 1),
+])
+def test_selection(n_seq, W, n_kv, G, hd, bs, hi, n_sel, first, last):
+    rng = np.random.default_rng(hi + W)
+    lens = rng.integers(max(1, hi // 3), hi + 1, n_seq)
+    lens[0] = hi
+    table, n_blocks = tables(rng, lens, bs)
+    codes, scales = random_bounds(rng, n_blocks, n_kv, hd)
+    check_select(codes, scales, queries(rng, n_seq, W, n_kv * G, hd), lens, table, bs, n_blocks, n_sel, first, last)
+
+
+def test_selection_over_the_longest_row():
+    rng = np.random.default_rng(8)
+    bs, n = 16, 32768
+    table, n_blocks = tables(rng, [n * bs], bs)
+    codes, scales = random_bounds(rng, n_blocks, 1, 64)
+    q = queries(rng, 1, 2, 3, 64)
+    check_select(codes, scales, q, [n * bs], table, bs, n_blocks, 2000, 1, 4)
+    check_select(codes, scales, q, [n * bs], table, bs, n_blocks, n + 5, 1, 4)      # every block
+
+
+def test_equal_scores_go_to_the_lower_block():
+    rng = np.random.default_rng(5)
+    bs, n = 16, 1000
+    table, n_blocks = tables(rng, [n * bs - 3], bs)
+    codes, scales = random_bounds(rng, n_blocks, 2, 128)
+    q = queries(rng, 1, 1, 4, 128)
+    codes[:], scales[:] = codes[:1], scales[:1]
+    for n_sel, first, last in ((1, 0, 0), (7, 0, 0), (64, 1, 2), (999, 0, 1), (1000, 0, 0)):
+        check_select(codes, scales, q, [n * bs - 3], table, bs, n_blocks, n_sel, first, last)
+    pick = rng.integers(0, 5, n_blocks)          # five values, the threshold inside a long tie
+    base, bsc = random_bounds(rng, 5, 2, 128)
+    codes, scales = base[pick], bsc[pick]
+    for n_sel in (2, 100, 333, 500, 801):
+        check_select(codes, scales, q, [n * bs - 3], table, bs, n_blocks, n_sel, 1, 1)
+    check_select(codes, scales, np.zeros_like(q), [n * bs - 3], table, bs, n_blocks, 100, 0, 0)   # all scores 0
+
+
+def test_selection_of_short_contexts_and_windows():
+    rng = np.random.default_rng(6)
+    bs, n_kv, W = 16, 2, 5
+    lens = np.array([0, 1, 3, 4, 5, 6, 16, 17, 20, 21, 100])       # some tokens see nothing
+    table, n_blocks = tables(rng, lens, bs)
+    codes, scales = random_bounds(rng, n_blocks, n_kv, 64)
+    q = queries(rng, len(lens), W, n_kv * 2, 64)
+    for n_sel, first, last in ((1, 0, 0), (2, 1, 1), (4, 0, 3), (9, 2, 2)):
+        want = check_select(codes, scales, q, lens, table, bs, n_blocks, n_sel, first, last)
+        assert (want[2][0] == 0).all() and (want[0][0] == -1).all()
+    check_select(codes, scales, q, lens, table, bs, n_blocks, 3, 1, 1, index=False)
+    check_select(codes, scales, q, lens, table, bs, n_blocks, 3, 1, 1, max_ctx=table.shape[1] * bs)
+
+
+def test_selection_never_takes_a_foreign_block():
+    rng = np.random.default_rng(7)
+    bs, n = 16, 300
+    table, n_blocks = tables(rng, [n * bs - 1, n * bs], bs)
+    holes = rng.random(table.shape) < 0.4
+    table[holes] = rng.choice([-1, n_blocks, 1 << 30, -(1 << 31)], holes.sum())
+    table[0, 0] = table[0, n - 1] = -1           # the forced ones too
+    table[1, 5:] = -1                            # hardly any left
+    codes, scales = random_bounds(rng, n_blocks, 1, 128)
+    q = queries(rng, 2, 1, 4, 128)
+    for n_sel in (4, 60, 250):
+        check_select(codes, scales, q, [n * bs - 1, n * bs], table, bs, n_blocks, n_sel, 2, 2)
+
+
+def test_selection_with_special_queries():
+    rng = np.random.default_rng(10)
+    bs, n = 16, 200
+    table, n_blocks = tables(rng, [n * bs], bs)
+    codes, scales = random_bounds(rng, n_blocks, 1, 128)
+    q = queries(rng, 1, 6, 2, 128)
+    q[0, 0, 0, 5] = np.nan
+    q[0, 1, 1, :] = np.nan
+    q[0, 2, 0, 9], q[0, 2, 0, 90] = np.inf, -np.inf      # saturated codes at 2^60
+    q[0, 3] *= 1e-30                                     # codes 0: all scores 0
+    q[0, 4, 0, :64] = 127 / 128                          # on the border of two scales
+    q[0, 4, 0, 64:] = np.nextafter(np.float32(127 / 128), np.float32(2))
+    q[0, 5] *= 1e30                                      # past 127 * 2^60: saturated
+    check_select(codes, scales, q, [n * bs], table, bs, n_blocks, 20, 0, 0)
+
+
+# ---------------------------------------------------------------- attention
+def check_attention(rng, fmt, p, h, q, blocks, lens, scale=None):
+    sm = 1 / math.sqrt(p.head_dim) if scale is None else scale
+    out = torch.full(q.shape, float("nan"), device="cuda")
+    p.decode_selected(dev(q), i32(blocks), i32(lens), sm, out=out)
+    torch.cuda.synchronize()
+    K, V = plain.pool_rows(fmt, h["k"], h["v"], h["ks"], h["vs"])
+    want, tol = plain.attention(fmt, K, V, q, blocks, lens, p.block_size, np.float64(np.float32(sm)))
+    err = np.abs(out.cpu().numpy() - want).max(-1)
+    assert np.isfinite(err).all()
+    assert (err <= tol).all(), (err - tol).max()
+    assert (out.cpu().numpy()[lens_rows(lens, q) <= 0] == 0).all()
+    return out
+
+
+def lens_rows(lens, q):
+    """sel_lens per query row: [n_seq][W][n_q]."""
+    return np.repeat(lens, q.shape[2] // lens.shape[2], 2)
+
+
+def random_lists(rng, n_seq, W, n_kv, n_sel, n_blocks, bs):
+    blocks = np.stack([rng.permutation(max(n_blocks, n_sel))[:n_sel] % n_blocks
+                       for _ in range(n_seq * W * n_kv)]).reshape(n_seq, W, n_kv, n_sel)
+    lens = rng.integers(0, n_sel * bs + 1, (n_seq, W, n_kv))
+    lens.flat[0] = n_sel * bs
+    return blocks, lens
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8", "k8v4"])
+@pytest.mark.parametrize("n_seq,W,n_kv,G,hd,bs,n_sel", [
+    (1, 1, 1, 1, 64, 16, 1), (1, 1, 1, 4, 128, 64, 70), (1, 1, 8, 4, 128, 64, 9), (3, 1, 2, 3, 64, 16, 13),
+    (2, 5, 3, 5, 128, 32, 7), (1, 17, 2, 2, 256, 16, 21), (2, 1, 2, 16, 128, 128, 4), (1, 2, 1, 32, 64, 256, 3),
+    (1, 1, 2, 32, 256, 16, 40), (9, 2, 4, 8, 256, 16, 5), (1, 3, 1, 7, 128, 1024, 2),
+])
+def test_attention_over_lists(fmt, n_seq, W, n_kv, G, hd, bs, n_sel):
+    rng = np.random.default_rng(hd + bs + W)
+    n_blocks = n_sel + 5
+    p, h = fill_pool(rng, fmt, n_blocks, n_kv, bs, hd)
+    blocks, lens = random_lists(rng, n_seq, W, n_kv, n_sel, n_blocks, bs)
+    check_attention(rng, fmt, p, h, queries(rng, n_seq, W, n_kv * G, hd), blocks, lens)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8", "k8v4"])
+def test_attention_lengths_holes_and_repeats(fmt):
+    rng = np.random.default_rng(3)
+    bs, n_sel, n_kv, hd = 16, 6, 2, 128
+    p, h = fill_pool(rng, fmt, 8, n_kv, bs, hd)
+    q = queries(rng, 4, 3, n_kv * 4, hd)
+    blocks, lens = random_lists(rng, 4, 3, n_kv, n_sel, 8, bs)
+    lens[0] = 0                                      # rows without a cell
+    lens[1] = -4
+    lens[2] = [[1, 2], [15, 16], [17, 1000]]         # one cell; past the list: clamped
+    blocks[3, 0, :, 2] = [-1, 8]                     # a hole inside
+    blocks[3, 1] = -1                                # nothing but holes
+    blocks[3, 2, :, 1:] = 3                          # the same block again and again
+    lens[3] = n_sel * bs
+    out = check_attention(rng, fmt, p, h, q, blocks, lens)
+    assert (out[3, 1] == 0).all()
+
+
+def test_attention_ignores_what_lies_behind_a_list():
+    # cells past sel_len inside the last block hold NaN and infinities
+    rng = np.random.default_rng(12)
+    bs, hd = 16, 64
+    for fmt in ("f16", "q8", "k8v4"):
+        p, h = fill_pool(rng, fmt, 4, 1, bs, hd)
+        blocks = np.array([0, 2, 3], np.int32).reshape(1, 1, 1, 3)
+        lens = np.full((1, 1, 1), 37)
+        q = queries(rng, 1, 1, 4, hd)
+        want = check_attention(rng, fmt, p, h, q, blocks, lens)
+        bad = float("nan")
+        if fmt == "f16":
+            p.k[3, 0, 5:], p.v[3, 0, 5:] = float("inf"), bad
+            p.k[1], p.v[1] = bad, bad
+        else:
+            p.ks[3, 0, 5:], p.vs[3, 0, 5:] = bad, float("-inf")
+            p.ks[1], p.vs[1] = bad, bad
+        out = p.decode_selected(dev(q), i32(blocks), i32(lens), 1 / math.sqrt(hd))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_attention_over_every_block_is_the_dense_decode():
+    rng = np.random.default_rng(13)
+    bs, n_kv, G, hd, L, W = 32, 2, 4, 128, 3001, 2
+    table, n_blocks = tables(rng, [L], bs)
+    for fmt in ("f16", "q8", "k8v4"):
+        p, h = fill_pool(rng, fmt, n_blocks, n_kv, bs, hd)
+        q = dev(queries(rng, 1, W, n_kv * G, hd))
+        bb = BlockBounds(p)
+        p.bound(bb, i32(table), i32([L]), L)
+        blocks, index, lens = p.select(bb, q, i32([L]), L, i32(table), table.shape[1])
+        assert lens[0, :, 0].tolist() == [L - 1, L]
+        assert torch.equal(blocks[0, 1, 1], i32(table)[0])
+        a = p.decode_selected(q, blocks, lens, 0.088)
+        b = p.decode(q, i32([L]), L, i32(table), 0.088)
+        torch.cuda.synchronize()
+        rel = ((a - b).norm() / b.norm()).item()
+        assert rel < 4e-5      # two sums within the bounds of the attention tests
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("fmt", ["f16", "q8", "k8v4"])
+def test_a_serving_loop(fmt):
+    """Requests arrive, decode over chosen blocks and leave: plan, append,
+    bound, select and attend each step from device arrays alone, checked
+    against the plain forms on the pool's own contents."""
+    rng = np.random.default_rng(21)
+    n, bs, n_blocks, max_tok, n_kv, G, hd = 5, 16, 120, 160, 2, 4, 128
+    width, n_sel = 30, 6
+    planner = StepPlanner(n, width, bs, n_blocks, max_tok)
+    p = PagedPool(FMT[fmt], n_kv, hd, bs, n_blocks)
+    bb = BlockBounds(p)
+    for step in range(8):
+        new = np.array([[90, 0, 17, 33, 0], [1, 1, 1, 1, 0], [1, 50, 1, 1, 1], [1, 1, -1, 1, 1],
+                        [1, 1, 40, 1, -1], [-1, 1, 1, 1, 0], [100, 1, 1, 1, 0], [1, 1, 1, 1, 0]][step])
+        planner.plan(i32(new))
+        k = rng.standard_normal((max_tok, n_kv, hd)).astype(np.float32)
+        v = rng.standard_normal((max_tok, n_kv, hd)).astype(np.float32)
+        p.append(dev(k), dev(v), planner.tok_seq, planner.tok_pos, planner.block_table)
+        p.bound(bb, planner.block_table, planner.ctx_lens, 100, planner.ctx_start)
+        q = queries(rng, n, 1, n_kv * G, hd)
+        blocks, index, lens = p.select(bb, dev(q), planner.ctx_lens, width * bs, planner.block_table, n_sel, 1, 2)
+        out = p.decode_selected(dev(q), blocks, lens, 1 / math.sqrt(hd))
+        torch.cuda.synchronize()
+        assert planner.info[3] == 0
+        ctx, table = planner.ctx_lens.cpu().numpy(), planner.block_table.cpu().numpy()
+        h = {m: None if getattr(p, m) is None else getattr(p, m).cpu().numpy() for m in ("k", "v", "ks", "vs")}
+        codes, scales = plain_bounds(fmt, h, bb.codes.cpu().numpy(), bb.scales.cpu().numpy(), table,
+                                     np.zeros(n, int), ctx, bs)
+        assert np.array_equal(codes, bb.codes.cpu().numpy()) and np.array_equal(scales, bb.scales.cpu().numpy())
+        want = plain.select(codes, scales, q, ctx, table, bs, n_blocks, n_sel, 1, 2)
+        for a, b in zip((blocks, index, lens), want):
+            assert np.array_equal(a.cpu().numpy(), b)
+        K, V = plain.pool_rows(fmt, h["k"], h["v"], h["ks"], h["vs"])
+        ref, tol = plain.attention(fmt, K, V, q, want[0], want[2], bs, np.float64(np.float32(1 / math.sqrt(hd))))
+        assert (np.abs(out.cpu().numpy() - ref).max(-1) <= tol).all()
+
+
+def test_a_step_on_a_side_stream_and_replayed_from_a_graph():
+    rng = np.random.default_rng(22)
+    n, bs, n_blocks, n_kv, G, hd, width, n_sel = 3, 16, 64, 2, 4, 64, 16, 4
+    sm = 1 / math.sqrt(hd)
+    s = torch.cuda.Stream()
+    planner = StepPlanner(n, width, bs, n_blocks, 64)
+    p = PagedPool(kvq.KVQ_Q8, n_kv, hd, bs, n_blocks)
+    bb = BlockBounds(p)
+    k, v = (torch.empty(64, n_kv, hd, device="cuda") for _ in range(2))
+    q = torch.empty(n, 1, n_kv * G, hd, device="cuda")
+    n_new = torch.empty(n, dtype=torch.int32, device="cuda")
+    sel = tuple(torch.empty(x, dtype=torch.int32, device="cuda")
+                for x in ((n, 1, n_kv, n_sel), (n, 1, n_kv, n_sel), (n, 1, n_kv)))
+    out = torch.empty_like(q)
+    ws = torch.empty(kvq.kvq_sparse_workspace_bytes(p.cache, n, 1, n_kv * G, n_sel), dtype=torch.uint8,
+                     device="cuda")
+
+    def step(stream=None):
+        planner.plan(n_new, stream)
+        p.append(k, v, planner.tok_seq, planner.tok_pos, planner.block_table, stream)
+        p.bound(bb, planner.block_table, planner.ctx_lens, 20, planner.ctx_start, stream)
+        p.select(bb, q, planner.ctx_lens, width * bs, planner.block_table, n_sel, out=sel, stream=stream)
+        p.decode_selected(q, sel[0], sel[2], sm, out=out, workspace=ws, stream=stream)
+
+    def feed(new):
+        n_new.copy_(i32(new))
+        for t in (k, v, q):
+            t.copy_(dev(rng.standard_normal(tuple(t.shape)).astype(np.float32)))
+
+    def verify():
+        torch.cuda.synchronize()
+        h = {m: getattr(p, m).cpu().numpy() for m in ("k", "v", "ks", "vs")}
+        table, ctx = planner.block_table.cpu().numpy(), planner.ctx_lens.cpu().numpy()
+        want = plain.select(bb.codes.cpu().numpy(), bb.scales.cpu().numpy(), q.cpu().numpy(), ctx, table, bs,
+                            n_blocks, n_sel, 1, 1)
+        for a, b in zip(sel, want):
+            assert np.array_equal(a.cpu().numpy(), b)
+        K, V = plain.pool_rows("q8", h["k"], h["v"], h["ks"], h["vs"])
+        ref, tol = plain.attention("q8", K, V, q.cpu().numpy(), want[0], want[2], bs, np.float64(np.float32(sm)))
+        assert (np.abs(out.cpu().numpy() - ref).max(-1) <= tol).all()
+
+    feed([20, 7, 0])
+    torch.cuda.synchronize()
+    step(s)
+    s.synchronize()
+    verify()
+    feed([1, 1, 18])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        step()
+    for new in ([1, 1, 18], [1, 20, 1], [-1, 1, 1], [15, 1, 1]):
+        feed(new)
+        g.replay()
+        verify()
+    assert planner.ctx_lens.tolist() == [15, 30, 21]
