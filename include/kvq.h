@@ -523,9 +523,9 @@ kvq_status kvq_plan_step(const int32_t *ctx_in, const int32_t *n_new, int n_seq,
  *
  * Per 64 dims the scale is 2^e, e in [-24, 16] the smallest with 127 * 2^e
  * >= max(|lo|, |hi|); the codes are floor(lo / 2^e) and ceil(hi / 2^e).  The
- * result is bit-identical to that definition for finite keys; NaN keys are
- * passed over (a dim with nothing else gets 0), infinite ones give codes of
- * +-127 at e = 16.  Bounds belong to the physical block: blocks shared by
+ * result is bit-identical to that definition for finite keys; NaN keys and
+ * int8 keys whose scale is not finite are passed over (a dim with nothing
+ * else gets 0), infinite FP16 keys give codes of +-127 at e = 16.  Bounds belong to the physical block: blocks shared by
  * several rows need one call, and a block that is refilled needs a new one.
  * Sequences with ctx_start >= ctx_lens and blocks with an id out of range
  * are skipped.  max_new == 0 is a no-op.

@@ -479,8 +479,11 @@ KVQ_API kvq_status kvq_bound_blocks(const kvq_cache* cache, const int32_t* block
   if (touched > max_blocks_per_seq) touched = max_blocks_per_seq;
   a.touched = (int)touched;
   if ((long long)n_seq * touched * cache->n_kv_heads >= (1LL << 31)) return KVQ_ERR_UNSUPPORTED;
-  const cudaError_t e =
-      launch_bound_blocks(cache->fmt, cache->head_dim, a, static_cast<cudaStream_t>(stream));
+  a.div_nkv = make_fastdiv((unsigned)cache->n_kv_heads);
+  a.div_touched = make_fastdiv((unsigned)a.touched);
+  const int sms = sm_count();
+  const cudaError_t e = launch_bound_blocks(cache->fmt, cache->head_dim, a, sms > 0 ? sms : 148,
+                                            static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 

@@ -233,6 +233,7 @@ struct BoundArgs {
   float* scales;               // [n_blocks][n_kv][hd / 64]
   int n_seq, max_blocks;
   int touched;                 // blocks per sequence the launch covers
+  FastDiv div_nkv, div_touched;
 };
 
 // Block selection (kvq_select.cu).
@@ -249,7 +250,9 @@ struct SelectArgs {
   int n_cap;                   // blocks of the longest context: ceil(max_ctx / block size)
   int n_sel, n_first, n_last;
   int wg_tok, n_wg;            // tokens per cluster, clusters per (sequence, KV head)
-  int cluster, lead_rows;      // CTAs per cluster, tokens each of them leads
+  int cluster, c_log2, lead_rows;  // CTAs per cluster (a power of two), tokens each of them leads
+  int wide;                    // 512 threads a CTA instead of 256
+  int gp_log2;                 // query rows of a token, padded to a power of two
 };
 constexpr int kSelMaxBlocks = 32768;       // keys of one token: 128 KB of shared memory
 constexpr int kSelMaxSmem = 200 * 1024;
@@ -258,7 +261,7 @@ constexpr int kSelMaxSmem = 200 * 1024;
 // status from the runtime.
 cudaError_t launch_append(int fmt, int hd, const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_bound_blocks(int fmt, int hd, const BoundArgs& a, cudaStream_t s);
+cudaError_t launch_bound_blocks(int fmt, int hd, const BoundArgs& a, int sms, cudaStream_t s);
 // Fills in the launch shape (wg_tok, n_wg, cluster, lead_rows); false if the
 // keys of one token do not fit the shared memory.
 bool plan_select(int hd, int sms, SelectArgs* a);

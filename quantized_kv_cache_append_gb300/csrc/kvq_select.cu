@@ -11,27 +11,36 @@
 // their maximum.  No sum depends on its order, so the chosen blocks do not
 // depend on how the work is split; ties go to the lower block.
 //
-// One cluster of CTAs per (sequence, KV head, up to kMaxTok tokens).  The
-// CTAs share the visible blocks: each lane holds 16 dims of a block (one
-// 16-byte load of lo and of hi), the q codes of 4 query heads in registers,
-// and sums by dp4a (4 products an instruction); the lanes of a group meet by
-// shuffles.  Each key (the score as an order-preserving integer) goes
-// straight to the shared memory of the CTA that leads its token's selection
-// (distributed shared memory).  After one cluster barrier the leaders find
-// the n_sel-th largest key by radix counting from the first bit in which the
-// keys differ, and write the list in ascending order.
+// One cluster of CTAs per (sequence, KV head, up to 32 query rows); its CTAs
+// share the visible blocks, a warp scores 16 at a time:
+//
+//   scores     mma.sync.m16n8k16, 16 blocks x 8 query rows, the codes as fp16
+//              (exact: whole numbers below 128, sums below 2^21 in fp32).
+//              The dims of a k-step are free to choose, so a lane's 16-byte
+//              loads of 16 consecutive dims are its A fragments of 4
+//              k-steps: no shared memory, no shuffles.  lo against min(c, 0)
+//              and hi against max(c, 0) add up in one accumulator per 64
+//              dims.  (dp4a, which the codes suggest, runs at 8 lanes a
+//              cycle and SM on this chip: 64 sequences took 121 us in it.)
+//   keys       the score as an order-preserving integer goes straight to the
+//              shared memory of the CTA that leads its token's selection
+//              (distributed shared memory)
+//   selection  after one cluster barrier each leader counts its keys (held in
+//              registers) in bins of equal score width, compares those of
+//              the bin that holds the n_sel-th largest, and writes the list
+//              in ascending order; up to 1024 keys one warp does it alone
+//
+// A token's query rows are padded to a power of two (or a multiple of 8) by
+// repeating its last row, which leaves the maximum as it is.
 #include <math.h>
 #include <stdint.h>
 
 #include "kvq_internal.cuh"
+#include "kvq_ptx.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kDigitBits = 10;
-constexpr int kBins = 1 << kDigitBits;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kForced = 0xffffffffu;   // keys: 0 not a candidate, kForced always kept
 
@@ -44,11 +53,16 @@ __device__ __forceinline__ int q_exponent(float m) {
 
 __device__ __forceinline__ float pow2f_exact(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// fp32 (no NaN) -> uint32 in the same order; finite scores map inside
-// (0x007fffff, 0xff800000), clear of 0 and kForced.  -0 counts as +0.
+// A score -> uint32 in the same order, clear of 0 and kForced; -0 counts as
+// +0.  Scores of kvq_bound_blocks's scales stay below 2^100; what other
+// scales may give is held to +-1e38 (NaN: the lowest), so differences of
+// scores are finite below.
 __device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t b = __float_as_uint(fminf(fmaxf(x, -1e38f), 1e38f) + 0.0f);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -66,16 +80,35 @@ __device__ __forceinline__ void store_remote(uint32_t addr, uint32_t rank, uint3
       : "memory");
 }
 
-// Layout of the dynamic shared memory.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 4 int8 codes of one word -> two fp16 pairs, exactly: 0x6400 | (c ^ 0x80) is
+// 1152 + c.
+__device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  w ^= 0x80808080u;
+  lo = hsub2(prmt(w, 0x64646464u, 0x4140u), 0x64806480u);
+  hi = hsub2(prmt(w, 0x64646464u, 0x4342u), 0x64806480u);
+}
+
+// Layout of the dynamic shared memory: the q codes as B fragments
+// [n-tile][64-dim group][k-step 0..3][lo, hi][lane][2 words], the q scales
+// [row][group] fp32, the keys [lead row][n_cap].
+// keys of one token, padded to whole 16-byte reads
+__host__ __device__ inline int key_row(int n_cap) { return (n_cap + 3) / 4 * 4; }
 struct SelSmem {
-  int codes, scales, keys, bytes;
+  int scales, keys, bytes;
 };
-__host__ __device__ inline SelSmem sel_smem(int hd, int rows, int lead_rows, int n_cap) {
+__host__ __device__ inline SelSmem sel_smem(int hd, int nt, int lead_rows, int n_cap) {
+  const int ng = hd / kGroup;
   SelSmem m;
-  m.codes = 0;                                   // [rows][2][hd] int8: min(c, 0), max(c, 0)
-  m.scales = rows * 2 * hd;                      // [rows][hd / 64] fp32
-  m.keys = (m.scales + rows * (hd / kGroup) * 4 + 15) / 16 * 16;   // [lead_rows][n_cap] uint32
-  m.bytes = m.keys + lead_rows * n_cap * 4;
+  m.scales = nt * ng * 8 * 256;
+  m.keys = m.scales + nt * 8 * ng * 4;
+  m.bytes = m.keys + lead_rows * key_row(n_cap) * 4;
   return m;
 }
 
@@ -88,108 +121,332 @@ struct Threshold {
   int count;      // how many are taken
 };
 
-__device__ Threshold find_threshold(const uint32_t* keys, int n, int k, uint32_t* s_hist, uint32_t* s_aux) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // counts of candidates and forced ones, range of the others
-  uint32_t cand = 0, forced = 0, kmin = 0xffffffffu, kmax = 0;
-  for (int i = tid; i < n; i += kSelThreads) {
-    const uint32_t x = keys[i];
-    cand += x != 0;
-    forced += x == kForced;
-    if (x != 0 && x != kForced) {
-      kmin = min(kmin, x);
-      kmax = max(kmax, x);
-    }
-  }
-  cand = __reduce_add_sync(kAll, cand);
-  forced = __reduce_add_sync(kAll, forced);
-  kmin = __reduce_min_sync(kAll, kmin);
-  kmax = __reduce_max_sync(kAll, kmax);
-  if (lane == 0) {
-    s_aux[warp] = cand;
-    s_aux[kSelWarps + warp] = forced;
-    s_aux[2 * kSelWarps + warp] = kmin;
-    s_aux[3 * kSelWarps + warp] = kmax;
-  }
-  for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-  __syncthreads();
-  cand = forced = 0;
-#pragma unroll
-  for (int w = 0; w < kSelWarps; ++w) {
-    cand += s_aux[w];
-    forced += s_aux[kSelWarps + w];
-    kmin = min(kmin, s_aux[2 * kSelWarps + w]);
-    kmax = max(kmax, s_aux[3 * kSelWarps + w]);
-  }
-  if ((int)cand <= k) return {0u, 0u, (int)cand};                   // all of them
-  if ((int)forced >= k) return {kForced, (uint32_t)k, k};           // (forced <= k by the call's checks)
-  uint32_t rem = (uint32_t)k - forced;                              // 1 <= rem < others
-  int bits = kmin == kmax ? 0 : 32 - __clz(kmin ^ kmax);            // the keys differ below this bit
-  uint32_t base = bits >= 32 ? 0u : kmin & ~((1u << bits) - 1u);
-  while (bits > 0) {
-    const int d = min(bits, kDigitBits), shift = bits - d;
-    const uint32_t mask = (1u << d) - 1u;
-    // keys that share the bits above this digit (>> 1 first: bits may be 32)
-    const uint32_t top = (base >> 1) >> (bits - 1);
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t x = keys[i];
-      if (x != 0 && x != kForced && ((x >> 1) >> (bits - 1)) == top) atomicAdd(&s_hist[(x >> shift) & mask], 1u);
-    }
+// Scratch of a selection: bins and ranked keys while the threshold is sought,
+// then the list's entries (16 bits each: indexes stay below 32768).
+constexpr int kBins = 512, kBinBits = 9, kBinsPL = kBins / 32;   // (kBinsPL: bins a lane sums)
+constexpr int kRanks = 3584;
+constexpr int kListMax = 2 * (kBins + kRanks);
+struct alignas(16) SelScratch {
+  union {
+    struct {
+      uint32_t hist[kBins];
+      uint32_t rank[kRanks];
+    };
+    uint16_t list[kListMax];
+  };
+  uint32_t sums[2][3][16];    // what the warps tell one another, two rounds in turn
+  uint4 found;                // bin, what is left to take in it, its keys
+  uint32_t n_rank;
+  int last;                   // the last visible block is in the list
+};
+
+// Sums over the CTA, one barrier each.
+template <int THREADS>
+struct Team {
+  static constexpr int warps = THREADS / 32;
+  SelScratch& sc;
+  int round = 0;
+
+  __device__ __forceinline__ uint32_t sum(uint32_t v) {
+    v = __reduce_add_sync(kAll, v);
+    uint32_t* s = sc.sums[round][0];
+    round ^= 1;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
-    // thread t: bins kBins - 1 - 4t .. kBins - 4 - 4t (from the top down)
-    constexpr int BPT = kBins / kSelThreads;
-    uint32_t c[BPT], sum = 0;
+    v = 0;
 #pragma unroll
-    for (int j = 0; j < BPT; ++j) {
-      c[j] = s_hist[kBins - 1 - (tid * BPT + j)];
-      sum += c[j];
+    for (int w = 0; w < warps; w += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(s + w);
+      v += (x.x + x.y) + (x.z + x.w);
     }
-    uint32_t incl = sum;
+    return v;
+  }
+  // the sum, and lo's minimum and hi's maximum
+  __device__ __forceinline__ uint32_t sum_range(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    lo = __reduce_min_sync(kAll, lo);
+    hi = __reduce_max_sync(kAll, hi);
+    uint32_t (*s)[16] = sc.sums[round];
+    if ((threadIdx.x & 31) == 0) {
+      s[1][threadIdx.x >> 5] = lo;
+      s[2][threadIdx.x >> 5] = hi;
+    }
+    v = sum(v);
+#pragma unroll
+    for (int w = 0; w < warps; w += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(s[1] + w), y = *reinterpret_cast<const uint4*>(s[2] + w);
+      lo = min(min(min(lo, x.x), min(x.y, x.z)), x.w);
+      hi = max(max(max(hi, y.x), max(y.y, y.z)), y.w);
+    }
+    return v;
+  }
+  // exclusive prefix sum over the threads
+  __device__ __forceinline__ uint32_t before(uint32_t v) {
+    const int lane = threadIdx.x & 31, me = threadIdx.x >> 5;
+    uint32_t incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += y;
     }
-    if (lane == 31) s_aux[warp] = incl;
+    uint32_t* s = sc.sums[round][0];
+    round ^= 1;
+    if (lane == 31) s[me] = incl;
     __syncthreads();
-    uint32_t above = incl - sum;
-    for (int w = 0; w < warp; ++w) above += s_aux[w];
-    if (above < rem && above + sum >= rem) {   // exactly one thread
+    uint32_t base = 0;
 #pragma unroll
-      for (int j = 0; j < BPT; ++j) {
-        if (above < rem && above + c[j] >= rem) {
-          s_aux[kSelWarps] = (uint32_t)(kBins - 1 - (tid * BPT + j));
-          s_aux[kSelWarps + 1] = rem - above;
-          s_aux[kSelWarps + 2] = c[j];
-        }
-        above += c[j];
-      }
+    for (int w = 0; w < warps; w += 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(s + w);
+      base += (w < me ? x.x : 0u) + (w + 1 < me ? x.y : 0u) + (w + 2 < me ? x.z : 0u) + (w + 3 < me ? x.w : 0u);
     }
-    // (the histogram is read: clear it for the next digit)
-#pragma unroll
-    for (int j = 0; j < BPT; ++j) s_hist[kBins - 1 - (tid * BPT + j)] = 0;
-    __syncthreads();
-    base |= s_aux[kSelWarps] << shift;
-    rem = s_aux[kSelWarps + 1];
-    const uint32_t in_bin = s_aux[kSelWarps + 2];
-    bits = shift;
-    if (in_bin == rem) return {base == 0 ? 0u : base - 1u, 0u, k};   // the bin is taken whole
+    return base + incl - v;
   }
-  return {base, rem, k};
+};
+
+// A thread's run of consecutive keys, read from shared memory in every pass.
+// Runs are a multiple of 4 long; keys past n read as 0.  (Kept in registers,
+// unrolled, the passes took longer: this code runs once per CTA, and its
+// length costs more than its loads.)
+template <int THREADS>
+struct KeyRun {
+  const uint32_t* keys;
+  int first, len, n;
+
+  __device__ __forceinline__ KeyRun(const uint32_t* k, int count) : keys(k), n(count) {
+    len = (count + 4 * THREADS - 1) / (4 * THREADS) * 4;
+    first = threadIdx.x * len;
+  }
+  // f(quad, index of its first key)
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll 1
+    for (int i = first; i < min(first + len, n); i += 4) {
+      uint4 v = *reinterpret_cast<const uint4*>(keys + i);   // (rows are padded to 4)
+      if (i + 1 >= n) v.y = 0;
+      if (i + 2 >= n) v.z = 0;
+      if (i + 3 >= n) v.w = 0;
+      f(v, i);
+    }
+  }
+};
+
+// The k largest keys: bins of equal score width count them (scores are spread
+// like a bell, so the k-th falls among a few), the keys of the bin that holds
+// the k-th are listed and compared with one another.  A bin still too full
+// for that (long ties) is cut again in key units, until one value is left.
+template <int THREADS>
+__device__ __forceinline__ Threshold find_threshold(Team<THREADS>& team, const KeyRun<THREADS>& run, int k,
+                                                    SelScratch& sc) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  // counts of candidates and forced ones, range of the others
+  uint32_t kmin = 0xffffffffu, kmax = 0, both = 0;
+  run.each([&](const uint4& v, int) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t x = c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+      both += (x != 0 ? 1u : 0u) + (x == kForced ? 0x10000u : 0u);   // (below 2^15 + 1 keys each)
+      kmin = min(kmin, x - 1u);               // 0 counts as the highest,
+      kmax = max(kmax, x + 1u);               // kForced as the lowest
+    }
+  });
+  uint4* hist4 = reinterpret_cast<uint4*>(sc.hist);
+  auto clear = [&]() {
+#pragma unroll
+    for (int j = tid; j < kBins / 4; j += THREADS) hist4[j] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) sc.n_rank = 0;
+  };
+  clear();
+  both = team.sum_range(both, kmin, kmax);
+  ++kmin;
+  --kmax;
+  const int cand = (int)(both & 0xffffu), forced = (int)(both >> 16);
+  if (cand <= k) return {0u, 0u, cand};                     // all of them
+  if (forced >= k) return {kForced, (uint32_t)k, k};
+  uint32_t rem = (uint32_t)(k - forced);                    // 1 <= rem < keys in [kmin, kmax]
+  bool linear = true;
+  for (;;) {
+    if (kmin == kmax) return {kmin, rem, k};
+    // bin = the whole number nearest (score - lowest) * width + 1, read off
+    // the mantissa of a sum with 2^23; it never falls with the score
+    const float f0 = score_of(kmin);
+    const float width = __fdividef((float)(kBins - 4), score_of(kmax) - f0);
+    const int shift = max(0, 32 - __clz(kmax - kmin) - kBinBits);
+    auto bin_of = [&](uint32_t x) -> uint32_t {   // kBins: outside the range
+      const uint32_t lin = min(__float_as_uint(fmaf(score_of(x) - f0, width, 8388609.0f)) - 0x4b000000u, (uint32_t)kBins - 1);
+      return x - kmin <= kmax - kmin ? (linear ? lin : (x - kmin) >> shift) : (uint32_t)kBins;
+    };
+    run.each([&](const uint4& v, int) {
+      const uint32_t b0 = bin_of(v.x), b1 = bin_of(v.y), b2 = bin_of(v.z), b3 = bin_of(v.w);
+      if (b0 < kBins) atomicAdd(&sc.hist[b0], 1u);
+      if (b1 < kBins) atomicAdd(&sc.hist[b1], 1u);
+      if (b2 < kBins) atomicAdd(&sc.hist[b2], 1u);
+      if (b3 < kBins) atomicAdd(&sc.hist[b3], 1u);
+    });
+    __syncthreads();
+    if (tid < 32) {
+      // lane l sums the bins from kBinsPL (31 - l) up, so lanes run from the
+      // top down; then the lane that holds the rem-th largest is scanned the
+      // same way, a bin a lane
+      uint32_t sum = 0;
+#pragma unroll
+      for (int j = 0; j < kBinsPL / 4; ++j) {
+        const uint4 v = hist4[(31 - lane) * (kBinsPL / 4) + j];
+        sum += (v.x + v.y) + (v.z + v.w);
+      }
+      uint32_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const int src = __ffs(__ballot_sync(kAll, incl >= rem)) - 1;
+      const uint32_t left = rem - __shfl_sync(kAll, incl - sum, src);
+      const uint32_t c = lane < kBinsPL ? sc.hist[(32 - src) * kBinsPL - 1 - lane] : 0u;
+      incl = c;
+#pragma unroll
+      for (int o = 1; o < kBinsPL; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const int at = __ffs(__ballot_sync(kAll, incl >= left)) - 1;
+      if (lane == at) sc.found = make_uint4((uint32_t)((32 - src) * kBinsPL - 1 - at), left - (incl - c), c, 0);
+    }
+    __syncthreads();
+    const uint32_t bin = sc.found.x, m = sc.found.z;
+    rem = sc.found.y;
+    if (m <= (uint32_t)kRanks) {
+      // list the bin's keys, then find the one with fewer than rem above it
+      // and at least rem at or above it
+      run.each([&](const uint4& v, int) {
+        const bool h0 = bin_of(v.x) == bin, h1 = bin_of(v.y) == bin;
+        const bool h2 = bin_of(v.z) == bin, h3 = bin_of(v.w) == bin;
+        if (h0 || h1 || h2 || h3) {   // (rare)
+          if (h0) sc.rank[atomicAdd(&sc.n_rank, 1u)] = v.x;
+          if (h1) sc.rank[atomicAdd(&sc.n_rank, 1u)] = v.y;
+          if (h2) sc.rank[atomicAdd(&sc.n_rank, 1u)] = v.z;
+          if (h3) sc.rank[atomicAdd(&sc.n_rank, 1u)] = v.w;
+        }
+      });
+      __syncthreads();
+      auto place = [&](uint32_t x, uint32_t& gt, uint32_t& ge) {
+        gt = ge = 0;
+#pragma unroll 4
+        for (uint32_t j = 0; j < m; ++j) {
+          const uint32_t y = sc.rank[j];
+          gt += y > x;
+          ge += y >= x;
+        }
+      };
+      uint32_t gt, ge;
+      if (m <= 32) {   // each warp by itself
+        const uint32_t x = (uint32_t)lane < m ? sc.rank[lane] : 0u;
+        place(x, gt, ge);
+        const int s = __ffs(__ballot_sync(kAll, x != 0 && gt < rem && ge >= rem)) - 1;
+        return {__shfl_sync(kAll, x, s), rem - __shfl_sync(kAll, gt, s), k};
+      }
+      for (uint32_t i = (int)threadIdx.x; i < m; i += THREADS) {
+        const uint32_t x = sc.rank[i];
+        place(x, gt, ge);
+        if (gt < rem && ge >= rem) {   // (equal keys write the same)
+          sc.found.x = x;
+          sc.found.y = rem - gt;
+        }
+      }
+      __syncthreads();
+      return {sc.found.x, sc.found.y, k};
+    }
+    // the range of the bin's keys, for the next round
+    uint32_t lo = 0xffffffffu, hi = 0;
+    run.each([&](const uint4& v, int) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x = c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+        if (bin_of(x) == bin) {
+          lo = min(lo, x);
+          hi = max(hi, x);
+        }
+      }
+    });
+    __syncthreads();   // every warp has read the histogram
+    clear();
+    (void)team.sum_range(0u, lo, hi);
+    __syncthreads();
+    kmin = lo;
+    kmax = hi;
+    linear = false;
+  }
 }
 
-// RC query heads of one token are scored together.
-template <int HD, int RC>
-__global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(SelectArgs a) {
-  constexpr int LPB = HD / 16;            // lanes per block
-  constexpr int BPP = 32 / LPB;           // blocks per warp pass
+// The list of one token: the k largest of its n keys in ascending index
+// order, looked up in the table, -1 behind them, and the list's cells.
+template <int THREADS>
+__device__ __forceinline__ void write_list(Team<THREADS>& team, SelScratch& sc, const uint32_t* keys, int n, int k,
+                                           const int32_t* table, int32_t* out_blk, int32_t* out_idx,
+                                           int32_t* out_len, int bs, int cells) {
+  const KeyRun<THREADS> run(keys, n);
+  const Threshold th = find_threshold(team, run, k, sc);
+  __syncthreads();   // (the bins and the ranked keys are free from here on)
+  // keys taken above the threshold and equal to it, before each thread's own
+  uint32_t own = 0;
+  run.each([&](const uint4& v, int) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t x = c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+      own += (x > th.thr ? 0x10000u : 0u) + (x == th.thr && x != 0u ? 1u : 0u);
+    }
+  });
+  if ((int)threadIdx.x == 0) sc.last = 0;
+  const uint32_t before = team.before(own);
+  __syncthreads();   // (sc.last)
+  uint32_t gb = before >> 16, eb = before & 0xffffu;
+  // Lists that fit go through shared memory, so their block ids are looked
+  // up all at once.
+  const bool staged = th.count <= kListMax;
+  if (own != 0)
+    run.each([&](const uint4& v, int i) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x = c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+        const bool above = x > th.thr, equal = x == th.thr && x != 0u;
+        if (above || (equal && eb < th.ties)) {
+          const uint32_t at = gb + min(eb, th.ties);
+          if (staged) {
+            sc.list[at] = (uint16_t)(i + c);
+          } else {
+            out_blk[at] = __ldg(table + i + c);
+            if (out_idx != nullptr) out_idx[at] = i + c;
+          }
+          if (i + c == n - 1) sc.last = 1;
+        }
+        gb += above;
+        eb += equal;
+      }
+    });
+  __syncthreads();
+#pragma unroll 4
+  for (int i = (int)threadIdx.x; i < k; i += THREADS) {
+    if (i < th.count && !staged) continue;
+    const int j = i < th.count ? sc.list[i] : -1;
+    out_blk[i] = j >= 0 ? __ldg(table + j) : -1;
+    if (out_idx != nullptr) out_idx[i] = j;
+  }
+  if ((int)threadIdx.x == 0) *out_len = th.count * bs - (sc.last ? bs - 1 - (cells - 1) % bs : 0);
+}
+
+// NT n-tiles of 8 query rows; THREADS 256 (3 CTAs an SM where the
+// registers allow it, else 2) or 512 (one).
+template <int HD, int NT, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <= 128 ? 3 : 2)
+    select_blocks_kernel(SelectArgs a) {
+  constexpr int kSelWarps = THREADS / 32;
   constexpr int NG = HD / kGroup;
-  constexpr int PASSES = HD == 256 ? 4 : 2;
-  constexpr int STRIP = BPP * PASSES;     // blocks whose loads a warp has in flight: 16, 8, 8
+  constexpr int STRIP = 16;               // blocks a warp scores at once
+  constexpr int DEPTH = NG < 2 ? NG : 2;  // units (16 blocks x 64 dims) whose loads a warp has in flight
+  constexpr int CHAINS = NT <= 2 ? 2 : 1;   // (registers)
+  constexpr bool BREG = NT == 1 && HD <= 128 && THREADS == 512;   // q fragments stay in registers
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ uint32_t s_hist[kBins];
-  __shared__ uint32_t s_aux[4 * kSelWarps + 4];
+  __shared__ SelScratch sc;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
   const uint32_t rank = cta_rank();
   const int C = a.cluster;
   cluster_arrive();   // every CTA of the cluster runs before a remote store below
@@ -202,152 +459,212 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(SelectArgs a
   id /= a.n_wg;
   const int h = id % a.n_kv, b = id / a.n_kv;
   const int w0 = wg * a.wg_tok, nw = min(a.wg_tok, a.W - w0);
+  const int len_raw = __ldg(a.ctx_lens + b);
+  // the query rows: a warp per (padded row, 64 dims), two dims a lane
+  constexpr int QPW = (NT * 8 * NG + kSelWarps - 1) / kSelWarps;
+  float2 qv[QPW];
+#pragma unroll
+  for (int k = 0; k < QPW; ++k) {
+    const int i = min(warp + k * kSelWarps, NT * 8 * NG - 1), r = i / NG, gq = i - r * NG;
+    const int w = min(r >> a.gp_log2, nw - 1), gg = min(r & ((1 << a.gp_log2) - 1), a.G - 1);
+    const float* src = a.q + (((size_t)b * a.W + w0 + w) * a.n_q + (size_t)h * a.G + gg) * HD + gq * kGroup;
+    qv[k] = __ldg(reinterpret_cast<const float2*>(src) + lane);
+  }
   const long long cap = min((long long)a.max_blocks << a.bs_log2, (long long)a.n_cap << a.bs_log2);
-  const int len = (int)max(0LL, min((long long)__ldg(a.ctx_lens + b), cap));
+  const int len = (int)max(0LL, min((long long)len_raw, cap));
   const int bs = 1 << a.bs_log2;
   auto visible = [&](int w) { return max(0, len - a.W + w0 + w + 1); };        // cells token w0 + w sees
-  auto blocks_of = [&](int cells) { return (cells + bs - 1) >> a.bs_log2; };
+  auto blocks_of = [&](int cells) { return (cells >> a.bs_log2) + ((cells & (bs - 1)) != 0); };
   const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
-  const int rows = nw * a.G;
-  const SelSmem lay = sel_smem(HD, a.wg_tok * a.G, a.lead_rows, a.n_cap);
-  int8_t* s_codes = reinterpret_cast<int8_t*>(smem + lay.codes);
+  const SelSmem lay = sel_smem(HD, NT, a.lead_rows, a.n_cap);
+  uint32_t* s_q = reinterpret_cast<uint32_t*>(smem);
   float* s_scale = reinterpret_cast<float*>(smem + lay.scales);
   uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + lay.keys);
 
-  // q codes: a warp per (row, 64 dims), two dims a lane
-  for (int i = warp; i < rows * NG; i += kSelWarps) {
-    const int r = i / NG, g = i - r * NG;
-    const int w = r / a.G, gg = r - w * a.G;
-    const float* src = a.q + (((size_t)b * a.W + w0 + w) * a.n_q + (size_t)h * a.G + gg) * HD + g * kGroup;
-    float2 x = __ldg(reinterpret_cast<const float2*>(src) + lane);
+  // this CTA's share of the blocks the last token sees; the first bounds are
+  // fetched while the q codes are made
+  const int n_all = blocks_of(visible(nw - 1));
+  const int share = ((n_all + C - 1) / C + STRIP - 1) / STRIP * STRIP;
+  const int j0 = min((int)rank * share, n_all), j1 = min(j0 + share, n_all);
+  constexpr int STEP = kSelWarps * STRIP;
+  auto load_ids = [&](int s0) -> int {
+    return s0 + (lane & 15) < j1 ? __ldg(table + s0 + (lane & 15)) : -1;
+  };
+  // A lane's loads of group q of a strip: dims 16 t .. + 15 of blocks g and
+  // g + 8, lo and hi.  Foreign blocks read as zeros.
+  struct Unit {
+    uint4 lo[2], hi[2];
+    float ks[2];
+  };
+  auto load_unit = [&](int ids, int gq, Unit& u) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int blk = __shfl_sync(kAll, ids, g + 8 * i);
+      u.lo[i] = u.hi[i] = make_uint4(0, 0, 0, 0);
+      u.ks[i] = 0.f;
+      if (blk >= 0 && blk < a.n_blocks) {
+        const size_t row = (size_t)blk * a.n_kv + h;
+        const int8_t* src = a.bounds + row * 2 * HD + gq * kGroup + t * 16;
+        u.lo[i] = __ldg(reinterpret_cast<const uint4*>(src));
+        u.hi[i] = __ldg(reinterpret_cast<const uint4*>(src + HD));
+        u.ks[i] = __ldg(a.scales + row * NG + gq);
+      }
+    }
+  };
+  const int first = j0 + warp * STRIP;
+  int ids = load_ids(first), ids_next = load_ids(first + STEP);
+
+  // q codes
+#pragma unroll
+  for (int k = 0; k < QPW; ++k) {
+    const int i = warp + k * kSelWarps, r = i / NG, gq = i - r * NG;
+    if (i >= NT * 8 * NG) break;
+    float2 x = qv[k];
     x.x = x.x == x.x ? x.x : 0.f;
     x.y = x.y == x.y ? x.y : 0.f;
     const float m = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(fmaxf(fabsf(x.x), fabsf(x.y)))));
     const int e = q_exponent(m);
     const float inv = pow2f_exact(-e);
-    const int c0 = __float2int_rn(fminf(fmaxf(x.x * inv, -127.f), 127.f));
-    const int c1 = __float2int_rn(fminf(fmaxf(x.y * inv, -127.f), 127.f));
-    char2* neg = reinterpret_cast<char2*>(s_codes + (size_t)r * 2 * HD + g * kGroup) + lane;
-    char2* pos = reinterpret_cast<char2*>(s_codes + (size_t)r * 2 * HD + HD + g * kGroup) + lane;
-    *neg = make_char2((signed char)min(c0, 0), (signed char)min(c1, 0));
-    *pos = make_char2((signed char)max(c0, 0), (signed char)max(c1, 0));
-    if (lane == 0) s_scale[r * NG + g] = pow2f_exact(e);
+    const float c0 = rintf(fminf(fmaxf(x.x * inv, -127.f), 127.f));
+    const float c1 = rintf(fminf(fmaxf(x.y * inv, -127.f), 127.f));
+    // dims 2 lane, + 1 of the group: fragment lane 4 (r % 8) + lane / 8,
+    // k-step (lane % 8) / 2, word lane % 2
+    const int at = ((((r >> 3) * NG + gq) * 4 + ((lane & 7) >> 1)) * 2) * 64 + ((r & 7) * 4 + (lane >> 3)) * 2 + (lane & 1);
+    s_q[at] = pack_half2(fminf(c0, 0.f), fminf(c1, 0.f));
+    s_q[at + 64] = pack_half2(fmaxf(c0, 0.f), fmaxf(c1, 0.f));
+    if (lane == 0) s_scale[r * NG + gq] = pow2f_exact(e);
   }
+  Unit unit[DEPTH];
+#pragma unroll
+  for (int q = 0; q < DEPTH; ++q) load_unit(ids, q, unit[q]);
   __syncthreads();
 
-  // this CTA's share of the blocks the last token sees
-  const int n_all = blocks_of(visible(nw - 1));
-  const int share = ((n_all + C - 1) / C + STRIP - 1) / STRIP * STRIP;
-  const int j0 = min((int)rank * share, n_all), j1 = min(j0 + share, n_all);
-  const int l = lane % LPB, sub = lane / LPB;      // lane's dims 16 l .. + 15 of block sub of a pass
   const uint32_t keys_addr = static_cast<uint32_t>(__cvta_generic_to_shared(s_keys));
-  const int n_chunks = (a.G + RC - 1) / RC;
-
-  // q codes (min and max parts) and scales of RC heads, the lane's dims; a
-  // chunk past the group's end repeats its last head, which leaves the
-  // maximum over heads as it is
-  auto load_q = [&](int w, int ch, uint4 (&qn)[RC], uint4 (&qp)[RC], float (&qs)[RC]) {
-#pragma unroll
-    for (int i = 0; i < RC; ++i) {
-      const int r = w * a.G + min(ch * RC + i, a.G - 1);
-      const int8_t* base = s_codes + (size_t)r * 2 * HD + l * 16;
-      qn[i] = *reinterpret_cast<const uint4*>(base);
-      qp[i] = *reinterpret_cast<const uint4*>(base + HD);
-      qs[i] = s_scale[r * NG + l / 4];
-    }
+  auto b_frag = [&](int nt, int q, int kk, int which) -> uint2 {
+    return *reinterpret_cast<const uint2*>(s_q + (((nt * NG + q) * 4 + kk) * 2 + which) * 64 + lane * 2);
   };
-  // this lane's score of one row chunk: which of the RC rows it holds after
-  // the reduction does not matter, the caller takes the maximum over them
-  auto score = [&](const uint4& lo, const uint4& hi, float ks, const uint4 (&qn)[RC], const uint4 (&qp)[RC],
-                   const float (&qs)[RC]) -> float {
-    int s[RC];
+  uint2 breg[BREG ? NG : 1][4][2];
+  if constexpr (BREG) {
 #pragma unroll
-    for (int i = 0; i < RC; ++i) {
-      int v = __dp4a((int)lo.x, (int)qn[i].x, 0);
-      v = __dp4a((int)hi.x, (int)qp[i].x, v);
-      v = __dp4a((int)lo.y, (int)qn[i].y, v);
-      v = __dp4a((int)hi.y, (int)qp[i].y, v);
-      v = __dp4a((int)lo.z, (int)qn[i].z, v);
-      v = __dp4a((int)hi.z, (int)qp[i].z, v);
-      v = __dp4a((int)lo.w, (int)qn[i].w, v);
-      s[i] = __dp4a((int)hi.w, (int)qp[i].w, v);
-    }
-    // sum over the 4 lanes of the 64 dims; with 4 rows each lane ends with
-    // one row's sum, with 2 rows each pair of lanes
-    int v;
-    float sc;
-    if constexpr (RC == 4) {
-      const bool odd = lane & 1, two = lane & 2;
-      const int k0 = odd ? s[2] : s[0], k1 = odd ? s[3] : s[1];
-      const int g0 = odd ? s[0] : s[2], g1 = odd ? s[1] : s[3];
-      const int a0 = k0 + __shfl_xor_sync(kAll, g0, 1), a1 = k1 + __shfl_xor_sync(kAll, g1, 1);
-      v = (two ? a1 : a0) + __shfl_xor_sync(kAll, two ? a0 : a1, 2);
-      sc = odd ? (two ? qs[3] : qs[2]) : (two ? qs[1] : qs[0]);
-    } else if constexpr (RC == 2) {
-      const bool odd = lane & 1;
-      v = (odd ? s[1] : s[0]) + __shfl_xor_sync(kAll, odd ? s[0] : s[1], 1);
-      v += __shfl_xor_sync(kAll, v, 2);
-      sc = odd ? qs[1] : qs[0];
-    } else {
-      v = s[0] + __shfl_xor_sync(kAll, s[0], 1);
-      v += __shfl_xor_sync(kAll, v, 2);
-      sc = qs[0];
-    }
-    float t = (float)v * (sc * ks);
-    if constexpr (NG >= 2) t += __shfl_xor_sync(kAll, t, 4);
-    if constexpr (NG >= 4) t += __shfl_xor_sync(kAll, t, 8);
-    return t;
-  };
+    for (int q = 0; q < NG; ++q)
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int which = 0; which < 2; ++which) breg[q][kk][which] = b_frag(0, q, kk, which);
+  }
+  const int gp = 1 << a.gp_log2;
+  // the key of block j for token w
   auto emit = [&](int w, int j, int blk, float best) {
+    if (w >= nw || j >= j1) return;
     const int nb = blocks_of(visible(w));
     uint32_t key = 0;
     if (j < nb && blk >= 0 && blk < a.n_blocks)
       key = (j < a.n_first || j >= nb - a.n_last) ? kForced : ordered(best);
-    const uint32_t lead = (uint32_t)w % (uint32_t)C, row = (uint32_t)w / (uint32_t)C;
-    store_remote(keys_addr + (row * (uint32_t)a.n_cap + (uint32_t)j) * 4u, lead, key);
+    const int row = w >> a.c_log2;
+    store_remote(keys_addr + (uint32_t)(row * key_row(a.n_cap) + j) * 4u, (uint32_t)(w - (row << a.c_log2)), key);
   };
 
-  uint4 qn[RC], qp[RC];
-  float qs[RC];
-  const bool fixed_q = nw == 1 && n_chunks == 1;   // one chunk: q stays in registers
-  if (fixed_q) load_q(0, 0, qn, qp, qs);
   __syncwarp();
   cluster_wait();
-  for (int s0 = j0 + warp * STRIP; s0 < j1; s0 += kSelWarps * STRIP) {
-    // physical ids of the strip, then every bound of it
-    const int my = s0 + lane < j1 && lane < STRIP ? __ldg(table + s0 + lane) : -1;
-    uint4 lo[PASSES], hi[PASSES];
-    float ks[PASSES];
-    int blk[PASSES];
+  for (int s0 = first; s0 < j1; s0 += STEP) {
+    const int ids_cur = ids;
+    ids = ids_next;
+    ids_next = load_ids(s0 + 2 * STEP);
+    float z[NT][4], z2[NG == 4 ? NT : 1][4];   // score sums: blocks g (0, 1), g + 8 (2, 3), rows 2t, 2t + 1
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) {
-      blk[p] = __shfl_sync(kAll, my, p * BPP + sub);
-      lo[p] = hi[p] = make_uint4(0, 0, 0, 0);
-      ks[p] = 0.f;
-      if (blk[p] >= 0 && blk[p] < a.n_blocks) {
-        const size_t row = (size_t)blk[p] * a.n_kv + h;
-        const int8_t* src = a.bounds + row * 2 * HD + l * 16;
-        lo[p] = __ldg(reinterpret_cast<const uint4*>(src));
-        hi[p] = __ldg(reinterpret_cast<const uint4*>(src + HD));
-        ks[p] = __ldg(a.scales + row * NG + l / 4);
+    for (int q = 0; q < NG; ++q) {
+      Unit& u = unit[q % DEPTH];
+      float acc[NT][CHAINS][4];   // lo and hi sums apart: shorter chains (whole numbers both)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 4 * CHAINS; ++k) acc[nt][k >> 2][k & 3] = 0.f;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        // fp16 fragments of the group: k-step kk is the lane's word kk
+        uint32_t af[4][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 v = which ? u.hi[i] : u.lo[i];
+          widen(v.x, af[0][i], af[0][2 + i]);
+          widen(v.y, af[1][i], af[1][2 + i]);
+          widen(v.z, af[2][i], af[2][2 + i]);
+          widen(v.w, af[3][i], af[3][2 + i]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            uint2 bf;
+            if constexpr (BREG) bf = breg[q][kk][which];
+            else bf = b_frag(nt, q, kk, which);
+            mma_f16(acc[nt][which % CHAINS], af[kk], bf.x, bf.y);
+          }
       }
+      const float ks0 = u.ks[0], ks1 = u.ks[1];
+      // the unit DEPTH further on, of this strip or the next
+      if (q + DEPTH < NG) load_unit(ids_cur, q + DEPTH, u);
+      else load_unit(ids, q + DEPTH - NG, u);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float qs = s_scale[(nt * 8 + 2 * t + c) * NG + q];
+          // S * (scale_q * scale_k), both exact; groups add pairwise
+#pragma unroll
+          for (int k = c; k < 4; k += 2) {
+            const float v = __fmul_rn(CHAINS == 2 ? acc[nt][0][k] + acc[nt][CHAINS - 1][k] : acc[nt][0][k], __fmul_rn(qs, k < 2 ? ks0 : ks1));
+            if (q == 0) z[nt][k] = v;
+            else if (q == 1) z[nt][k] = __fadd_rn(z[nt][k], v);
+            else if (q == 2) z2[NG == 4 ? nt : 0][k] = v;
+            else z[nt][k] = __fadd_rn(z[nt][k], __fadd_rn(z2[NG == 4 ? nt : 0][k], v));
+          }
+        }
     }
-    for (int w = 0; w < nw; ++w) {
-      float best[PASSES];
+    // the largest over a token's rows, then its keys
+    const int blk0 = __shfl_sync(kAll, ids_cur, g), blk1 = __shfl_sync(kAll, ids_cur, g + 8);
+    const int ja = s0 + g, jb = s0 + g + 8;
+    if (gp == 1) {
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) best[p] = -INFINITY;
-      for (int ch = 0; ch < n_chunks; ++ch) {
-        if (!fixed_q) load_q(w, ch, qn, qp, qs);
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int p = 0; p < PASSES; ++p) best[p] = fmaxf(best[p], score(lo[p], hi[p], ks[p], qn, qp, qs));
+        for (int c = 0; c < 2; ++c) {
+          emit(nt * 8 + 2 * t + c, ja, blk0, z[nt][c]);
+          emit(nt * 8 + 2 * t + c, jb, blk1, z[nt][2 + c]);
+        }
+    } else if (gp <= 8) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float m0 = fmaxf(z[nt][0], z[nt][1]), m1 = fmaxf(z[nt][2], z[nt][3]);
+        for (int o = 1; 2 * o < gp; o <<= 1) {
+          m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, o));
+          m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, o));
+        }
+        if (((2 * t) & (gp - 1)) == 0) {
+          const int w = (nt * 8 + 2 * t) >> a.gp_log2;
+          emit(w, ja, blk0, m0);
+          emit(w, jb, blk1, m1);
+        }
       }
+    } else {   // 16 or 32 rows a token: 2 or 4 n-tiles
+      float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-      for (int p = 0; p < PASSES; ++p) {
-        float v = best[p];
-        if constexpr (RC >= 2) v = fmaxf(v, __shfl_xor_sync(kAll, v, 1));
-        if constexpr (RC >= 4) v = fmaxf(v, __shfl_xor_sync(kAll, v, 2));
-        const int j = s0 + p * BPP + sub;
-        if (l == 0 && j < j1) emit(w, j, blk[p], v);
+      for (int nt = 0; nt < NT; ++nt) {
+        m0 = fmaxf(m0, fmaxf(z[nt][0], z[nt][1]));
+        m1 = fmaxf(m1, fmaxf(z[nt][2], z[nt][3]));
+        if (((nt * 8 + 8) & (gp - 1)) == 0) {
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, o));
+          }
+          if (t == 0) {
+            const int w = (nt * 8) >> a.gp_log2;
+            emit(w, ja, blk0, m0);
+            emit(w, jb, blk1, m1);
+          }
+          m0 = m1 = -INFINITY;
+        }
       }
     }
   }
@@ -356,75 +673,37 @@ __global__ void __launch_bounds__(kSelThreads) select_blocks_kernel(SelectArgs a
   cluster_wait();   // every key is in its leader's shared memory
 
   // ---------------- selection: token w is led by CTA w % C ----------------
+  auto out_row = [&](int w) { return ((size_t)b * a.W + w0 + w) * a.n_kv + h; };
+  auto keys_of = [&](int w) { return s_keys + (size_t)(w >> a.c_log2) * key_row(a.n_cap); };
+  auto index_of = [&](size_t row) { return a.sel_index != nullptr ? a.sel_index + row * a.n_sel : nullptr; };
+  Team<THREADS> team{sc};
   for (int w = (int)rank; w < nw; w += C) {
-    const uint32_t* keys = s_keys + (size_t)(w / C) * a.n_cap;
-    const int cells = visible(w), nb = blocks_of(cells);
-    const size_t out_row = ((size_t)b * a.W + w0 + w) * a.n_kv + h;
-    int32_t* out_blk = a.sel_blocks + out_row * a.n_sel;
-    int32_t* out_idx = a.sel_index != nullptr ? a.sel_index + out_row * a.n_sel : nullptr;
-    const Threshold th = find_threshold(keys, nb, a.n_sel, s_hist, s_aux);
-    // each warp lists a contiguous range of blocks
-    const int seg = ((nb + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-    const int i0 = min(warp * seg, nb), i1 = min(i0 + seg, nb);
-    int gt = 0, eq = 0;
-    for (int i = i0; i < i1; i += 32) {
-      const uint32_t x = i + lane < i1 ? keys[i + lane] : 0u;
-      gt += __popc(__ballot_sync(kAll, x > th.thr));
-      eq += __popc(__ballot_sync(kAll, x == th.thr && x != 0u));
-    }
-    __syncthreads();   // s_aux is free again
-    if (lane == 0) {
-      s_aux[warp] = (uint32_t)gt;
-      s_aux[kSelWarps + warp] = (uint32_t)eq;
-    }
-    if (tid == 0) s_aux[2 * kSelWarps] = 0;
-    __syncthreads();
-    uint32_t gb = 0, eb = 0;   // taken above, and equal, in the ranges before
-    for (int v = 0; v < warp; ++v) {
-      gb += s_aux[v];
-      eb += s_aux[kSelWarps + v];
-    }
-    const uint32_t lt = (1u << lane) - 1u;
-    for (int i = i0; i < i1; i += 32) {
-      const uint32_t x = i + lane < i1 ? keys[i + lane] : 0u;
-      const uint32_t mg = __ballot_sync(kAll, x > th.thr), me = __ballot_sync(kAll, x == th.thr && x != 0u);
-      const uint32_t ebl = eb + __popc(me & lt);
-      const bool take = ((mg >> lane) & 1u) || (((me >> lane) & 1u) && ebl < th.ties);
-      if (take) {
-        const uint32_t at = gb + __popc(mg & lt) + min(ebl, th.ties);
-        out_blk[at] = __ldg(table + i + lane);
-        if (out_idx != nullptr) out_idx[at] = i + lane;
-        if (i + lane == nb - 1) s_aux[2 * kSelWarps] = 1u;
-      }
-      gb += __popc(mg);
-      eb += __popc(me);
-    }
-    for (int i = th.count + tid; i < a.n_sel; i += kSelThreads) {
-      out_blk[i] = -1;
-      if (out_idx != nullptr) out_idx[i] = -1;
-    }
-    __syncthreads();
-    if (tid == 0) a.sel_lens[out_row] = th.count * bs - (s_aux[2 * kSelWarps] ? nb * bs - cells : 0);
-    __syncthreads();   // s_aux and the histogram are reused by the next token
+    const size_t row = out_row(w);
+    write_list(team, sc, keys_of(w), blocks_of(visible(w)), a.n_sel, table, a.sel_blocks + row * a.n_sel,
+                  index_of(row), a.sel_lens + row, bs, visible(w));
+    if (w + C < nw) __syncthreads();   // the scratch is reused by the next token
   }
 }
 
-template <int HD, int RC>
-cudaError_t launch_rc(const SelectArgs& a, cudaStream_t s) {
+template <int HD, int NT, int THREADS>
+cudaError_t launch_nt(const SelectArgs& a, cudaStream_t s) {
   static ContextCache<int> cache;
   int ready = 0;
   if (!per_context(cache, &ready, [](int* v) {
         *v = 1;
-        return cudaFuncSetAttribute(select_blocks_kernel<HD, RC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kSelMaxSmem) == cudaSuccess;
+        // clusters of 16 are past the portable 8
+        return cudaFuncSetAttribute(select_blocks_kernel<HD, NT, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSelMaxSmem) == cudaSuccess &&
+               cudaFuncSetAttribute(select_blocks_kernel<HD, NT, THREADS>,
+                                    cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
       }))
     return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   const long long ctas = (long long)a.n_seq * a.n_kv * a.n_wg * a.cluster;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
   cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = sel_smem(HD, a.wg_tok * a.G, a.lead_rows, a.n_cap).bytes;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = sel_smem(HD, NT, a.lead_rows, a.n_cap).bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -435,33 +714,57 @@ cudaError_t launch_rc(const SelectArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_blocks_kernel<HD, RC>, a);
+  return cudaLaunchKernelEx(&cfg, select_blocks_kernel<HD, NT, THREADS>, a);
+}
+
+int n_tiles(const SelectArgs& a) {
+  const int rows = a.wg_tok << a.gp_log2;
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
 template <int HD>
 cudaError_t launch_hd(const SelectArgs& a, cudaStream_t s) {
-  if (a.G == 1) return launch_rc<HD, 1>(a, s);
-  if (a.G == 2) return launch_rc<HD, 2>(a, s);
-  return launch_rc<HD, 4>(a, s);
+  const int nt = n_tiles(a);
+  if (a.wide) {
+    if (nt == 1) return launch_nt<HD, 1, 512>(a, s);
+    if (nt == 2) return launch_nt<HD, 2, 512>(a, s);
+    return launch_nt<HD, 4, 512>(a, s);
+  }
+  if (nt == 1) return launch_nt<HD, 1, 256>(a, s);
+  if (nt == 2) return launch_nt<HD, 2, 256>(a, s);
+  return launch_nt<HD, 4, 256>(a, s);
 }
 
 }  // namespace
 
 bool plan_select(int hd, int sms, SelectArgs* a) {
-  // tokens per cluster: as many as keep the q codes at 32 rows, whose
-  // bounds are then read once
-  const int max_tok = 32 / a->G;
+  a->gp_log2 = 0;
+  while ((1 << a->gp_log2) < a->G) ++a->gp_log2;
+  // tokens per cluster: up to 32 padded rows, for which the bounds are read
+  // once
+  const int max_tok = 32 >> a->gp_log2;
   a->wg_tok = a->W < max_tok ? a->W : max_tok;
-  // CTAs per cluster: enough to fill the SMs, at least 64 blocks each
-  int c = 1;
   for (;;) {
     a->n_wg = (a->W + a->wg_tok - 1) / a->wg_tok;
     const long long clusters = (long long)a->n_seq * a->n_kv * a->n_wg;
-    c = 1;
-    while (c < 8 && clusters * c < sms && a->n_cap >= 128 * c) c *= 2;
-    a->cluster = c;
-    a->lead_rows = (a->wg_tok + c - 1) / c;
-    if (sel_smem(hd, a->wg_tok * a->G, a->lead_rows, a->n_cap).bytes <= kSelMaxSmem) return true;
+    // CTAs per cluster: as many as fill the SMs once, at least 64 blocks each
+    // and at most 8 (16 from 8192 blocks: 16384 blocks x 2 heads 29 us, with
+    // 8 CTAs 42 us; 512 blocks x 8 heads 6.1 us either way, 4096 blocks x 8
+    // heads x 4 tokens 15.6 us, with 8 CTAs 12.7 us); for batches of long rows
+    // up to four times the SMs, at least 1024 blocks each, which evens
+    // out ragged lengths (64 sequences 83 -> 79 us; 16 of up to 256 blocks
+    // would take 10.1 us instead of 8.5).
+    const int most = a->n_cap >= 8192 ? 4 : 3;
+    int c = 0;
+    while (c < most && (clusters << c) < sms && a->n_cap >= (64 << c)) ++c;
+    while (c < most && (clusters << c) < 4 * sms && a->n_cap >= (2048 << c)) ++c;
+    a->c_log2 = c;
+    a->cluster = 1 << c;
+    // 512 threads where every CTA has an SM to itself and rows are long (4096
+    // blocks x 8 heads x 4 tokens 14.6 -> 12.7 us, 16384 x 2 40 -> 29 us)
+    a->wide = a->n_cap >= 2048 && (clusters << c) <= sms;
+    a->lead_rows = (a->wg_tok + a->cluster - 1) >> c;
+    if (sel_smem(hd, n_tiles(*a), a->lead_rows, a->n_cap).bytes <= kSelMaxSmem) return true;
     if (a->wg_tok == 1) return false;
     a->wg_tok = (a->wg_tok + 1) / 2;
   }
