@@ -99,6 +99,27 @@ bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, Dec
   if (sms <= 0) sms = 148;
   const long long capacity = (long long)per_sm * sms;
   const long long target = capacity * (lists ? kListWaves : n_seq > 1 ? 4 : 1);
+  p->c_log2 = -1;
+  if (lists) {
+    // Splits of a row tile in one cluster of up to 8, merged there, if that
+    // fills four fifths of one wave, else through the workspace and the
+    // combine.  4096 cells a list, 128 int8 lists: 33.7 us in clusters of 4,
+    // 35.2 us through the workspace; 512 FP16 lists 165 and 170 us, one split
+    // each.  Where clusters leave a third of the wave empty, or 16 CTAs have to
+    // be placed together, they lose: 96 int8 lists 26 and 22 us, 8 FP16 lists
+    // 10.7 and 9.2 us.
+    int c = 0;
+    while (c < 3 && (units << (c + 1)) <= capacity && (1 << c) < tiles) ++c;
+    if ((units << c) * 5 >= capacity * 4) {
+      const int split_tiles = (tiles + (1 << c) - 1) >> c;
+      p->c_log2 = c;
+      p->split_cells = split_tiles * tile;
+      p->nsplit = 1 << c;
+      p->off_o = p->off_ml = 0;
+      p->bytes = 256;
+      return true;
+    }
+  }
   long long ns = target / units;
   if (ns < 1) ns = 1;
   if (ns > tiles) ns = tiles;
@@ -240,6 +261,7 @@ kvq_status decode_impl(const kvq_cache* cache, const float* q, int n_seq, int W,
   a.n_q = n_q;
   a.G = n_q / cache->n_kv_heads;
   a.g_magic = (0x100000000ull + (unsigned long long)a.G - 1) / (unsigned long long)a.G;
+  a.c_log2 = -1;
   a.n_kv = cache->n_kv_heads;
   a.div_heads = make_fastdiv(1);
   a.div_nseq = make_fastdiv(1);
@@ -346,6 +368,7 @@ KVQ_API kvq_status kvq_sparse_decode_attn(const kvq_cache* cache, const float* q
   if (!plan.use_mma) return KVQ_ERR_CUDA;
   DecodeArgs a;
   a.pool = make_pool(cache);
+  a.c_log2 = plan.c_log2;
   a.n_kv = 1;
   a.div_heads = make_fastdiv((unsigned)cache->n_kv_heads);
   a.div_nseq = make_fastdiv((unsigned)ls.n_lists);

@@ -244,6 +244,133 @@ __device__ __forceinline__ bool item_of(const DecodeArgs& a, int c, int& b, int&
 }
 
 // ---------------------------------------------------------------------------
+// Block lists, the splits of a row tile in one thread-block cluster: the CTAs'
+// rows meet through distributed shared memory and the output is written
+// here, without partials in global memory and a second kernel.  Called after
+// the 4 warps' slabs are in place; leaves when every CTA has read its peers.
+// ---------------------------------------------------------------------------
+template <int FMT, int HD, int NT>
+__device__ __forceinline__ void merge_cluster(const DecodeArgs& a, unsigned char* smem, int list, int r0, int Rc) {
+  using C = Cfg<FMT, HD, NT>;
+  constexpr int RP = NT * 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* s_slab = reinterpret_cast<float*>(smem);                          // [warp][Rc][HD]
+  const float* s_wml = reinterpret_cast<const float*>(smem + C::SMEM_WML);  // [warp][RP][m, l]
+  float2* s_fin = reinterpret_cast<float2*>(smem + C::SMEM_Q);             // [Rc] (q is done with)
+  // this CTA's rows, in slab 0, and their maximum (NaN: a lost wait) and sum
+  if constexpr (C::V4) {
+    constexpr int U = HD >= 128 ? 4 : 2, NI = HD / (32 * U);
+    for (int r = warp; r < Rc; r += kConsumerWarps) {
+      float x[NI][U];
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < U; ++e) {
+          const float* col = s_slab + r * HD + U * lane + 32 * U * i + e;
+          x[i][e] = (col[0] + col[Rc * HD]) + (col[2 * Rc * HD] + col[3 * Rc * HD]);
+        }
+      wht_warp<U, NI>(x, lane);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < U; ++e) s_slab[r * HD + U * lane + 32 * U * i + e] = x[i][e] * (1.0f / HD);
+    }
+  } else {
+    float4* s4 = reinterpret_cast<float4*>(s_slab);
+    const int n4 = Rc * HD / 4;
+    for (int i4 = threadIdx.x; i4 < n4; i4 += kThreads) {
+      const float4 v0 = s4[i4], v1 = s4[n4 + i4], v2 = s4[2 * n4 + i4], v3 = s4[3 * n4 + i4];
+      s4[i4] = make_float4((v0.x + v1.x) + (v2.x + v3.x), (v0.y + v1.y) + (v2.y + v3.y),
+                           (v0.z + v1.z) + (v2.z + v3.z), (v0.w + v1.w) + (v2.w + v3.w));
+    }
+  }
+  if (threadIdx.x < Rc) {
+    const int r = threadIdx.x;
+    float M = s_wml[r * 2];
+    bool bad = M != M;
+#pragma unroll
+    for (int w = 1; w < kConsumerWarps; ++w) {
+      const float mw = s_wml[(w * RP + r) * 2];
+      bad |= mw != mw;
+      M = fmaxf(M, mw);
+    }
+    float lsum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kConsumerWarps; ++w)
+      lsum = fmaf(s_wml[(w * RP + r) * 2 + 1], fast_exp2(s_wml[(w * RP + r) * 2] - M), lsum);
+    s_fin[r] = make_float2(bad ? __int_as_float(0x7fc00000) : M, lsum);
+  }
+  __syncthreads();
+  const uint32_t n_cta = 1u << a.c_log2, rank = blockIdx.x & (n_cta - 1u);
+  if (n_cta > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+  const uint32_t fin = smem_u32(s_fin), slab = smem_u32(s_slab);
+  auto peer_addr = [](uint32_t addr, uint32_t peer) -> uint32_t {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(peer));
+    return r;
+  };
+  // the cluster's threads share the row tile's float4 columns
+  for (int i4 = (int)rank * kThreads + (int)threadIdx.x; i4 < Rc * HD / 4; i4 += (int)n_cta * kThreads) {
+    const int r = i4 / (HD / 4);
+    float M = -INFINITY, lam = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool bad = false;
+    constexpr int B = 4;   // peers whose loads are in flight together
+    for (uint32_t j0 = 0; j0 < n_cta; j0 += B) {
+      float2 ml[B];
+      float4 v[B];
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const uint32_t j = min(j0 + u, n_cta - 1u);
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(ml[u].x), "=f"(ml[u].y)
+                     : "r"(peer_addr(fin + 8 * r, j)));
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[u].x), "=f"(v[u].y), "=f"(v[u].z), "=f"(v[u].w)
+                     : "r"(peer_addr(slab + 16 * i4, j)));
+        if (j0 + u >= n_cta) ml[u] = make_float2(-INFINITY, 0.f);
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        bad |= ml[u].x != ml[u].x;
+        top = fmaxf(top, ml[u].x);
+      }
+      const float keep = M == -INFINITY ? 0.f : fast_exp2(M - top);
+      acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+      lam *= keep;
+#pragma unroll
+      for (int u = 0; u < B; ++u) {
+        const float w = ml[u].y > 0.f ? fast_exp2(ml[u].x - top) : 0.f;
+        if (w > 0.f) {
+          acc.x = fmaf(w, v[u].x, acc.x);
+          acc.y = fmaf(w, v[u].y, acc.y);
+          acc.z = fmaf(w, v[u].z, acc.z);
+          acc.w = fmaf(w, v[u].w, acc.w);
+          lam = fmaf(w, ml[u].y, lam);
+        }
+      }
+      M = top;
+    }
+    const float inv = lam > 0.f ? 1.f / lam : 0.f;   // (no cell: 0)
+    float4 res = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (bad) {
+      const float nan = __int_as_float(0x7fc00000);
+      res = make_float4(nan, nan, nan, nan);
+    }
+    reinterpret_cast<float4*>(a.out + ((size_t)list * a.G + r0) * HD)[i4] = res;
+  }
+  if (n_cta > 1) {   // the peers may still read this CTA's rows
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+// ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
 // HL (at most 4 query rows, NT = 1): the MMA's 8 columns carry the hi
@@ -320,24 +447,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   // (a verify window wider than one CTA's accumulators), one CTA each; the
   // CTAs of an item are neighbours in the grid, so all but the first find
   // the item's K/V tiles in L2.
-  const int item = (int)fdiv(blockIdx.x, a.div_nrt);
-  const int r0 = ((int)blockIdx.x - item * a.n_rt) * a.RT;  // first query row of this CTA
+  // (block lists in clusters: the CTAs of a cluster are the splits of one row
+  // tile)
+  const bool clustered = kLists && a.c_log2 >= 0;
+  const int tile_id = clustered ? (int)(blockIdx.x >> a.c_log2) : (int)blockIdx.x;
+  const int item = (int)fdiv((unsigned)tile_id, a.div_nrt);
+  const int r0 = (tile_id - item * a.n_rt) * a.RT;          // first query row of this CTA
   const int Rc = min(a.RT, a.R - r0);                         // and its row count
   int b, kvh, split;
   int L_raw = 0;
-  const bool single = a.n_seq == 1;
-  if (single) {
+  // (lists too: their block ids are copied ahead of the length, -1 past the end)
+  const bool single = kLists || a.n_seq == 1;
+  if (single && !kLists) {
     b = 0;
     split = (int)fdiv((unsigned)item, a.div_nkv);
     kvh = item - split * a.n_kv;
     L_raw = __ldg(a.ctx_lens);
   } else if (kLists) {
     // block lists: split-major, no search (the lists are about equally long)
-    split = (int)fdiv((unsigned)item, a.div_nseq);
-    b = item - split * a.n_seq;
+    split = clustered ? (int)(blockIdx.x & ((1u << a.c_log2) - 1u)) : (int)fdiv((unsigned)item, a.div_nseq);
+    b = clustered ? item : item - split * a.n_seq;
     kvh = 0;
     L_raw = __ldg(a.ctx_lens + b);
-    if (split * a.split_cells >= clamp_len_mma(L_raw, a)) return;
   } else {
     if (!item_of(a, item, b, kvh, split)) return;
     L_raw = __ldg(a.ctx_lens + b);
@@ -349,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   // and the block table
   int c_end = min(clamp_len_mma(single ? INT_MAX : L_raw, a), c_begin + a.split_cells);
   int n_tiles = (c_end - c_begin + kTC - 1) / kTC;
+  if (kLists && n_tiles < 0) n_tiles = 0;   // (an empty split of a cluster)
   const int n_first = n_tiles < C::STAGES ? n_tiles : C::STAGES;   // tiles of the first wave
   const int pc_log2 = a.pool.bs_log2 < 6 ? a.pool.bs_log2 : 6;  // cells per TMA piece
   const int n_pieces = kTC >> pc_log2;
@@ -509,7 +641,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   if (single) {
     c_end = min(L, c_begin + a.split_cells);
     n_tiles = c_end > c_begin ? (c_end - c_begin + kTC - 1) / kTC : 0;
-    if (n_tiles == 0) {
+    // (a cluster's empty splits go through the merge with nothing to add)
+    if (n_tiles == 0 && !clustered) {
       // a split past the context: its slots tell the combine "no cells"
       if (producer && n_first > 0) (void)mbar_wait(bar_full, 0, a.wait_limit);
       const size_t slot0 = (((size_t)b * a.n_kv + kvh) * a.nsplit + split) * a.R;
@@ -1155,6 +1288,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       }
     }
   __syncthreads();
+  if constexpr (kLists) {
+    if (clustered) {
+      merge_cluster<FMT, HD, NT>(a, smem, b, r0, Rc);
+      return;
+    }
+  }
   // this CTA's rows of the split's partial
   const size_t row0 = (((size_t)b * a.n_kv + kvh) * a.nsplit + split) * a.R + r0;
   if constexpr (C::V4) {
@@ -1252,7 +1391,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) combine_partials(DecodeArg
   const int d = d0 + 4 * dv;
   // one sequence: every split slot is written (splits past the context say
   // "no cells"), so the context length need not be read
-  const int nlive = a.n_seq == 1 ? a.nsplit
+  const int nlive = !kLists && a.n_seq == 1 ? a.nsplit
                                  : (int)fdiv((unsigned)(clamp_len_mma(__ldg(a.ctx_lens + b), a) +
                                                         a.split_cells - 1),
                                              a.div_split);
@@ -1426,6 +1565,10 @@ int ctas_per_sm_impl() {
     if (cudaFuncSetAttribute(decode_mma<FMT, HD, NT, HL>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
       return false;
+    // clusters of 16 are past the portable 8
+    if (kLists && cudaFuncSetAttribute(decode_mma<FMT, HD, NT, HL>,
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return false;
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma<FMT, HD, NT, HL>, kThreads,
                                                       C::SMEM) != cudaSuccess)
@@ -1455,11 +1598,19 @@ cudaError_t launch_impl(const DecodePlan& p, const DecodeArgs& a, cudaStream_t s
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (kLists && a.c_log2 >= 0) {   // no partials, no combine
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1u << a.c_log2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, decode_mma<FMT, HD, NT, HL>, maps, a);
+  }
   cudaError_t e = cudaLaunchKernelEx(&cfg, decode_mma<FMT, HD, NT, HL>, maps, a);
   if (e != cudaSuccess) return e;
   return launch_combine<HD>(a, s);

@@ -128,6 +128,7 @@ struct DecodePlan {
   int split_cells;     // cells per split (a multiple of the cell tile)
   int nsplit;          // splits per (sequence, KV head), one partial each
   size_t off_o, off_ml, bytes;  // workspace layout
+  int c_log2;          // block lists: see DecodeArgs
 };
 
 // Division of a 32-bit x by a divisor d fixed per call: q = x / d is the
@@ -162,6 +163,8 @@ struct DecodeArgs {
   // place in the pool is the sequence's index mod the pool's KV heads.
   int n_kv;            // KV heads per "sequence": pool.n_kv, or 1
   FastDiv div_heads, div_nseq;  // pool.n_kv, n_seq (block lists)
+  int c_log2;          // block lists: 2^c_log2 splits in a cluster, merged there; -1:
+                       // splits through the workspace and the combine
   const float* q;      // [n_seq][W][n_q][hd]
   float* out;          // [n_seq][W][n_q][hd]
   const int32_t* ctx_lens;
