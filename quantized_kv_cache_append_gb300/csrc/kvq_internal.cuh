@@ -254,6 +254,7 @@ struct SelectArgs {
   int n_sel, n_first, n_last;
   int wg_tok, n_wg;            // tokens per cluster, clusters per (sequence, KV head)
   int cluster, c_log2, lead_rows;  // CTAs per cluster (a power of two), tokens each of them leads
+  int order;                   // clusters start with the longer sequences
   int wide;                    // 512 threads a CTA instead of 256
   int gp_log2;                 // query rows of a token, padded to a power of two
 };

@@ -41,6 +41,7 @@
 namespace kvq {
 namespace {
 
+constexpr int kOrderRegs = 4;               // up to 128 sequences are ordered by length
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kForced = 0xffffffffu;   // keys: 0 not a candidate, kForced always kept
 
@@ -72,13 +73,6 @@ __device__ __forceinline__ uint32_t cta_rank() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ void store_remote(uint32_t addr, uint32_t rank, uint32_t v) {
-  asm volatile(
-      "{\n .reg .b32 ra;\n mapa.shared::cluster.u32 ra, %0, %1;\n st.shared::cluster.u32 [ra], %2;\n}\n" ::"r"(addr),
-      "r"(rank), "r"(v)
-      : "memory");
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -457,9 +451,35 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
   int id = blockIdx.x / C;
   const int wg = id % a.n_wg;
   id /= a.n_wg;
-  const int h = id % a.n_kv, b = id / a.n_kv;
+  const int h = id % a.n_kv;
+  int b = id / a.n_kv, len_raw;
+  if (a.order) {
+    // Sequences of at least half of max_ctx go first, then those of at least
+    // a quarter: clusters start roughly in order, and short rows fill the
+    // end of the launch (64 ragged sequences: 79 -> 74 us).
+    const int rank_b = b;
+    const long long most = (long long)a.n_cap << a.bs_log2;
+    int v[kOrderRegs], base = 0;
+#pragma unroll
+    for (int i = 0; i < kOrderRegs; ++i) v[i] = lane + 32 * i < a.n_seq ? __ldg(a.ctx_lens + lane + 32 * i) : 0;
+    len_raw = 0;
+#pragma unroll 1
+    for (int c = 0; c < 3; ++c)
+#pragma unroll
+      for (int i = 0; i < kOrderRegs; ++i) {
+        const int cls = 2LL * v[i] >= most ? 0 : 4LL * v[i] >= most ? 1 : 2;
+        const unsigned m = __ballot_sync(kAll, lane + 32 * i < a.n_seq && cls == c);
+        const unsigned hit = __ballot_sync(kAll, ((m >> lane) & 1u) && base + __popc(m & ((1u << lane) - 1u)) == rank_b);
+        if (hit) {
+          b = 32 * i + __ffs(hit) - 1;
+          len_raw = __shfl_sync(kAll, v[i], b & 31);
+        }
+        base += __popc(m);
+      }
+  } else {
+    len_raw = __ldg(a.ctx_lens + b);
+  }
   const int w0 = wg * a.wg_tok, nw = min(a.wg_tok, a.W - w0);
-  const int len_raw = __ldg(a.ctx_lens + b);
   // the query rows: a warp per (padded row, 64 dims), two dims a lane
   constexpr int QPW = (NT * 8 * NG + kSelWarps - 1) / kSelWarps;
   float2 qv[QPW];
@@ -491,24 +511,32 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
     return s0 + (lane & 15) < j1 ? __ldg(table + s0 + (lane & 15)) : -1;
   };
   // A lane's loads of group q of a strip: dims 16 t .. + 15 of blocks g and
-  // g + 8, lo and hi.  Foreign blocks read as zeros.
+  // g + 8, lo and hi.  A foreign block reads block 0 (it gets no key).
   struct Unit {
     uint4 lo[2], hi[2];
     float ks[2];
   };
-  auto load_unit = [&](int ids, int gq, Unit& u) {
+  struct Rows {
+    const int8_t* bound[2];
+    const float* scale[2];
+  };
+  auto rows_of = [&](int ids) -> Rows {
+    Rows x;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int blk = __shfl_sync(kAll, ids, g + 8 * i);
-      u.lo[i] = u.hi[i] = make_uint4(0, 0, 0, 0);
-      u.ks[i] = 0.f;
-      if (blk >= 0 && blk < a.n_blocks) {
-        const size_t row = (size_t)blk * a.n_kv + h;
-        const int8_t* src = a.bounds + row * 2 * HD + gq * kGroup + t * 16;
-        u.lo[i] = __ldg(reinterpret_cast<const uint4*>(src));
-        u.hi[i] = __ldg(reinterpret_cast<const uint4*>(src + HD));
-        u.ks[i] = __ldg(a.scales + row * NG + gq);
-      }
+      const size_t row = (size_t)((unsigned)blk < (unsigned)a.n_blocks ? blk : 0) * a.n_kv + h;
+      x.bound[i] = a.bounds + row * 2 * HD + t * 16;
+      x.scale[i] = a.scales + row * NG;
+    }
+    return x;
+  };
+  auto load_unit = [&](const Rows& x, int gq, Unit& u) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u.lo[i] = __ldg(reinterpret_cast<const uint4*>(x.bound[i] + gq * kGroup));
+      u.hi[i] = __ldg(reinterpret_cast<const uint4*>(x.bound[i] + gq * kGroup + HD));
+      u.ks[i] = __ldg(x.scale[i] + gq);
     }
   };
   const int first = j0 + warp * STRIP;
@@ -535,8 +563,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
     if (lane == 0) s_scale[r * NG + gq] = pow2f_exact(e);
   }
   Unit unit[DEPTH];
+  Rows rows = rows_of(ids);
 #pragma unroll
-  for (int q = 0; q < DEPTH; ++q) load_unit(ids, q, unit[q]);
+  for (int q = 0; q < DEPTH; ++q) load_unit(rows, q, unit[q]);
   __syncthreads();
 
   const uint32_t keys_addr = static_cast<uint32_t>(__cvta_generic_to_shared(s_keys));
@@ -553,15 +582,31 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
         for (int which = 0; which < 2; ++which) breg[q][kk][which] = b_frag(0, q, kk, which);
   }
   const int gp = 1 << a.gp_log2;
-  // the key of block j for token w
-  auto emit = [&](int w, int j, int blk, float best) {
-    if (w >= nw || j >= j1) return;
-    const int nb = blocks_of(visible(w));
+  // The tokens whose keys this lane writes, from column c = 0 (and, one row a
+  // token, 1) of each n-tile: the blocks they see (0: not this lane's to
+  // write) and where their keys go.
+  constexpr int TOKS = 2;
+  int tok_nb[NT][TOKS];
+  uint32_t tok_at[NT][TOKS];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int c = 0; c < TOKS; ++c) {
+      const int row = nt * 8 + 2 * t + c, w = row >> a.gp_log2, lead_row = w >> a.c_log2;
+      // (more than 8 rows a token: written at its last n-tile)
+      const bool mine = gp <= 8 ? (row & (gp - 1)) == 0 : t == 0 && c == 0 && ((nt * 8 + 8) & (gp - 1)) == 0;
+      tok_nb[nt][c] = mine && w < nw ? blocks_of(visible(w)) : 0;
+      const uint32_t at = keys_addr + (uint32_t)(lead_row * key_row(a.n_cap)) * 4u;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;"
+          : "=r"(tok_at[nt][c])
+          : "r"(at), "r"((uint32_t)(w - (lead_row << a.c_log2)) & (uint32_t)(C - 1)));
+    }
+  auto emit = [&](int nt, int c, int j, bool valid, float best) {
+    const int nb = tok_nb[nt][c];
+    if (nb == 0 || j >= j1) return;
     uint32_t key = 0;
-    if (j < nb && blk >= 0 && blk < a.n_blocks)
-      key = (j < a.n_first || j >= nb - a.n_last) ? kForced : ordered(best);
-    const int row = w >> a.c_log2;
-    store_remote(keys_addr + (uint32_t)(row * key_row(a.n_cap) + j) * 4u, (uint32_t)(w - (row << a.c_log2)), key);
+    if (j < nb && valid) key = (j < a.n_first || j >= nb - a.n_last) ? kForced : ordered(best);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tok_at[nt][c] + 4u * (uint32_t)j), "r"(key) : "memory");
   };
 
   __syncwarp();
@@ -570,6 +615,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
     const int ids_cur = ids;
     ids = ids_next;
     ids_next = load_ids(s0 + 2 * STEP);
+    const Rows rows_cur = rows;
+    rows = rows_of(ids);
     float z[NT][4], z2[NG == 4 ? NT : 1][4];   // score sums: blocks g (0, 1), g + 8 (2, 3), rows 2t, 2t + 1
 #pragma unroll
     for (int q = 0; q < NG; ++q) {
@@ -603,8 +650,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
       }
       const float ks0 = u.ks[0], ks1 = u.ks[1];
       // the unit DEPTH further on, of this strip or the next
-      if (q + DEPTH < NG) load_unit(ids_cur, q + DEPTH, u);
-      else load_unit(ids, q + DEPTH - NG, u);
+      if (q + DEPTH < NG) load_unit(rows_cur, q + DEPTH, u);
+      else load_unit(rows, q + DEPTH - NG, u);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -622,49 +669,35 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
         }
     }
     // the largest over a token's rows, then its keys
-    const int blk0 = __shfl_sync(kAll, ids_cur, g), blk1 = __shfl_sync(kAll, ids_cur, g + 8);
+    const bool va = (unsigned)__shfl_sync(kAll, ids_cur, g) < (unsigned)a.n_blocks;
+    const bool vb = (unsigned)__shfl_sync(kAll, ids_cur, g + 8) < (unsigned)a.n_blocks;
     const int ja = s0 + g, jb = s0 + g + 8;
     if (gp == 1) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          emit(nt * 8 + 2 * t + c, ja, blk0, z[nt][c]);
-          emit(nt * 8 + 2 * t + c, jb, blk1, z[nt][2 + c]);
+          emit(nt, c, ja, va, z[nt][c]);
+          emit(nt, c, jb, vb, z[nt][2 + c]);
         }
-    } else if (gp <= 8) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float m0 = fmaxf(z[nt][0], z[nt][1]), m1 = fmaxf(z[nt][2], z[nt][3]);
-        for (int o = 1; 2 * o < gp; o <<= 1) {
-          m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, o));
-          m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, o));
-        }
-        if (((2 * t) & (gp - 1)) == 0) {
-          const int w = (nt * 8 + 2 * t) >> a.gp_log2;
-          emit(w, ja, blk0, m0);
-          emit(w, jb, blk1, m1);
-        }
-      }
-    } else {   // 16 or 32 rows a token: 2 or 4 n-tiles
+    } else {
       float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         m0 = fmaxf(m0, fmaxf(z[nt][0], z[nt][1]));
         m1 = fmaxf(m1, fmaxf(z[nt][2], z[nt][3]));
-        if (((nt * 8 + 8) & (gp - 1)) == 0) {
-#pragma unroll
-          for (int o = 1; o < 4; o <<= 1) {
-            m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, o));
-            m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, o));
-          }
-          if (t == 0) {
-            const int w = (nt * 8) >> a.gp_log2;
-            emit(w, ja, blk0, m0);
-            emit(w, jb, blk1, m1);
-          }
-          m0 = m1 = -INFINITY;
+        if (gp > 8 && ((nt * 8 + 8) & (gp - 1)) != 0) continue;   // (the token goes on)
+        if (gp >= 4) {
+          m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, 1));
+          m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, 1));
         }
+        if (gp >= 8) {
+          m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, 2));
+          m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, 2));
+        }
+        emit(nt, 0, ja, va, m0);
+        emit(nt, 0, jb, vb, m1);
+        m0 = m1 = -INFINITY;
       }
     }
   }
@@ -762,6 +795,7 @@ bool plan_select(int hd, int sms, SelectArgs* a) {
     a->cluster = 1 << c;
     // 512 threads where every CTA has an SM to itself and rows are long (4096
     // blocks x 8 heads x 4 tokens 14.6 -> 12.7 us, 16384 x 2 40 -> 29 us)
+    a->order = a->n_seq > 1 && a->n_seq <= 32 * kOrderRegs && (clusters << c) > 2 * sms;
     a->wide = a->n_cap >= 2048 && (clusters << c) <= sms;
     a->lead_rows = (a->wg_tok + a->cluster - 1) >> c;
     if (sel_smem(hd, n_tiles(*a), a->lead_rows, a->n_cap).bytes <= kSelMaxSmem) return true;
