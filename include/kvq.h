@@ -599,6 +599,20 @@ kvq_status kvq_sparse_decode_attn(const kvq_cache *cache, const float *q, int n_
                                   float sm_scale, float *out, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/*
+ * kvq_sparse_decode_attn with the failure path of its copy waits exercised,
+ * for tests of that path only, as kvq_decode_attn_lost_wait_test does: every
+ * wait runs out, and a correct failure path returns KVQ_OK with NaN in
+ * every output row of a list with cells, whether its splits meet through
+ * the workspace or in a cluster.
+ */
+kvq_status kvq_sparse_decode_attn_lost_wait_test(const kvq_cache *cache, const float *q, int n_seq,
+                                                 int W, int n_q, const int32_t *sel_blocks,
+                                                 const int32_t *sel_lens, int n_sel, float sm_scale,
+                                                 float *out, void *workspace,
+                                                 size_t workspace_bytes, uint32_t wait_limit,
+                                                 uint32_t extra_tx_bytes, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *kvq_status_string(int status);
 

@@ -55,6 +55,7 @@ EXPORTED_SYMBOLS = (
     "kvq_select_blocks",
     "kvq_sparse_workspace_bytes",
     "kvq_sparse_decode_attn",
+    "kvq_sparse_decode_attn_lost_wait_test",
     "kvq_status_string",
 )
 
@@ -139,6 +140,9 @@ def load_library(path: Optional[str] = None):
     lib.kvq_sparse_workspace_bytes.argtypes = [CP, I, I, I, I]
     lib.kvq_sparse_decode_attn.restype = I
     lib.kvq_sparse_decode_attn.argtypes = [CP, P, I, I, I, P, P, I, ctypes.c_float, P, P, Z, P]
+    lib.kvq_sparse_decode_attn_lost_wait_test.restype = I
+    lib.kvq_sparse_decode_attn_lost_wait_test.argtypes = [CP, P, I, I, I, P, P, I, ctypes.c_float, P,
+                                                          P, Z, ctypes.c_uint32, ctypes.c_uint32, P]
     lib.kvq_status_string.restype = ctypes.c_char_p
     lib.kvq_status_string.argtypes = [I]
     if path is None:
@@ -327,6 +331,16 @@ def kvq_sparse_decode_attn(cache: kvq_cache, q, n_seq: int, W: int, n_q: int, se
     return load_library().kvq_sparse_decode_attn(
         ctypes.byref(cache), _ptr(q), n_seq, W, n_q, _ptr(sel_blocks), _ptr(sel_lens), n_sel,
         float(sm_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def kvq_sparse_decode_attn_lost_wait_test(cache: kvq_cache, q, n_seq: int, W: int, n_q: int,
+                                          sel_blocks, sel_lens, n_sel: int, sm_scale: float, out,
+                                          workspace, workspace_bytes: int, wait_limit: int,
+                                          extra_tx_bytes: int, stream=None) -> int:
+    return load_library().kvq_sparse_decode_attn_lost_wait_test(
+        ctypes.byref(cache), _ptr(q), n_seq, W, n_q, _ptr(sel_blocks), _ptr(sel_lens), n_sel,
+        float(sm_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), wait_limit,
+        extra_tx_bytes, _stream(stream))
 
 
 def kvq_status_string(status: int) -> str:

@@ -347,11 +347,13 @@ KVQ_API size_t kvq_sparse_workspace_bytes(const kvq_cache* cache, int n_seq, int
   return p.bytes;
 }
 
-KVQ_API kvq_status kvq_sparse_decode_attn(const kvq_cache* cache, const float* q, int n_seq, int W,
-                                          int n_q, const int32_t* sel_blocks,
-                                          const int32_t* sel_lens, int n_sel, float sm_scale,
-                                          float* out, void* workspace, size_t workspace_bytes,
-                                          void* stream) {
+namespace kvq {
+namespace {
+
+kvq_status sparse_impl(const kvq_cache* cache, const float* q, int n_seq, int W, int n_q,
+                       const int32_t* sel_blocks, const int32_t* sel_lens, int n_sel, float sm_scale,
+                       float* out, void* workspace, size_t workspace_bytes, void* stream,
+                       uint32_t wait_limit = kDefaultWaitLimit, uint32_t extra_tx = 0) {
   kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
   ListShape ls;
@@ -393,11 +395,35 @@ KVQ_API kvq_status kvq_sparse_decode_attn(const kvq_cache* cache, const float* q
   a.split_cells = plan.split_cells;
   a.nsplit = plan.nsplit;
   a.qscale = sm_scale * 1.4426950408889634f;  // log2(e)
-  a.wait_limit = kDefaultWaitLimit;
-  a.extra_tx = 0;
+  a.wait_limit = wait_limit;
+  a.extra_tx = extra_tx;
   const cudaError_t e =
       launch_decode_lists(cache->fmt, cache->head_dim, plan, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace kvq
+
+KVQ_API kvq_status kvq_sparse_decode_attn(const kvq_cache* cache, const float* q, int n_seq, int W,
+                                          int n_q, const int32_t* sel_blocks,
+                                          const int32_t* sel_lens, int n_sel, float sm_scale,
+                                          float* out, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+  return kvq::sparse_impl(cache, q, n_seq, W, n_q, sel_blocks, sel_lens, n_sel, sm_scale, out, workspace,
+                          workspace_bytes, stream);
+}
+
+KVQ_API kvq_status kvq_sparse_decode_attn_lost_wait_test(const kvq_cache* cache, const float* q, int n_seq,
+                                                         int W, int n_q, const int32_t* sel_blocks,
+                                                         const int32_t* sel_lens, int n_sel,
+                                                         float sm_scale, float* out, void* workspace,
+                                                         size_t workspace_bytes, uint32_t wait_limit,
+                                                         uint32_t extra_tx_bytes, void* stream) {
+  if (wait_limit == 0 || wait_limit > kDefaultWaitLimit) return KVQ_ERR_ARG;
+  if (extra_tx_bytes == 0 || extra_tx_bytes > 4096 || extra_tx_bytes % 16 != 0) return KVQ_ERR_ARG;
+  return kvq::sparse_impl(cache, q, n_seq, W, n_q, sel_blocks, sel_lens, n_sel, sm_scale, out, workspace,
+                          workspace_bytes, stream, wait_limit, extra_tx_bytes);
 }
 
 namespace kvq {

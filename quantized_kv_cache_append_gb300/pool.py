@@ -10,7 +10,7 @@ import contextlib
 
 import torch
 
-from . import (KVQ_F16, KVQ_GROUP, KVQ_K8V4, KVQ_Q4_BLOCK, KVQ_Q8, check, kvq_append,
+from . import (KVQ_ERR_ARG, KVQ_F16, KVQ_GROUP, KVQ_K8V4, KVQ_Q4_BLOCK, KVQ_Q8, KvqError, check, kvq_append,
                kvq_bound_blocks, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
                kvq_select_blocks, kvq_sparse_decode_attn, kvq_sparse_workspace_bytes, make_cache)
 
@@ -113,12 +113,38 @@ class PagedPool:
                   "kvq_compact_f16")
         return out_k, out_v
 
+    def _check(self, where: str, **tensors) -> None:
+        """Each given (tensor, dtype, shape) is contiguous on the pool's device;
+        None in a shape stands for any size, a tensor of None is left out."""
+        for name, (t, dtype, shape) in tensors.items():
+            if t is None:
+                continue
+            if (t.dtype != dtype or t.device != self.k.device or not t.is_contiguous()
+                    or t.dim() != len(shape)
+                    or any(w is not None and n != w for n, w in zip(t.shape, shape))):
+                raise KvqError(KVQ_ERR_ARG, f"{where}: {name} must be a contiguous {dtype} tensor of "
+                                            f"shape {shape} on {self.k.device}")
+
+    @contextlib.contextmanager
+    def _on(self, stream):
+        """The pool's device, and the stream the call runs on."""
+        with torch.cuda.device(self.k.device), on_stream(stream):
+            yield
+
     def bound(self, bounds: BlockBounds, block_table, ctx_lens, max_new: int, ctx_start=None,
               stream=None) -> None:
         """Bounds of the blocks that cells [ctx_start, ctx_lens) touch (None: from 0)."""
-        check(kvq_bound_blocks(self.cache, block_table, int(block_table.shape[0]),
-                               int(block_table.shape[1]), ctx_start, ctx_lens, max_new,
-                               bounds.codes, bounds.scales, stream), "kvq_bound_blocks")
+        n_seq = block_table.shape[0]
+        i32 = torch.int32
+        self._check("bound", block_table=(block_table, i32, (None, None)),
+                    ctx_lens=(ctx_lens, i32, (n_seq,)), ctx_start=(ctx_start, i32, (n_seq,)),
+                    codes=(bounds.codes, torch.int8, (self.n_blocks, self.n_kv, 2, self.head_dim)),
+                    scales=(bounds.scales, torch.float32,
+                            (self.n_blocks, self.n_kv, self.head_dim // KVQ_GROUP)))
+        with self._on(stream):
+            check(kvq_bound_blocks(self.cache, block_table, n_seq, int(block_table.shape[1]), ctx_start,
+                                   ctx_lens, max_new, bounds.codes, bounds.scales, stream),
+                  "kvq_bound_blocks")
 
     def select(self, bounds: BlockBounds, q, ctx_lens, max_ctx: int, block_table, n_sel: int,
                n_first: int = 1, n_last: int = 1, out=None, stream=None):
@@ -126,12 +152,17 @@ class PagedPool:
         their indexes in the sequence) [n_seq][W][n_kv][n_sel] and the lists'
         cells [n_seq][W][n_kv]."""
         n_seq, W, n_q, hd = q.shape
-        with on_stream(stream):
+        i32, lists = torch.int32, (n_seq, W, self.n_kv, n_sel)
+        with self._on(stream):
             if out is None:
-                new = lambda *s: torch.empty(s, dtype=torch.int32, device=q.device)
-                out = (new(n_seq, W, self.n_kv, n_sel), new(n_seq, W, self.n_kv, n_sel),
-                       new(n_seq, W, self.n_kv))
+                new = lambda *s: torch.empty(s, dtype=i32, device=q.device)
+                out = (new(*lists), new(*lists), new(*lists[:3]))
             blocks, index, lens = out
+            self._check("select", q=(q, torch.float32, (n_seq, W, n_q, self.head_dim)),
+                        ctx_lens=(ctx_lens, i32, (n_seq,)), block_table=(block_table, i32, (n_seq, None)),
+                        codes=(bounds.codes, torch.int8, (self.n_blocks, self.n_kv, 2, hd)),
+                        scales=(bounds.scales, torch.float32, (self.n_blocks, self.n_kv, hd // KVQ_GROUP)),
+                        blocks=(blocks, i32, lists), index=(index, i32, lists), lens=(lens, i32, lists[:3]))
             check(kvq_select_blocks(self.cache, bounds.codes, bounds.scales, q, n_seq, W, n_q,
                                     ctx_lens, max_ctx, block_table, int(block_table.shape[1]),
                                     n_sel, n_first, n_last, blocks, index, lens, stream),
@@ -143,12 +174,17 @@ class PagedPool:
         """decode over a list of blocks for each (token, KV head)."""
         n_seq, W, n_q, hd = q.shape
         n_sel = int(sel_blocks.shape[-1])
-        with on_stream(stream):
+        f32, i32 = torch.float32, torch.int32
+        with self._on(stream):
             if out is None:
                 out = torch.empty_like(q)
             if workspace is None:
                 need = kvq_sparse_workspace_bytes(self.cache, n_seq, W, n_q, n_sel)
                 workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+            self._check("decode_selected", q=(q, f32, (n_seq, W, n_q, self.head_dim)),
+                        sel_blocks=(sel_blocks, i32, (n_seq, W, self.n_kv, n_sel)),
+                        sel_lens=(sel_lens, i32, (n_seq, W, self.n_kv)), out=(out, f32, (n_seq, W, n_q, hd)),
+                        workspace=(workspace, torch.uint8, (None,)))
             check(kvq_sparse_decode_attn(self.cache, q, n_seq, W, n_q, sel_blocks, sel_lens, n_sel,
                                          sm_scale, out, workspace, workspace.numel(), stream),
                   "kvq_sparse_decode_attn")

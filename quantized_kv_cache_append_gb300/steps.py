@@ -45,9 +45,11 @@ class StepPlanner:
         """n_new int32 [n_seq] on the device: tokens each sequence gets;
         negative: it ends and gives its blocks back.  A step that cannot be
         placed changes nothing and says why in info[3]."""
-        if n_new.shape != (self.n_seq,) or n_new.dtype != torch.int32 or not n_new.is_contiguous():
-            raise KvqError(KVQ_ERR_ARG, "StepPlanner.plan: n_new must be a contiguous int32 [n_seq]")
-        with on_stream(stream):
+        if (n_new.shape != (self.n_seq,) or n_new.dtype != torch.int32 or not n_new.is_contiguous()
+                or n_new.device != self.info.device):
+            raise KvqError(KVQ_ERR_ARG, "StepPlanner.plan: n_new must be a contiguous int32 [n_seq] on "
+                                        f"{self.info.device}")
+        with torch.cuda.device(self.info.device), on_stream(stream):
             self._before.copy_(self._after)
             check(kvq_plan_step(self.ctx_start, n_new, self.n_seq, self.block_size, self.n_blocks,
                                 self.block_table, self.max_blocks, self.free_list, self._count_in,

@@ -220,6 +220,43 @@ def test_selection_over_the_longest_row():
     check_select(codes, scales, q, [n * bs], table, bs, n_blocks, n + 5, 1, 4)      # every block
 
 
+def test_selection_over_the_longest_row_of_many_wide_query_heads():
+    rng = np.random.default_rng(18)
+    bs, n = 16, 32768
+    table, n_blocks = tables(rng, [n * bs - 5], bs)
+    codes, scales = random_bounds(rng, n_blocks, 1, 256)
+    check_select(codes, scales, queries(rng, 1, 3, 32, 256), [n * bs - 5], table, bs, n_blocks, 77, 0, 2)
+
+
+def test_selection_orders_a_ragged_batch_without_mixing_it_up():
+    # clusters start with the longer sequences when a batch takes several
+    # waves: 70 and 129 sequences, empty and full ones among them
+    rng = np.random.default_rng(19)
+    bs = 16
+    for n_seq, n_kv in ((70, 8), (129, 4)):
+        lens = rng.integers(0, 1500, n_seq)
+        lens[[0, 5, n_seq - 1]] = 0, 1500, 1
+        lens[10:14] = [750, 749, 375, 374]      # on the classes' borders
+        table, n_blocks = tables(rng, lens, bs)
+        codes, scales = random_bounds(rng, n_blocks, n_kv, 64)
+        check_select(codes, scales, queries(rng, n_seq, 1, n_kv, 64), lens, table, bs, n_blocks, 9, 1, 1)
+
+
+def test_whole_number_sums_at_their_largest():
+    # every product 127 * 127, all of one sign, and sums that differ by one
+    bs, n, hd = 16, 64, 256
+    codes = np.full((n, 1, 2, hd), 127, np.int8)
+    codes[:, :, 0] = -127
+    scales = np.full((n, 1, hd // 64), 2.0 ** -3, np.float32)
+    for j in range(n):          # block j is short of the largest sum by j % 5 products' units
+        codes[j, 0, 1, :j % 5] = 126
+    q = np.full((1, 2, 2, hd), 127.0, np.float32)
+    q[0, 1, :, ::2] = -127.0
+    table = np.arange(n, dtype=np.int32)[None]
+    for n_sel in (1, 12, 13, 26, 40):
+        check_select(codes, scales, q, [n * bs], table, bs, n, n_sel, 0, 0)
+
+
 def test_equal_scores_go_to_the_lower_block():
     rng = np.random.default_rng(5)
     bs, n = 16, 1000
@@ -380,6 +417,74 @@ def test_attention_over_every_block_is_the_dense_decode():
         torch.cuda.synchronize()
         rel = ((a - b).norm() / b.norm()).item()
         assert rel < 4e-5      # two sums within the bounds of the attention tests
+
+
+def clustered(p, n_seq, W, n_q, n_sel):
+    """Whether a call's splits meet in clusters (it needs no partials then)."""
+    return kvq.kvq_sparse_workspace_bytes(p.cache, n_seq, W, n_q, n_sel) == 256
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8", "k8v4"])
+@pytest.mark.parametrize("hd,G,bs", [(64, 4, 16), (128, 4, 16), (128, 8, 64), (256, 4, 16), (256, 32, 16)])
+def test_attention_with_splits_through_clusters_and_through_the_workspace(fmt, hd, G, bs):
+    # few lists and many: splits through the workspace, in clusters of
+    # several sizes, and one split each; lists of every length, most splits of
+    # the short ones empty
+    rng = np.random.default_rng(hd + G)
+    n_sel, n_kv, n_blocks = 512 // bs, 2, 40
+    p, h = fill_pool(rng, fmt, n_blocks, n_kv, bs, hd)
+    seen = set()
+    for n_seq in (1, 20, 37, 75, 151, 310):
+        n_q = n_kv * G
+        seen.add(clustered(p, n_seq, 1, n_q, n_sel))
+        if G == 32 and n_seq > 75:
+            continue
+        q = queries(rng, n_seq, 1, n_q, hd)
+        blocks, lens = random_lists(rng, n_seq, 1, n_kv, n_sel, n_blocks, bs)
+        check_attention(rng, fmt, p, h, q, blocks, lens)
+    assert seen == {False, True}
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8", "k8v4"])
+def test_lost_copy_waits_give_nan_rows(fmt):
+    # one wave's worth of lists in clusters, and a single one through the
+    # workspace; an ordinary call on the same buffers is right afterwards
+    rng = np.random.default_rng(30)
+    bs, hd, n_kv, G, n_sel = 16, 128, 2, 4, 16
+    p, h = fill_pool(rng, fmt, 20, n_kv, bs, hd)
+    for n_seq in (1, 75, 310):
+        q = queries(rng, n_seq, 1, n_kv * G, hd)
+        blocks, lens = random_lists(rng, n_seq, 1, n_kv, n_sel, 20, bs)
+        lens = np.maximum(lens, 1)
+        out = torch.zeros(q.shape, device="cuda")
+        ws = torch.empty(kvq.kvq_sparse_workspace_bytes(p.cache, n_seq, 1, n_kv * G, n_sel), dtype=torch.uint8,
+                         device="cuda")
+        st = kvq.kvq_sparse_decode_attn_lost_wait_test(p.cache, dev(q), n_seq, 1, n_kv * G, i32(blocks), i32(lens),
+                                                       n_sel, 0.1, out, ws, ws.numel(), 4096, 16)
+        assert st == kvq.KVQ_OK, kvq.kvq_status_string(st)
+        torch.cuda.synchronize()
+        assert torch.isnan(out).all()
+        check_attention(rng, fmt, p, h, q, blocks, lens)
+
+
+def test_methods_refuse_tensors_they_cannot_read():
+    p = PagedPool(kvq.KVQ_F16, 2, 64, 16, 8)
+    bb = BlockBounds(p)
+    q = torch.zeros(1, 1, 4, 64, device="cuda")
+    table, lens = i32([[0, 1, 2]]), i32([40])
+    blocks, index, cells = p.select(bb, q, lens, 40, table, 2)
+    bad_q = torch.zeros(1, 1, 64, 4, device="cuda").transpose(2, 3)
+    for call in (lambda: p.select(bb, bad_q, lens, 40, table, 2), lambda: p.select(bb, q.half(), lens, 40, table, 2),
+                 lambda: p.select(bb, q, lens.long(), 40, table, 2), lambda: p.select(bb, q, lens.cpu(), 40, table, 2),
+                 lambda: p.select(bb, q, lens, 40, table.repeat(2, 1), 2),
+                 lambda: p.bound(bb, table[:, ::2], lens, 40), lambda: p.bound(bb, table, lens, 40, i32([0, 0])),
+                 lambda: p.decode_selected(bad_q, blocks, cells, 0.1),
+                 lambda: p.decode_selected(q, blocks.long(), cells, 0.1),
+                 lambda: p.decode_selected(q, blocks, cells[..., :1], 0.1),
+                 lambda: p.decode_selected(q, blocks, cells, 0.1, workspace=torch.zeros(64, device="cuda")),
+                 lambda: StepPlanner(2, 4, 16, 8, 16).plan(i32([1]))):
+        with pytest.raises(kvq.KvqError):
+            call()
 
 
 # ---------------------------------------------------------------- together
