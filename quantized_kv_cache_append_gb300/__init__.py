@@ -164,6 +164,14 @@ def _ptr(x):
     raise TypeError(f"cannot take the address of {type(x)}")
 
 
+def _ptrs(*xs):
+    """Addresses of several arguments (tensors first: the common case)."""
+    try:
+        return [x.data_ptr() for x in xs]
+    except AttributeError:
+        return [_ptr(x) for x in xs]
+
+
 _current_stream = None   # () -> cudaStream_t of torch's current stream, set on first use
 
 
@@ -297,28 +305,28 @@ def kvq_decode_attn_lost_wait_test(cache: kvq_cache, q, n_seq: int, W: int, n_q:
 def kvq_plan_step(ctx_in, n_new, n_seq: int, block_size: int, n_blocks: int, block_table,
                   max_blocks_per_seq: int, free_list, free_count_in, max_tok: int, ctx_out,
                   tok_start, tok_seq, tok_pos, slots, free_count_out, info, stream=None) -> int:
-    return load_library().kvq_plan_step(
-        _ptr(ctx_in), _ptr(n_new), n_seq, block_size, n_blocks, _ptr(block_table),
-        max_blocks_per_seq, _ptr(free_list), _ptr(free_count_in), max_tok, _ptr(ctx_out),
-        _ptr(tok_start), _ptr(tok_seq), _ptr(tok_pos), _ptr(slots), _ptr(free_count_out),
-        _ptr(info), _stream(stream))
+    a = _ptrs(ctx_in, n_new, block_table, free_list, free_count_in, ctx_out, tok_start, tok_seq,
+              tok_pos, slots, free_count_out, info)
+    return load_library().kvq_plan_step(a[0], a[1], n_seq, block_size, n_blocks, a[2],
+                                        max_blocks_per_seq, a[3], a[4], max_tok, *a[5:],
+                                        _stream(stream))
 
 
 def kvq_bound_blocks(cache: kvq_cache, block_table, n_seq: int, max_blocks_per_seq: int, ctx_start,
                      ctx_lens, max_new: int, bounds, bound_scales, stream=None) -> int:
-    return load_library().kvq_bound_blocks(
-        ctypes.byref(cache), _ptr(block_table), n_seq, max_blocks_per_seq, _ptr(ctx_start),
-        _ptr(ctx_lens), max_new, _ptr(bounds), _ptr(bound_scales), _stream(stream))
+    a = _ptrs(block_table, ctx_start, ctx_lens, bounds, bound_scales)
+    return load_library().kvq_bound_blocks(ctypes.byref(cache), a[0], n_seq, max_blocks_per_seq, a[1],
+                                           a[2], max_new, a[3], a[4], _stream(stream))
 
 
 def kvq_select_blocks(cache: kvq_cache, bounds, bound_scales, q, n_seq: int, W: int, n_q: int,
                       ctx_lens, max_ctx: int, block_table, max_blocks_per_seq: int, n_sel: int,
                       n_first: int, n_last: int, sel_blocks, sel_index, sel_lens,
                       stream=None) -> int:
-    return load_library().kvq_select_blocks(
-        ctypes.byref(cache), _ptr(bounds), _ptr(bound_scales), _ptr(q), n_seq, W, n_q,
-        _ptr(ctx_lens), max_ctx, _ptr(block_table), max_blocks_per_seq, n_sel, n_first, n_last,
-        _ptr(sel_blocks), _ptr(sel_index), _ptr(sel_lens), _stream(stream))
+    a = _ptrs(bounds, bound_scales, q, ctx_lens, block_table, sel_blocks, sel_index, sel_lens)
+    return load_library().kvq_select_blocks(ctypes.byref(cache), a[0], a[1], a[2], n_seq, W, n_q, a[3],
+                                            max_ctx, a[4], max_blocks_per_seq, n_sel, n_first, n_last,
+                                            a[5], a[6], a[7], _stream(stream))
 
 
 def kvq_sparse_workspace_bytes(cache: kvq_cache, n_seq: int, W: int, n_q: int, n_sel: int) -> int:
@@ -328,9 +336,10 @@ def kvq_sparse_workspace_bytes(cache: kvq_cache, n_seq: int, W: int, n_q: int, n
 def kvq_sparse_decode_attn(cache: kvq_cache, q, n_seq: int, W: int, n_q: int, sel_blocks, sel_lens,
                            n_sel: int, sm_scale: float, out, workspace, workspace_bytes: int,
                            stream=None) -> int:
-    return load_library().kvq_sparse_decode_attn(
-        ctypes.byref(cache), _ptr(q), n_seq, W, n_q, _ptr(sel_blocks), _ptr(sel_lens), n_sel,
-        float(sm_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    a = _ptrs(q, sel_blocks, sel_lens, out, workspace)
+    return load_library().kvq_sparse_decode_attn(ctypes.byref(cache), a[0], n_seq, W, n_q, a[1], a[2],
+                                                 n_sel, float(sm_scale), a[3], a[4],
+                                                 int(workspace_bytes), _stream(stream))
 
 
 def kvq_sparse_decode_attn_lost_wait_test(cache: kvq_cache, q, n_seq: int, W: int, n_q: int,

@@ -8,8 +8,8 @@
 // holds exactly, and a division by a power of two does not round.
 //
 // A work item is one (block, KV head): block_size contiguous rows of K.  One
-// warp or the CTA's 8 read it with 16-byte loads, each lane always at the same
-// 16 or 8 dims, the running minima and maxima in registers.  The lanes of the
+// warp or the CTA's 8 read it with 16-byte (int8: 8-byte) loads, each lane
+// always at the same 8 dims, the running minima and maxima in registers.  The lanes of the
 // same dims meet by a halving exchange (each step a lane keeps half of its
 // dims), which leaves HD / 32 consecutive dims a lane; 8 warps meet through
 // shared memory.  CTAs are persistent and fetch the next item's block id
@@ -24,9 +24,10 @@
 // Bound by the read of K.  One GB300: 262144 FP16 cells x 2 heads x 256 dims
 // (268 MB) 44 us, 6.1 TB/s, 90 % of the measured copy rate; the newest block
 // of 16 sequences (8 heads x 128 dims, blocks of 256) 3.4 us, a launch with
-// one dependent chain of loads; 131072 int8 cells x 8 heads in blocks of 64
-// 38 us, 3.7 TB/s, where the 32 running fp32 extremes of a lane leave two
-// CTAs an SM and too few loads in flight.
+// one dependent chain of loads.  131072 int8 cells x 8 heads x 128 dims in
+// blocks of 64 37 us, 3.8 TB/s: 4.2 instructions a code keep the ALU half
+// busy and the loads' latency shows between them (16-byte loads with two
+// CTAs an SM, batches fetched ahead and 2 to 5 CTAs an SM all took 35-45 us).
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>
@@ -104,10 +105,10 @@ __device__ __forceinline__ void halve(T* x, int lane) {
 
 // FMT: KVQ_F16, or KVQ_Q8 for both int8-K formats.  WPI warps per item.
 template <int FMT, int HD, int WPI>
-__global__ void __launch_bounds__(kBoundThreads, FMT == KVQ_F16 ? 5 : 2)
+__global__ void __launch_bounds__(kBoundThreads, FMT == KVQ_F16 ? 5 : 3)
     bound_blocks_kernel(BoundArgs a) {
   constexpr bool I8 = FMT != KVQ_F16;
-  constexpr int VD = I8 ? 16 : 8;         // dims per 16-byte load
+  constexpr int VD = 8;                   // dims per load (16 or 8 bytes)
   constexpr int LPR = HD / VD;            // lanes per row
   constexpr int RPW = 32 / LPR;           // rows a warp reads at once
   constexpr int NG = HD / kGroup;
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kBoundThreads, FMT == KVQ_F16 ? 5 : 2)
         hi[2 * e + 1] = __high2float(mx[e]);
       }
     } else {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(a.pool.k) + row0 * HD) + l;
+      const uint2* src = reinterpret_cast<const uint2*>(static_cast<const int8_t*>(a.pool.k) + row0 * HD) + l;
       const __half* sc = a.pool.ks + row0 * NG + l / LG;
       float mn[VD], mx[VD];
 #pragma unroll
@@ -194,15 +195,15 @@ __global__ void __launch_bounds__(kBoundThreads, FMT == KVQ_F16 ? 5 : 2)
         mn[e] = INFINITY;
         mx[e] = -INFINITY;
       }
-#pragma unroll 2
+#pragma unroll 4
       for (int r = r0; r < it.live; r += 2 * STEP) {
         const int r2 = r + STEP < it.live ? r + STEP : r;
-        const uint4 u = __ldg(src + (size_t)r * LPR), v = __ldg(src + (size_t)r2 * LPR);
+        const uint2 u = __ldg(src + (size_t)r * LPR), v = __ldg(src + (size_t)r2 * LPR);
         const float su = __half2float(__ldg(sc + (size_t)r * NG)), sv = __half2float(__ldg(sc + (size_t)r2 * NG));
         const float tu = -32896.0f * su, tv = -32896.0f * sv;
-        const uint32_t wu[4] = {u.x, u.y, u.z, u.w}, wv[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t wu[2] = {u.x, u.y}, wv[2] = {v.x, v.y};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           float x[4], y[4];
           widen4(wu[e], su, tu, x);
           widen4(wv[e], sv, tv, y);
