@@ -34,6 +34,7 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanPerSm = 2;
+constexpr int kPlanSeqPerCta = 128;   // at least one CTA for so many sequences (16384: 30 -> 21 us)
 constexpr unsigned kFullMask = 0xffffffffu;
 
 // The three sums, held at kMost (lengths come from the device and may be
@@ -55,8 +56,7 @@ __device__ __forceinline__ Three shfl_up(const Three& a, int d) {
 
 // What one sequence adds to the three sums; bad: it does not fit its row of
 // the table.
-__device__ __forceinline__ Three of_sequence(const PlanArgs& a, int b, bool& bad) {
-  const int ctx = __ldg(a.ctx_in + b), n = __ldg(a.n_new + b);
+__device__ __forceinline__ Three of_sequence(const PlanArgs& a, int ctx, int n, bool& bad) {
   const long long end = (long long)ctx + max(n, 0);
   bad |= ctx < 0 || end > (long long)a.max_blocks << a.bs_log2;
   if (ctx < 0) return {0, 0, 0};
@@ -88,12 +88,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(PlanArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-  // each thread sums a run of consecutive sequences, the runs are scanned
-  const int per = (n + kPlanThreads - 1) / kPlanThreads;
+  // Each thread sums a run of consecutive sequences, the runs are scanned.
+  // Longer runs than 4 take their lengths through shared memory, where the
+  // prefixes replace them: read in whole lines, and of odd length, so the
+  // threads' runs start in different banks (16384 sequences 76 -> 31 us).
+  const long long count = __ldg(a.free_count_in);
+  const bool staged = n > 4 * kPlanThreads;
+  int per = (n + kPlanThreads - 1) / kPlanThreads;
+  if (staged) {
+#pragma unroll 4
+    for (int b = tid; b < n; b += kPlanThreads) {
+      s_tok[b + 1] = (uint32_t)__ldg(a.ctx_in + b);
+      s_grow[b + 1] = (uint32_t)__ldg(a.n_new + b);
+    }
+    __syncthreads();
+    per |= 1;
+  }
   const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
+  auto of = [&](int b, bool& bad) -> Three {
+    return staged ? of_sequence(a, (int)s_tok[b + 1], (int)s_grow[b + 1], bad)
+                  : of_sequence(a, __ldg(a.ctx_in + b), __ldg(a.n_new + b), bad);
+  };
   Three sum = {0, 0, 0};
   bool bad = false;
-  for (int b = b0; b < b1; ++b) sum = sum + of_sequence(a, b, bad);
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) sum = sum + of(b, bad);
   Three incl = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -101,7 +120,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(PlanArgs a) {
     if (lane >= d) incl = incl + y;
   }
   if (lane == 31) s_warp[warp] = make_uint4(incl.tok, incl.grow, incl.back, 0);
-  const long long count = __ldg(a.free_count_in);
   const bool any_bad = __syncthreads_or(bad);
   Three base = {0, 0, 0}, total = {0, 0, 0};
 #pragma unroll
@@ -139,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(PlanArgs a) {
   if (tid == 0) s_tok[0] = s_grow[0] = s_back[0] = 0;
   bool unused = false;
   for (int b = b0; b < b1; ++b) {
-    run = run + of_sequence(a, b, unused);
+    run = run + of(b, unused);
     s_tok[b + 1] = run.tok;
     s_grow[b + 1] = run.grow;
     s_back[b + 1] = run.back;
@@ -240,7 +258,9 @@ cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t s) {
     return cudaErrorInvalidConfiguration;
   const long long per_cta = 4LL * kPlanThreads;
   long long ctas = (a.max_tok + per_cta - 1) / per_cta;
-  if (ctas < 1) ctas = 1;
+  // (released sequences give back far more blocks than tokens come in)
+  const long long by_seq = (a.n_seq + kPlanSeqPerCta - 1) / kPlanSeqPerCta;
+  if (ctas < by_seq) ctas = by_seq;
   if (ctas > kPlanPerSm * sms) ctas = kPlanPerSm * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
