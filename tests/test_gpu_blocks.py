@@ -581,3 +581,66 @@ def test_a_step_on_a_side_stream_and_replayed_from_a_graph():
         g.replay()
         verify()
     assert planner.ctx_lens.tolist() == [15, 30, 21]
+
+
+def test_offsets_past_32_bits():
+    # a pool whose keys lie beyond 4 GB: sequences at its far end
+    rng = np.random.default_rng(40)
+    bs, n_kv, hd, G, n_blocks = 1024, 8, 256, 2, 2600       # 5.5 GB of K codes, 5.5 of V
+    p = PagedPool(kvq.KVQ_Q8, n_kv, hd, bs, n_blocks)
+    assert p.k.numel() > 1 << 32
+    lens = np.array([1500, 700])
+    table = np.array([[n_blocks - 1, n_blocks - 3], [n_blocks - 2, -1]], np.int32)
+    k = rng.standard_normal((2200, n_kv, hd)).astype(np.float32)
+    seq = np.repeat([0, 1], lens)
+    pos = np.concatenate([np.arange(n) for n in lens])
+    p.append(dev(k), dev(k[::-1].copy()), i32(seq), i32(pos), i32(table))
+    bb = BlockBounds(p)
+    p.bound(bb, i32(table), i32(lens), 1500)
+    q = queries(rng, 2, 1, n_kv * G, hd)
+    blocks, index, cells = p.select(bb, dev(q), i32(lens), 1500, i32(table), 1, 0, 1)
+    out = p.decode_selected(dev(q), blocks, cells, 1 / 16)
+    torch.cuda.synchronize()
+    assert (blocks[0] == n_blocks - 3).all() and (blocks[1] == n_blocks - 2).all()
+    assert cells[:, 0, 0].tolist() == [476, 700]
+    tail = slice(n_blocks - 3, n_blocks)
+    h = {m: getattr(p, m)[tail].cpu().numpy() for m in ("k", "v", "ks", "vs")}
+    want = plain_bounds("q8", h, np.zeros((3, n_kv, 2, hd), np.int8), np.zeros((3, n_kv, hd // 64), np.float32),
+                        np.where(table < 0, -1, table - (n_blocks - 3)), [0, 0], lens, bs)
+    assert np.array_equal(bb.codes[tail].cpu().numpy(), want[0])
+    assert np.array_equal(bb.scales[tail].cpu().numpy(), want[1])
+    assert not bb.codes[:-3].any()
+    K, V = plain.pool_rows("q8", h["k"], h["v"], h["ks"], h["vs"])
+    ref, tol = plain.attention("q8", K, V, q, blocks.cpu().numpy() - (n_blocks - 3), cells.cpu().numpy(), bs,
+                               1 / 16)
+    assert (np.abs(out.cpu().numpy() - ref).max(-1) <= tol).all()
+
+
+def test_two_streams_at_once():
+    # the same calls on two streams, each with its own outputs and workspace,
+    # many times over: nothing is shared between calls
+    rng = np.random.default_rng(41)
+    bs, n_kv, hd, G, n_sel = 16, 2, 128, 4, 12
+    lens = np.array([900, 333, 1600])
+    table, n_blocks = tables(rng, lens, bs)
+    p, h = fill_pool(rng, "q8", n_blocks, n_kv, bs, hd)
+    bb = BlockBounds(p)
+    p.bound(bb, i32(table), i32(lens), 1600)
+    t, L = i32(table), i32(lens)
+    qs = [dev(queries(rng, 3, 1, n_kv * G, hd)) for _ in range(2)]
+    want = []
+    for q in qs:
+        sel = p.select(bb, q, L, 1600, t, n_sel)
+        want.append((sel, p.decode_selected(q, sel[0], sel[2], 0.1)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(30):
+        for i, s in enumerate(streams):
+            sel = p.select(bb, qs[i], L, 1600, t, n_sel, stream=s)
+            got[i].append((sel, p.decode_selected(qs[i], sel[0], sel[2], 0.1, stream=s)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for sel, out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(sel, want[i][0]))
+            assert torch.equal(out, want[i][1])
