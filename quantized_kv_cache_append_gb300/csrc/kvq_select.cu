@@ -469,16 +469,20 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
 #pragma unroll
     for (int i = 0; i < kOrderRegs; ++i) v[i] = lane + 32 * i < a.n_seq ? __ldg(a.ctx_lens + lane + 32 * i) : 0;
     len_raw = 0;
+    bool found = false;
 #pragma unroll 1
-    for (int c = 0; c < 3; ++c)
+    for (int c = 0; c < 3 && !found; ++c)
 #pragma unroll
       for (int i = 0; i < kOrderRegs; ++i) {
+        if (32 * i >= a.n_seq || found) continue;
         const int cls = 2LL * v[i] >= most ? 0 : 4LL * v[i] >= most ? 1 : 2;
         const unsigned m = __ballot_sync(kAll, lane + 32 * i < a.n_seq && cls == c);
-        const unsigned hit = __ballot_sync(kAll, ((m >> lane) & 1u) && base + __popc(m & ((1u << lane) - 1u)) == rank_b);
-        if (hit) {
+        const int k = rank_b - base;   // the k-th of them, if it is among these
+        if (k < __popc(m)) {
+          const unsigned hit = __ballot_sync(kAll, ((m >> lane) & 1u) && __popc(m & ((1u << lane) - 1u)) == k);
           b = 32 * i + __ffs(hit) - 1;
           len_raw = __shfl_sync(kAll, v[i], b & 31);
+          found = true;
         }
         base += __popc(m);
       }

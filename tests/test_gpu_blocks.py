@@ -162,6 +162,31 @@ def test_bounds_skip_foreign_ids_and_clamp_lengths():
     check_bounds(rng, "f16", p, h, table, [-5, 60], [1000, 64], max_new=64)       # past the row: clamped
 
 
+def test_bounds_cover_what_max_new_covers_and_no_more():
+    rng = np.random.default_rng(5)
+    bs = 16
+    table, n_blocks = tables(rng, [160], bs)
+    p, h = fill_pool(rng, "q8", n_blocks, 2, bs, 64)
+    bb = BlockBounds(p)
+    bb.codes.fill_(55)
+    p.bound(bb, i32(table), i32([160]), 30, i32([20]))       # cells 20 .. 49: blocks 1, 2, 3
+    torch.cuda.synchronize()
+    old = np.full(bb.codes.shape, 55, np.int8)
+    want = plain_bounds("q8", h, old, np.zeros(bb.scales.shape, np.float32), table, [20], [64], bs)
+    assert np.array_equal(bb.codes.cpu().numpy(), want[0])
+
+
+def test_bounds_of_many_items():
+    # more (block, head) items than one wave of warps or CTAs takes, per
+    # layout of the work: persistent CTAs come round again
+    rng = np.random.default_rng(6)
+    for fmt, hd, bs, n in (("f16", 64, 16, 3000), ("q8", 64, 16, 3000), ("f16", 256, 32, 400), ("q8", 256, 64, 300)):
+        lens = np.array([n * bs - 7])
+        table, n_blocks = tables(rng, lens, bs)
+        p, h = fill_pool(rng, fmt, n_blocks, 3, bs, hd)
+        check_bounds(rng, fmt, p, h, table, [0], lens, use_start=False)
+
+
 # ---------------------------------------------------------------- selection
 def random_bounds(rng, n_blocks, n_kv, hd):
     hi = np.clip(np.rint(rng.normal(60, 30, (n_blocks, n_kv, 2, hd))), -127, 127).astype(np.int8)

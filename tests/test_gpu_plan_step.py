@@ -148,6 +148,31 @@ def test_the_most_sequences_and_no_tokens():
     check(ctx, n_new, table, free, count, 16, n_blocks, n)
 
 
+def test_a_step_without_token_arrays():
+    rng = np.random.default_rng(4)
+    ctx, n_new = np.array([20, 5, 0]), np.array([-1, 0, 0])
+    table, free, count, n_blocks = state(rng, ctx, 16, 3, 2)
+    bt, fl = dev(table), dev(free)
+    mk = lambda m: torch.full((m,), 12345, dtype=torch.int32, device="cuda")
+    ctx_out, start, cnt, info = mk(3), mk(4), mk(1), mk(4)
+    st = kvq.kvq_plan_step(dev(ctx), dev(n_new), 3, 16, n_blocks, bt, 3, fl, dev([count]), 0, ctx_out, start,
+                           None, None, None, cnt, info)
+    assert st == kvq.KVQ_OK
+    torch.cuda.synchronize()
+    assert ctx_out.tolist() == [0, 5, 0] and info.tolist() == [0, 0, 2, 0] and cnt.tolist() == [4]
+    assert fl.tolist()[2:4] == table[0, :2].tolist() and start.tolist() == [0, 0, 0, 0]
+
+
+@pytest.mark.parametrize("n_seq", [1024, 1025, 2047, 5000])
+def test_many_sequences(n_seq):
+    # up to and past the lengths that go through shared memory
+    rng = np.random.default_rng(n_seq)
+    ctx = rng.integers(0, 200, n_seq)
+    n_new = np.where(rng.random(n_seq) < 0.2, -1, rng.integers(0, 40, n_seq))
+    table, free, count, n_blocks = state(rng, ctx, 16, 16, n_seq * 3)
+    check(ctx, n_new, table, free, count, 16, n_blocks, int(np.maximum(n_new, 0).sum()) + 3)
+
+
 def test_planner_runs_requests_to_their_end():
     # 40 steps of arrivals, decoding and endings, replayed on the host; the
     # blocks in use are never handed out twice, and all come back at the end
