@@ -31,9 +31,9 @@
 //
 // One GB300: 512 blocks x 8 heads 6.1 us (launch, three dependent loads and 2.5
 // us of selection), 4096 blocks x 8 heads x 4 tokens 12.3 us, 64 sequences of
-// 129 to 4096 blocks x 8 heads 69.7 us (4.1 TB/s of bounds, 61 % of the
-// measured copy rate; about 500 instructions a strip of 16 blocks and the
-// 512 selections keep it from more).
+// 129 to 4096 blocks x 8 heads 68 us (4.2 TB/s of bounds, 62 % of the measured
+// copy rate; an SM holds 24 warps, which spend a third of their time on the
+// dependent loads before a row's first score and on its selection).
 //
 // A token's query rows are padded to a power of two (or a multiple of 8) by
 // repeating its last row, which leaves the maximum as it is.
@@ -46,7 +46,8 @@
 namespace kvq {
 namespace {
 
-constexpr int kOrderRegs = 4;               // up to 128 sequences are ordered by length
+constexpr int kOrderRegs = 4;               // up to 128 sequences are ordered by length,
+constexpr int kOrderSteps = 4;              // in so many steps of max_ctx
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kForced = 0xffffffffu;   // keys: 0 not a candidate, kForced always kept
 
@@ -453,6 +454,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+  const int bs = 1 << a.bs_log2;
   // this cluster's (sequence, KV head, tokens w0 ..)
   int id = blockIdx.x / C;
   const int wg = id % a.n_wg;
@@ -460,22 +462,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
   const int h = id % a.n_kv;
   int b = id / a.n_kv, len_raw;
   if (a.order) {
-    // Sequences of at least half of max_ctx go first, then those of at least
-    // a quarter: clusters start roughly in order, and short rows fill the
-    // end of the launch (64 ragged sequences: 79 -> 74 us).
+    // Sequences go by length, longest first, in kOrderSteps steps of max_ctx:
+    // clusters start roughly in order, and short rows fill the end of the
+    // launch (64 ragged sequences: 79 -> 74 us).
     const int rank_b = b;
-    const long long most = (long long)a.n_cap << a.bs_log2;
+    const float step = (float)kOrderSteps / ((float)a.n_cap * (float)bs);
     int v[kOrderRegs], base = 0;
 #pragma unroll
     for (int i = 0; i < kOrderRegs; ++i) v[i] = lane + 32 * i < a.n_seq ? __ldg(a.ctx_lens + lane + 32 * i) : 0;
     len_raw = 0;
     bool found = false;
 #pragma unroll 1
-    for (int c = 0; c < 3 && !found; ++c)
+    for (int c = kOrderSteps - 1; c >= 0 && !found; --c)
 #pragma unroll
       for (int i = 0; i < kOrderRegs; ++i) {
         if (32 * i >= a.n_seq || found) continue;
-        const int cls = 2LL * v[i] >= most ? 0 : 4LL * v[i] >= most ? 1 : 2;
+        const int cls = min(max((int)((float)v[i] * step), 0), kOrderSteps - 1);
         const unsigned m = __ballot_sync(kAll, lane + 32 * i < a.n_seq && cls == c);
         const int k = rank_b - base;   // the k-th of them, if it is among these
         if (k < __popc(m)) {
@@ -502,7 +504,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
   }
   const long long cap = min((long long)a.max_blocks << a.bs_log2, (long long)a.n_cap << a.bs_log2);
   const int len = (int)max(0LL, min((long long)len_raw, cap));
-  const int bs = 1 << a.bs_log2;
   auto visible = [&](int w) { return max(0, len - a.W + w0 + w + 1); };        // cells token w0 + w sees
   auto blocks_of = [&](int cells) { return (cells >> a.bs_log2) + ((cells & (bs - 1)) != 0); };
   const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
@@ -793,14 +794,14 @@ bool plan_select(int hd, int sms, SelectArgs* a) {
     // CTAs per cluster: as many as fill the SMs once, at least 64 blocks each
     // and at most 8 (16 from 8192 blocks: 16384 blocks x 2 heads 29 us, with
     // 8 CTAs 42 us; 512 blocks x 8 heads 6.1 us either way, 4096 blocks x 8
-    // heads x 4 tokens 15.6 us, with 8 CTAs 12.7 us); for batches of long rows
-    // up to four times the SMs, at least 1024 blocks each, which evens
-    // out ragged lengths (64 sequences 83 -> 79 us; 16 of up to 256 blocks
-    // would take 10.1 us instead of 8.5).
+    // heads x 4 tokens 15.6 us, with 8 CTAs 12.7 us); for batches of longer rows
+    // up to four times the SMs, at least 512 blocks each (64 sequences of up
+    // to 4096 blocks 73 -> 68 us; 32 sequences of up to 2048 blocks, 4 tokens,
+    // 35 us, with 1024 blocks each 44 us, with 256 43 us).
     const int most = a->n_cap >= 8192 ? 4 : 3;
     int c = 0;
     while (c < most && (clusters << c) < sms && a->n_cap >= (64 << c)) ++c;
-    while (c < most && (clusters << c) < 4 * sms && a->n_cap >= (2048 << c)) ++c;
+    while (c < most && (clusters << c) < 4 * sms && a->n_cap >= (1024 << c)) ++c;
     a->c_log2 = c;
     a->cluster = 1 << c;
     // 512 threads where every CTA has an SM to itself and rows are long (4096
