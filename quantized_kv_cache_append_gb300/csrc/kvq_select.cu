@@ -804,12 +804,21 @@ bool plan_select(int hd, int sms, SelectArgs* a) {
     while (c < most && (clusters << c) < 4 * sms && a->n_cap >= (1024 << c)) ++c;
     a->c_log2 = c;
     a->cluster = 1 << c;
-    // 512 threads where every CTA has an SM to itself and rows are long (4096
-    // blocks x 8 heads x 4 tokens 14.6 -> 12.7 us, 16384 x 2 40 -> 29 us)
     a->order = a->n_seq > 1 && a->n_seq <= 32 * kOrderRegs && (clusters << c) > 2 * sms;
-    a->wide = a->n_cap >= 2048 && (clusters << c) <= sms;
+    // 512 threads where rows are long and the CTAs take half of the SMs at
+    // most (4096 blocks x 8 heads x 4 tokens 14.6 -> 12.7 us, 16384 x 2 40 -> 29
+    // us; 4096 x 16, on 128 CTAs, 14.4 us with 256 threads, 16.4 with 512)
+    a->wide = a->n_cap >= 2048 && (clusters << c) * 2 <= sms;
     a->lead_rows = (a->wg_tok + a->cluster - 1) >> c;
-    if (sel_smem(hd, n_tiles(*a), a->lead_rows, a->n_cap).bytes <= kSelMaxSmem) return true;
+    const bool fits = sel_smem(hd, n_tiles(*a), a->lead_rows, a->n_cap).bytes <= kSelMaxSmem;
+    // Where that leaves more than half of the SMs idle, fewer tokens a cluster
+    // (their bounds are then read again, from L2): 4096 blocks x 2 heads x 256
+    // dims x 4 tokens 19.5 -> 12.9 us, 256 blocks x 8 heads x 4 tokens 6.5 ->
+    // 6.2.  Long rows stop sooner (their clusters of 8 have to find places
+    // together: 4096 blocks x 8 heads x 4 tokens 12.3 us on 64 CTAs, 14.9 on
+    // 128).
+    const bool fills = (clusters << c) * 2 > sms || (a->n_cap >= 2048 && (clusters << c) * 5 > 2 * sms);
+    if (fits && (fills || a->wg_tok == 1)) return true;
     if (a->wg_tok == 1) return false;
     a->wg_tok = (a->wg_tok + 1) / 2;
   }
