@@ -224,7 +224,9 @@ def queries(rng, *shape):
     (1, 4, 2, 8, 256, 16, 20011, 100, 2, 4), (2, 1, 1, 32, 256, 16, 3001, 9, 0, 0),
     (2, 17, 1, 5, 64, 16, 1500, 11, 1, 1), (1, 2, 1, 16, 128, 1024, 70000, 8, 1, 1),
     (40, 1, 8, 4, 128, 16, 900, 12, 1, 2), (2, 9, 2, 7, 128, 16, 1200, 30, 1, 2),
-    (1, 1, 2, 1, 256, 16, 131072, 700, 0, 1),
+    (1, 1, 2, 1, 256, 16, 131072, 700, 0, 1), (2, 3, 1, 12, 128, 16, 1777, 20, 1, 1),
+    (1, 2, 2, 20, 256, 32, 3333, 15, 0, 1), (1, 130, 1, 6, 64, 16, 1999, 13, 1, 2),
+    (3, 5, 1, 9, 64, 16, 700, 6, 0, 0), (1, 3, 2, 8, 128, 16, 70001, 250, 1, 1),
 ])
 def test_selection(n_seq, W, n_kv, G, hd, bs, hi, n_sel, first, last):
     rng = np.random.default_rng(hi + W)
@@ -376,6 +378,8 @@ def random_lists(rng, n_seq, W, n_kv, n_sel, n_blocks, bs):
     (1, 1, 1, 1, 64, 16, 1), (1, 1, 1, 4, 128, 64, 70), (1, 1, 8, 4, 128, 64, 9), (3, 1, 2, 3, 64, 16, 13),
     (2, 5, 3, 5, 128, 32, 7), (1, 17, 2, 2, 256, 16, 21), (2, 1, 2, 16, 128, 128, 4), (1, 2, 1, 32, 64, 256, 3),
     (1, 1, 2, 32, 256, 16, 40), (9, 2, 4, 8, 256, 16, 5), (1, 3, 1, 7, 128, 1024, 2),
+    (2, 1, 1, 12, 256, 32, 6), (1, 2, 2, 20, 128, 16, 9), (1, 2, 1, 20, 256, 16, 12), (1, 150, 2, 4, 128, 16, 3),
+    (1, 40, 1, 3, 64, 32, 5),
 ])
 def test_attention_over_lists(fmt, n_seq, W, n_kv, G, hd, bs, n_sel):
     rng = np.random.default_rng(hd + bs + W)
