@@ -102,15 +102,16 @@ bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, Dec
   p->c_log2 = -1;
   if (lists) {
     // Splits of a row tile in one cluster of up to 8, merged there, if that
-    // fills four fifths of one wave, else through the workspace and the
-    // combine.  4096 cells a list, 128 int8 lists: 33.7 us in clusters of 4,
+    // fills four fifths of one wave or the lists have at most 4 tiles, one a
+    // CTA (8 FP16 lists of 64 cells 5.2 -> 3.9 us, of 256 cells 5.3 -> 4.8);
+    // else through the workspace and the combine.  4096 cells a list, 128 int8 lists: 33.7 us in clusters of 4,
     // 35.2 us through the workspace; 512 FP16 lists 165 and 170 us, one split
     // each.  Where clusters leave a third of the wave empty, or 16 CTAs have to
     // be placed together, they lose: 96 int8 lists 26 and 22 us, 8 FP16 lists
     // 10.7 and 9.2 us.
     int c = 0;
     while (c < 3 && (units << (c + 1)) <= capacity && (1 << c) < tiles) ++c;
-    if ((units << c) * 5 >= capacity * 4) {
+    if ((units << c) * 5 >= capacity * 4 || (tiles <= 4 && tiles <= (1 << c))) {
       const int split_tiles = (tiles + (1 << c) - 1) >> c;
       p->c_log2 = c;
       p->split_cells = split_tiles * tile;
