@@ -29,9 +29,9 @@
 //              of equal score width, compares those of the bin that holds
 //              the n_sel-th largest, and writes the list in ascending order
 //
-// One GB300: 512 blocks x 8 heads 6.1 us (launch, three dependent loads and 2.5
-// us of selection), 4096 blocks x 8 heads x 4 tokens 12.3 us, 64 sequences of
-// 129 to 4096 blocks x 8 heads 68 us (4.2 TB/s of bounds, 62 % of the measured
+// One GB300: 512 blocks x 8 heads 6.2 us (launch, three dependent loads and 2.5
+// us of selection), 4096 blocks x 8 heads x 4 tokens 12.6 us, 64 sequences of
+// 129 to 4096 blocks x 8 heads 70 us (4.1 TB/s of bounds, 60 % of the measured
 // copy rate; an SM holds 24 warps, which spend a third of their time on the
 // dependent loads before a row's first score and on its selection).
 //
@@ -433,6 +433,40 @@ __device__ __forceinline__ void write_list(Team<THREADS>& team, SelScratch& sc, 
   if ((int)threadIdx.x == 0) *out_len = th.count * bs - (sc.last ? bs - 1 - (cells - 1) % bs : 0);
 }
 
+// The list of one token that takes every block of its row that is the pool's.
+template <int THREADS>
+__device__ __forceinline__ void take_all(SelScratch& sc, int n, int n_blocks, int k, const int32_t* table,
+                                         int32_t* out_blk, int32_t* out_idx, int32_t* out_len, int bs, int cells) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int count = 0;
+  bool last = false;
+#pragma unroll 1
+  for (int j0 = 0; j0 < n; j0 += THREADS) {
+    const int j = j0 + tid, blk = j < n ? __ldg(table + j) : -1;
+    const unsigned m = __ballot_sync(kAll, (unsigned)blk < (unsigned)n_blocks);
+    if (lane == 0) sc.sums[0][0][warp] = (uint32_t)__popc(m);
+    last |= __syncthreads_or(j == n - 1 && ((m >> lane) & 1u)) != 0;
+    int at = count + __popc(m & ((1u << lane) - 1u));
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const int c = (int)sc.sums[0][0][w];
+      at += w < warp ? c : 0;
+      count += c;
+    }
+    if ((m >> lane) & 1u) {
+      out_blk[at] = blk;
+      if (out_idx != nullptr) out_idx[at] = j;
+    }
+    __syncthreads();   // the counts are written again
+  }
+#pragma unroll 1
+  for (int i = count + tid; i < k; i += THREADS) {
+    out_blk[i] = -1;
+    if (out_idx != nullptr) out_idx[i] = -1;
+  }
+  if (tid == 0) *out_len = count * bs - (last ? bs - 1 - (cells - 1) % bs : 0);
+}
+
 // NT n-tiles of 8 query rows; THREADS 256 (3 CTAs an SM where the
 // registers allow it, else 2) or 512 (one).
 template <int HD, int NT, int THREADS>
@@ -512,9 +546,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
   float* s_scale = reinterpret_cast<float*>(smem + lay.scales);
   uint32_t* s_keys = reinterpret_cast<uint32_t*>(smem + lay.keys);
 
+  const int n_all = blocks_of(visible(nw - 1));
+  auto out_row = [&](int w) { return ((size_t)b * a.W + w0 + w) * a.n_kv + h; };
+  auto index_of = [&](size_t row) { return a.sel_index != nullptr ? a.sel_index + row * a.n_sel : nullptr; };
+  if (__builtin_expect(n_all <= a.n_sel, 0)) {
+    // What the last token sees, and with it every other, fits the list: all of
+    // it is taken without a score (8 heads of 2048 cells, 64 blocks of 64 a
+    // list, 4.4 -> 2.2 us; 64 sequences of 100 to 4096 cells 10.6 -> 5.3 us; the
+    // branch costs longer rows 1 to 2 %).
+    cluster_wait();
+    for (int w = (int)rank; w < nw; w += C) {
+      const size_t row = out_row(w);
+      take_all<THREADS>(sc, blocks_of(visible(w)), a.n_blocks, a.n_sel, table, a.sel_blocks + row * a.n_sel,
+                        index_of(row), a.sel_lens + row, bs, visible(w));
+    }
+    return;
+  }
+
   // this CTA's share of the blocks the last token sees; its first ids are on
   // their way while the q codes are made
-  const int n_all = blocks_of(visible(nw - 1));
   const int share = ((n_all + C - 1) / C + STRIP - 1) / STRIP * STRIP;
   const int j0 = min((int)rank * share, n_all), j1 = min(j0 + share, n_all);
   constexpr int STEP = kSelWarps * STRIP;
@@ -717,9 +767,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 512 ? 1 : NT == 1 && HD <=
   cluster_wait();   // every key is in its leader's shared memory
 
   // ---------------- selection: token w is led by CTA w % C ----------------
-  auto out_row = [&](int w) { return ((size_t)b * a.W + w0 + w) * a.n_kv + h; };
   auto keys_of = [&](int w) { return s_keys + (size_t)(w >> a.c_log2) * key_row(a.n_cap); };
-  auto index_of = [&](size_t row) { return a.sel_index != nullptr ? a.sel_index + row * a.n_sel : nullptr; };
   Team<THREADS> team{sc};
   for (int w = (int)rank; w < nw; w += C) {
     const size_t row = out_row(w);

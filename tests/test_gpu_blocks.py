@@ -329,6 +329,23 @@ def test_selection_never_takes_a_foreign_block():
         check_select(codes, scales, q, [n * bs - 1, n * bs], table, bs, n_blocks, n_sel, 2, 2)
 
 
+def test_lists_that_hold_every_block():
+    # nothing to score: rows at, below and one past the list's length, longer
+    # than the CTA's threads, with holes, and beside rows that are scored
+    rng = np.random.default_rng(14)
+    bs, n_kv, W = 16, 2, 3
+    for n_sel in (1, 4, 300, 700):
+        lens = np.array([n_sel * bs, n_sel * bs + 1, n_sel * bs + 2, n_sel * bs + 3, bs, 1, 0, 5 * n_sel * bs])
+        table, n_blocks = tables(rng, lens, bs)
+        table[4, 0] = -1
+        table[0, n_sel - 1] = n_blocks            # the last visible block is foreign
+        table[1, ::3] = -1
+        codes, scales = random_bounds(rng, n_blocks, n_kv, 64)
+        check_select(codes, scales, queries(rng, len(lens), W, n_kv, 64), lens, table, bs, n_blocks, n_sel, 0, 1)
+        check_select(codes, scales, queries(rng, len(lens), 1, n_kv * 4, 64), lens, table, bs, n_blocks, n_sel, 1, 0,
+                     index=False)
+
+
 def test_selection_with_special_queries():
     rng = np.random.default_rng(10)
     bs, n = 16, 200
