@@ -79,6 +79,11 @@ constexpr float kTau = 8.0f;                 // lazy rescale threshold (log2 uni
 // error 3.2e-6 without, below 1e-6 with it) at the price of a rescale
 // whenever the maximum rises at all.
 constexpr float kBelowMax = kLists ? kTau : 0.0f;
+// int8 and K8V4 fold the V scale into p before the fp16 split: 2^kTau times a
+// scale of kScaleMost stays below fp16's 65504.  Cells with a larger one have
+// p at most 1 (see softmax).
+constexpr uint32_t kScaleMost = 0x5800u;   // fp16 bits of 128
+constexpr bool kFoldGuard = kLists;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int FMT, int HD, int NT>
@@ -907,8 +912,55 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
 
   };
 
-  // causal / length masks, online softmax -> p (rescales o when the maximum rises)
-  auto softmax = [&](int nvalid, int cw0, float (&z)[NT][4], float (&p)[NT][4]) {
+  // The V scales of this thread's cells g and g + 8, two fp16 a word, read with
+  // the slice's K and kept until its p.v.
+  constexpr int VSW = C::KI8 ? (C::VNS + 1) / 2 : 1;
+  auto load_scales = [&](int s, uint32_t (&vw)[2][VSW]) {
+    if constexpr (C::KI8) {
+      const unsigned char* vsc = smem + C::SMEM_SC + s * C::SC_STAGE_B + C::KSCALE_B;
+#pragma unroll
+      for (int ci = 0; ci < 2; ++ci) {
+        const unsigned char* src = vsc + (cl + g + 8 * ci) * (C::VNS * 2);
+        if constexpr (C::VNS == 1) {
+          vw[ci][0] = *reinterpret_cast<const unsigned short*>(src);
+        } else if constexpr (VSW == 1) {
+          vw[ci][0] = *reinterpret_cast<const uint32_t*>(src);
+        } else if constexpr (VSW == 2) {
+          const uint2 u = *reinterpret_cast<const uint2*>(src);
+          vw[ci][0] = u.x;
+          vw[ci][VSW - 1] = u.y;
+        } else {
+          const uint4 u = *reinterpret_cast<const uint4*>(src);
+          vw[ci][0] = u.x;
+          vw[ci][VSW > 1 ? 1 : 0] = u.y;
+          vw[ci][VSW > 2 ? 2 : 0] = u.z;
+          vw[ci][VSW > 3 ? 3 : 0] = u.w;
+        }
+      }
+    }
+  };
+
+  // causal / length masks, online softmax -> p (rescales o when the maximum
+  // rises).  A lane whose live cells have a V scale above kScaleMost asks for a
+  // reference maximum no lower than their logits, so that p (at most 1 then)
+  // times the scale is an fp16 number.
+  auto softmax = [&](int nvalid, int cw0, const uint32_t (&vw)[2][VSW], float (&z)[NT][4], float (&p)[NT][4]) {
+    bool large = false;
+    if constexpr (C::KI8 && kFoldGuard) {
+      // a half above kScaleMost plus the constant carries into bit 15, and no
+      // further
+      uint32_t x[2] = {0, 0};
+#pragma unroll
+      for (int ci = 0; ci < 2; ++ci)
+#pragma unroll
+        for (int i = 0; i < VSW; ++i) x[ci] |= (vw[ci][i] & 0x7fff7fffu) + (0x7fff7fffu - kScaleMost * 0x10001u);
+      if (nvalid < kCellsPerWarp) {   // (the scales of masked cells may be anything)
+        if (g >= nvalid) x[0] = 0;
+        if (g + 8 >= nvalid) x[1] = 0;
+      }
+      large = ((x[0] | x[1]) & 0x80008000u) != 0;
+    }
+    const float tau = large ? 0.f : kTau;
     // padding rows never reach the output, so only a short slice or a causal
     // limit inside it needs masks
     const bool need_mask = nvalid < kCellsPerWarp || row_last_min - cw0 < kCellsPerWarp - 1;
@@ -941,11 +993,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
         if (g + 8 > vis) z[nt][2 + j] = kNegInf;
       }
       lmax[nt][j] = fmaxf(z[nt][j], z[nt][2 + j]);
-      rise |= lmax[nt][j] > m[nt][j] + kTau;  // also true for the first finite maximum
+      rise |= lmax[nt][j] > m[nt][j] + tau;  // also true for the first finite maximum
     }
   }
   probs();
   if (__any_sync(kFull, rise)) {
+    const bool exact = C::KI8 && kFoldGuard && __any_sync(kFull, large);
+    const float tau_w = exact ? 0.f : kTau, below = exact ? 0.f : kBelowMax;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -954,8 +1008,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 4));
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 8));
         tmax = fmaxf(tmax, __shfl_xor_sync(kFull, tmax, 16));
-        if (tmax > m[nt][j] + kTau) {
-          const float top = tmax - kBelowMax;
+        if (tmax > m[nt][j] + tau_w) {
+          const float top = tmax - below;
           const float alpha = fast_exp2(m[nt][j] - top);  // 0 from the finite start
           m[nt][j] = top;
           l[nt][j] *= alpha;
@@ -977,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   };
 
   // o += V^T . P^T for one stage
-  auto pv = [&](int s, int nvalid, const float (&p)[NT][4]) {
+  auto pv = [&](int s, int nvalid, const float (&p)[NT][4], const uint32_t (&vw)[2][VSW]) {
     const uint32_t st = sbase + s * C::STAGE_B;
   // ---------------- O^T += V^T . P^T ----------------
   if constexpr (FMT == KVQ_F16) {
@@ -1018,30 +1072,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       }
     }
   } else if constexpr (C::V4) {
-    // The fp16 scales of this thread's cells g and g + 8 (the rows of its
-    // p fragments), every 32-dim block: one vector load per cell.
-    constexpr int SWD = C::VNS / 2;
-    const unsigned char* vsc = smem + C::SMEM_SC + s * C::SC_STAGE_B + C::KSCALE_B;
-    uint32_t sw[2][SWD];
+    uint32_t sw[2][VSW];
 #pragma unroll
-    for (int ci = 0; ci < 2; ++ci) {
-      const unsigned char* src = vsc + (cl + g + 8 * ci) * (C::VNS * 2);
-      if constexpr (SWD == 4) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src);
-        sw[ci][0] = u.x;
-        sw[ci][SWD > 1 ? 1 : 0] = u.y;
-        sw[ci][SWD > 2 ? 2 : 0] = u.z;
-        sw[ci][SWD > 3 ? 3 : 0] = u.w;
-      } else if constexpr (SWD == 2) {
-        const uint2 u = *reinterpret_cast<const uint2*>(src);
-        sw[ci][0] = u.x;
-        sw[ci][SWD > 1 ? 1 : 0] = u.y;
-      } else {
-        sw[ci][0] = *reinterpret_cast<const uint32_t*>(src);
-      }
+    for (int ci = 0; ci < 2; ++ci)
 #pragma unroll
-      for (int i = 0; i < SWD; ++i) sw[ci][i] = clamp_finite_h2(sw[ci][i]);
-    }
+      for (int i = 0; i < VSW; ++i) sw[ci][i] = clamp_finite_h2(vw[ci][i]);
     // One ldmatrix.trans x4 per two 32-dim blocks, on 16-bit units of 4
     // nibbles: register (cells 2t, 2t + 1; unit g) holds dims 4g .. 4g + 3
     // of the block for both cells.  Nibble e of both halves becomes the
@@ -1095,15 +1130,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       }
     }
   } else {
-    const unsigned short* vsc =
-        reinterpret_cast<const unsigned short*>(smem + C::SMEM_SC + s * C::SC_STAGE_B + C::KSCALE_B);
+    // p = 0 exactly for masked cells, whose scale bits may be anything
+    // (even +-inf / NaN): clamping to +-65504 keeps 0 * s == 0.  Finite
+    // fp16 scales pass unchanged.
+    uint32_t sw[2][VSW];
+#pragma unroll
+    for (int ci = 0; ci < 2; ++ci)
+#pragma unroll
+      for (int i = 0; i < VSW; ++i) sw[ci][i] = clamp_finite_h2(vw[ci][i]);
 #pragma unroll
     for (int gv = 0; gv < C::NG; ++gv) {
-      // p = 0 exactly for masked cells, whose scale bits may be anything
-      // (even +-inf / NaN): clamping to +-65504 keeps 0 * s == 0.  Finite
-      // fp16 scales pass unchanged.
-      const float s0 = fmaxf(fminf(__half2float(__ushort_as_half(vsc[(cl + g) * C::NG + gv])), 65504.f), -65504.f);
-      const float s8 = fmaxf(fminf(__half2float(__ushort_as_half(vsc[(cl + g + 8) * C::NG + gv])), 65504.f), -65504.f);
+      const float s0 = gv & 1 ? half_hi(sw[0][gv >> 1]) : half_lo(sw[0][gv >> 1]);
+      const float s8 = gv & 1 ? half_hi(sw[1][gv >> 1]) : half_lo(sw[1][gv >> 1]);
       uint32_t bh[NT][2], bl[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -1185,15 +1223,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   int blk_n = slice_blk(0);
   int nv_cur = 0;
   float p_cur[NT][4];
+  uint32_t vw[2][VSW];   // V scales of the tile whose p.v comes next
   if (n_tiles > 0) {
     if (!mbar_wait(bar_full, 0, a.wait_limit)) {
       lost = true;
     } else {
       nv_cur = slice_nvalid(0, blk_n);
       blk_n = slice_blk(1);
+      load_scales(0, vw);
       float z[NT][4];
       qk(0, z);
-      softmax(nv_cur, c_begin + cl, z, p_cur);
+      softmax(nv_cur, c_begin + cl, vw, z, p_cur);
     }
   }
   int it = 0;
@@ -1205,15 +1245,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     }
     const int nv_next = slice_nvalid(it + 1, blk_n);
     blk_n = slice_blk(it + 2);
+    uint32_t vn[2][VSW];
+    load_scales(sn, vn);
     float zn[NT][4];
     qk(sn, zn);
-    pv(it % C::STAGES, nv_cur, p_cur);
+    pv(it % C::STAGES, nv_cur, p_cur, vw);
     release(it);
-    softmax(nv_next, c_begin + (it + 1) * kTC + cl, zn, p_cur);
+    softmax(nv_next, c_begin + (it + 1) * kTC + cl, vn, zn, p_cur);
     nv_cur = nv_next;
+#pragma unroll
+    for (int i = 0; i < 2 * VSW; ++i) vw[i / VSW][i % VSW] = vn[i / VSW][i % VSW];
   }
   if (!lost && n_tiles > 0) {  // the last tile
-    pv(it % C::STAGES, nv_cur, p_cur);
+    pv(it % C::STAGES, nv_cur, p_cur, vw);
     release(it);
   }
   if (producer) {
