@@ -10,7 +10,7 @@ import torch
 
 import quantized_kv_cache_append_gb300 as kvq
 from tests import plain_blocks as plain
-from tests.test_gpu_blocks import dev, fill_pool, i32, queries, random_lists
+from tests.test_gpu_blocks import dev, fill_pool, i32, queries, random_lists, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,63 @@ def test_lists_whose_logits_rise_under_large_value_scales(fmt, rise):
             lens = rng.integers(1, n_sel * bs + 1, (n_seq, 1, n_kv))
             lens.flat[0] = n_sel * bs
             check_lists(fmt, p, h, q, blocks, lens)
+
+
+def check_dense(fmt, p, h, q, table, ctx, some=None):
+    """some: so many sequences are compared (the first, the others spread)."""
+    sm = float(np.float32(1 / math.sqrt(p.head_dim)))
+    n_seq, W, n_q, hd = q.shape
+    out = p.decode(dev(q), i32(ctx), int(max(ctx)), i32(table), sm)
+    torch.cuda.synchronize()
+    at = np.arange(n_seq) if some is None else np.unique(np.linspace(0, n_seq - 1, some).astype(int))
+    out, q, table, ctx, n_seq = out.cpu().numpy()[at], q[at], table[at], np.asarray(ctx)[at], len(at)
+    assert np.isfinite(out).all()
+    K, V = plain.pool_rows(fmt, h["k"], h["v"], h["ks"], h["vs"])
+    blocks = np.broadcast_to(table[:, None, None], (n_seq, W, p.n_kv, table.shape[1]))
+    lens = np.maximum(0, ctx[:, None] - W + 1 + np.arange(W))[..., None].repeat(p.n_kv, 2)
+    want, tol = plain.attention(fmt, K, V, q, blocks, lens, p.block_size, sm)
+    # K enters q.k as 1152 + code here: a group of 64 dims is summed in fp32 at
+    # up to (1152 + 127) sum |q| (4 steps and the 1152 sum |q| taken off, itself
+    # a sum in 6 steps: 12 roundings of 2^-23 at most), times the K scale
+    dz = 12 * 2.0 ** -23 * 1279 * np.abs(q).sum(-1) * float(np.abs(h["ks"].astype(np.float64)).max()) * sm
+    spread = np.abs(V).max()
+    tol = tol + 2 * dz * spread + lowest_rounding(h, fmt, table.shape[1] * p.block_size) / weights_sum(
+        K, q, blocks, lens, p.block_size, sm)
+    err = np.abs(out - want).max(-1)
+    assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("fmt", ["q8", "k8v4"])
+@pytest.mark.parametrize("W,hd,G", [(1, 128, 4), (1, 64, 1), (3, 128, 4), (2, 64, 5), (1, 256, 8), (2, 256, 2)])
+@pytest.mark.parametrize("rise", [3.0, 7.5, 60.0])
+def test_dense_decode_whose_logits_rise_under_large_value_scales(fmt, W, hd, G, rise):
+    # The reference maximum may lie up to 2^8 behind the row's own: weights up
+    # to 256, times the scale.  Sequences enough that each is one split of all
+    # its tiles (all of them read the same blocks).
+    rng = np.random.default_rng(hd + W)
+    bs, L, n_seq, n_kv = 32, 640, 320, 8
+    nb = L // bs
+    for S, first in ((260, 0), (1000, 0), (65504, 0), (65504, 300)):     # the first cell with such a scale
+        p, h = fill_pool(rng, fmt, nb, n_kv, bs, hd)
+        row = rng.permutation(nb)
+        order = [(int(b), c) for b in row for c in range(bs)]
+        ramp(rng, p, h, order, 1.0, rise)
+        for b, c in order[first:]:
+            h["vs"][b, :, c] = np.float16(S)
+        p.vs.copy_(dev(h["vs"]))
+        q = (1 + 0.1 * rng.standard_normal((n_seq, W, n_kv * G, hd))).astype(np.float32)
+        ctx = rng.integers(L // 2, L + 1, n_seq)
+        ctx[0] = L
+        check_dense(fmt, p, h, q, np.broadcast_to(row, (n_seq, nb)).astype(np.int32), ctx, some=12)
+
+
+@pytest.mark.parametrize("fmt", ["q8", "k8v4"])
+@pytest.mark.parametrize("W,G", [(1, 4), (4, 8)])
+def test_dense_decode_with_large_value_scales(fmt, W, G):
+    rng = np.random.default_rng(W)
+    bs, L, hd = 16, 1500, 128
+    table, n_blocks = tables(rng, [L, 7, 333], bs)
+    for S, kind in ((300, "all"), (65504, "some"), (4096, "one")):
+        p, h = fill_pool(rng, fmt, n_blocks, 2, bs, hd)
+        set_scales(rng, p, h, kind, S)
+        check_dense(fmt, p, h, queries(rng, 3, W, 2 * G, hd), table, [L, 7, 333])
