@@ -342,7 +342,8 @@ __device__ __forceinline__ void merge_cluster(const DecodeArgs& a, unsigned char
       float top = M;
 #pragma unroll
       for (int u = 0; u < B; ++u) {
-        bad |= ml[u].x != ml[u].x;
+        // (a NaN sum: a NaN or infinite logit in a live cell)
+        bad |= ml[u].x != ml[u].x || ml[u].y != ml[u].y;
         top = fmaxf(top, ml[u].x);
       }
       const float keep = M == -INFINITY ? 0.f : fast_exp2(M - top);
