@@ -171,7 +171,9 @@ class PagedPool:
 
     def decode_selected(self, q, sel_blocks, sel_lens, sm_scale: float, out=None, workspace=None,
                         stream=None):
-        """decode over a list of blocks for each (token, KV head)."""
+        """decode over a list of blocks for each (token, KV head).  workspace:
+        uint8, any size from 256 bytes up (kvq_sparse_workspace_bytes is the
+        fastest)."""
         n_seq, W, n_q, hd = q.shape
         n_sel = int(sel_blocks.shape[-1])
         f32, i32 = torch.float32, torch.int32
