@@ -85,6 +85,12 @@ constexpr float kBelowMax = kLists ? kTau : 0.0f;
 // (int8 with head_dim 64, whose tiles are the shortest, 1-6 %: 8 sequences of
 // 8192 cells x 8 heads 29.7 -> 31.5 us).
 constexpr uint32_t kScaleMost = 0x5800u;   // fp16 bits of 128
+// int8 K in q.k.  Dense: as 1152 + code, the 1152 * sum(q) taken off through
+// the accumulator's start (no subtraction per element).  The sums then run
+// at 1152 times the codes' weight and leave a logit error of up to about
+// 1e-5; block lists subtract first (4 HSUB2 more per 16 x 16 tile) and keep
+// it at the FP16 cache's 1e-6.
+constexpr bool kCodesExact = kLists;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int FMT, int HD, int NT>
@@ -122,9 +128,9 @@ struct Cfg {
   static constexpr int QROW = HD * 2 + 16;
   static constexpr int QBYTES_MAX = 2 * NT * 8 * QROW;   // hi and lo, NT*8 padded rows
   static constexpr int SMEM_Q = SMEM_SC + STAGES * SC_STAGE_B;
-  // int8: per (padded row, 64-dim group, 32-dim half) 1152 * sum of q (hi + lo)
+  // int8, dense: per (padded row, 64-dim group, 32-dim half) 1152 * sum of q (hi + lo)
   static constexpr int SMEM_QC = SMEM_Q + (QBYTES_MAX + 15) / 16 * 16;
-  static constexpr int QC_BYTES = KI8 ? (NT * 8 * NG * 2 * 4 + 15) / 16 * 16 : 0;
+  static constexpr int QC_BYTES = KI8 && !kCodesExact ? (NT * 8 * NG * 2 * 4 + 15) / 16 * 16 : 0;
   // per-warp row maxima and sums for the merge at the end: [4][RP][2] fp32
   static constexpr int SMEM_WML = SMEM_QC + QC_BYTES;
   static constexpr int SMEM_BAR = SMEM_WML + kConsumerWarps * NT * 8 * 2 * 4;
@@ -155,13 +161,6 @@ struct TmaMaps {
 // the fp16 bit pattern 0x6400 | u is 1024 + u, and (1024 + u) - 1152 = c.
 constexpr uint32_t kMagic = 0x64646464u;
 constexpr uint32_t kBias = 0x64806480u;  // fp16 1152 in both halves
-
-// int8 K in q.k.  Dense: as 1152 + code, the 1152 * sum(q) taken off through
-// the accumulator's start (no subtraction per element).  The sums then run
-// at 1152 times the codes' weight and leave a logit error of up to about
-// 1e-5; block lists subtract first (4 HSUB2 more per 16 x 16 tile) and keep
-// it at the FP16 cache's 1e-6.
-constexpr bool kCodesExact = kLists;
 
 // Swizzled shared-memory byte offset of logical byte `b` of cell `c` (0..63)
 // in a K or V tile laid out [span][cell][SWB]: every TMA box (one piece of
@@ -493,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   const int n_pieces = kTC >> pc_log2;
   const int32_t* bt = a.block_table + (size_t)b * a.max_blocks;
   const bool producer = threadIdx.x == 0;
-  // the cache is read once per call: its lines leave L2 first
+  // Dense: the cache is read once per call, so its lines leave L2 first.  (Lists
+  // keep the hint, although the tokens of a verify window may share blocks.)
   const uint64_t pol = l2_evict_first_policy();
   // Let the combine grid be scheduled as soon as SMs free up; it still waits
   // (griddepcontrol.wait) for this whole grid to finish before reading.
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
         const __half lo = __float2half_rn(x - __half2float(h));
         *reinterpret_cast<__half*>(qs + r * C::QROW + k * 2) = h;
         *reinterpret_cast<__half*>(qs + (HL ? 4 + r : RP + r) * C::QROW + k * 2) = lo;
-        if constexpr (C::KI8) {
+        if constexpr (C::KI8 && !kCodesExact) {
           // The 32 lanes of a warp hold 32 consecutive k of one row and one
           // 64-dim group (RP * HD is a multiple of 128): their sum of q,
           // times 1152, fills the (row, group, half) slot of the int8 bias.
@@ -669,11 +669,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   // ---------------- consumer setup ----------------
   const int g = lane >> 2, t = lane & 3;
 
-  // int8 K enters the MMA as fp16 (1152 + code) (no subtraction per
+  // Dense: int8 K enters the MMA as fp16 (1152 + code) (no subtraction per
   // element); the 1152 * sum(q) of each (row, 64-dim group) is taken off
   // once, as the starting value of that group's hi accumulator.
   float qcorr[C::KI8 ? C::NG : 1][NT][2];
-  if constexpr (C::KI8) {
+  if constexpr (C::KI8 && !kCodesExact) {
     const float* s_qc = reinterpret_cast<const float*>(smem + C::SMEM_QC);
 #pragma unroll
     for (int gq = 0; gq < C::NG; ++gq)
@@ -858,15 +858,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
         w[2 * h + 1][0] = r[2] ^ 0x80808080u;
         w[2 * h + 1][1] = r[3] ^ 0x80808080u;
       }
-      float acc[2][NT][4];  // hi chain (starts at -1152 sum q), lo chain
+      float acc[2][NT][4];  // hi chain (dense: starts at -1152 sum q), lo chain
+      if constexpr (!kCodesExact) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        acc[0][nt][0] = acc[0][nt][2] = kCodesExact ? 0.f : qcorr[gq][nt][0];
-        acc[0][nt][1] = acc[0][nt][3] = kCodesExact ? 0.f : qcorr[gq][nt][1];
+        for (int nt = 0; nt < NT; ++nt) {
+          acc[0][nt][0] = acc[0][nt][2] = qcorr[gq][nt][0];
+          acc[0][nt][1] = acc[0][nt][3] = qcorr[gq][nt][1];
+        }
       }
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
-        uint32_t af[4];  // fp16 1152 + code, exact
+        uint32_t af[4];  // fp16 1152 + code (lists: code), exact
         af[0] = prmt(w[kk][0], kMagic, 0x4140u);
         af[2] = prmt(w[kk][0], kMagic, 0x4342u);
         af[1] = prmt(w[kk][1], kMagic, 0x4140u);
@@ -876,14 +878,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
           for (int i = 0; i < 4; ++i) af[i] = hsub2(af[i], kBias);
         }
         if constexpr (HL) {
-          // one chain: columns 0-3 hi (start at -1152 sum q), 4-7 lo (at 0)
-          mma16816(acc[0][0], af, qreg[gq * 4 + kk][0], qreg[gq * 4 + kk][1]);
+          // one chain: columns 0-3 hi (dense: start at -1152 sum q), 4-7 lo (at 0)
+          if (kCodesExact && kk == 0) mma16816_zc(acc[0][0], af, qreg[gq * 4][0], qreg[gq * 4][1]);
+          else mma16816(acc[0][0], af, qreg[gq * 4 + kk][0], qreg[gq * 4 + kk][1]);
         } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             uint32_t qf[4];
             ldsm_x4(qf, q_lane + (uint32_t)(nt * 8) * C::QROW + (gq * 4 + kk) * 32);
-            mma16816(acc[0][nt], af, qf[0], qf[1]);
+            if (kCodesExact && kk == 0) mma16816_zc(acc[0][nt], af, qf[0], qf[1]);
+            else mma16816(acc[0][nt], af, qf[0], qf[1]);
             if (kk == 0) mma16816_zc(acc[1][nt], af, qf[2], qf[3]);
             else mma16816(acc[1][nt], af, qf[2], qf[3]);
           }
@@ -1610,10 +1614,6 @@ int ctas_per_sm_impl() {
     using C = Cfg<FMT, HD, NT>;
     if (cudaFuncSetAttribute(decode_mma<FMT, HD, NT, HL>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-      return false;
-    // clusters of 16 are past the portable 8
-    if (kLists && cudaFuncSetAttribute(decode_mma<FMT, HD, NT, HL>,
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return false;
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_mma<FMT, HD, NT, HL>, kThreads,
