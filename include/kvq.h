@@ -20,7 +20,7 @@
  *   kvq_bound_blocks bounds of each block's keys
  *   kvq_select_blocks
  *                    the blocks each query token and KV head attends to,
- *                    chosen by those bounds
+ *                    ranked by those bounds
  *   kvq_sparse_decode_attn
  *                    decode attention over such lists of blocks
  *
@@ -525,8 +525,11 @@ kvq_status kvq_plan_step(const int32_t *ctx_in, const int32_t *n_new, int n_seq,
  * >= max(|lo|, |hi|); the codes are floor(lo / 2^e) and ceil(hi / 2^e).  The
  * result is bit-identical to that definition for finite keys; NaN keys and
  * int8 keys whose scale is not finite are passed over (a dim with nothing
- * else gets 0), infinite FP16 keys give codes of +-127 at e = 16.  Bounds belong to the physical block: blocks shared by
- * several rows need one call, and a block that is refilled needs a new one.
+ * else gets 0), infinite FP16 keys give codes of +-127 at e = 16.  Bounds
+ * belong to the physical block: a block that several rows share needs one of
+ * them bounded, and a block that is refilled needs a new call.  (Rows of one
+ * call that end at different cells of a block they share leave the bounds of
+ * either.)
  * Sequences with ctx_start >= ctx_lens and blocks with an id out of range
  * are skipped.  max_new == 0 is a no-op.
  */
@@ -536,13 +539,17 @@ kvq_status kvq_bound_blocks(const kvq_cache *cache, const int32_t *block_table, 
                             float *bound_scales, void *stream);
 
 /*
- * The blocks each query token attends to, chosen per KV head by an upper
- * bound of its logits over each block.
+ * The blocks each query token attends to, chosen per KV head by an estimate
+ * of the largest q . k over each block: the bound that kvq_bound_blocks's
+ * codes give for q rounded to 8 bits.  It is not a bound for q itself: the
+ * rounding moves it up or down by at most half a code step of every dim
+ * times that dim's larger bound, and infinite FP16 keys have finite bounds.
  *
  *   q          device fp32 [n_seq][W][n_q][head_dim], 16-byte aligned, as
  *              kvq_decode_attn takes it (token w sees cells [0, ctx_lens[b]
  *              - W + w]); any W >= 1
- *   max_ctx    host int: an upper bound of ctx_lens
+ *   max_ctx    host int: an upper bound of ctx_lens, at most
+ *              max_blocks_per_seq * block_size (KVQ_ERR_ARG)
  *   n_sel      blocks per list, of which the first n_first and the last
  *              n_last visible blocks are always kept (n_first + n_last <=
  *              n_sel)

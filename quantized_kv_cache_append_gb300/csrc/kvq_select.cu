@@ -2,8 +2,9 @@
 // (kvq_select_blocks): a score for every block from its key bounds, and the
 // n_sel highest.
 //
-// The score bounds q . k over a block's keys from above: per dim the larger
-// of q lo and q hi, i.e. max(q, 0) hi + min(q, 0) lo.  q enters as int8
+// The score estimates the largest q . k over a block's keys: per dim the larger
+// of q lo and q hi, i.e. max(q, 0) hi + min(q, 0) lo, an upper bound for the q
+// it is computed with.  That q is rounded to int8
 // codes with a power-of-two scale per 64 dims, the bounds are int8 codes
 // with a power-of-two scale per 64 dims, so a group's sum S is a whole
 // number below 2^21 and S * scale_q * scale_k is exact in fp32; 2 or 4
