@@ -515,8 +515,10 @@ kvq_status kvq_plan_step(const int32_t *ctx_in, const int32_t *n_new, int n_seq,
  *   ctx_start    device int32 [n_seq]: first cell that changed (NULL: 0,
  *                all blocks)
  *   ctx_lens     device int32 [n_seq]
- *   max_new      host int: an upper bound of ctx_lens - ctx_start; blocks
- *                beyond what it covers keep their old bounds
+ *   max_new      host int: an upper bound of ctx_lens - ctx_start, at most
+ *                what a row holds (max_blocks_per_seq * block_size, else
+ *                KVQ_ERR_ARG); blocks beyond what it covers keep their old
+ *                bounds
  *   bounds       device int8 [n_blocks][n_kv_heads][2][head_dim], 256-byte
  *                aligned: lo codes, then hi codes
  *   bound_scales device fp32 [n_blocks][n_kv_heads][head_dim / 64]

@@ -133,7 +133,9 @@ class PagedPool:
 
     def bound(self, bounds: BlockBounds, block_table, ctx_lens, max_new: int, ctx_start=None,
               stream=None) -> None:
-        """Bounds of the blocks that cells [ctx_start, ctx_lens) touch (None: from 0)."""
+        """Bounds of the blocks that cells [ctx_start, ctx_lens) touch (None: from
+        0).  max_new: the most cells any sequence has there, at most a row's
+        max_blocks * block_size."""
         n_seq = block_table.shape[0]
         i32 = torch.int32
         self._check("bound", block_table=(block_table, i32, (None, None)),
