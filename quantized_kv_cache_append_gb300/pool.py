@@ -128,6 +128,8 @@ class PagedPool:
     @contextlib.contextmanager
     def _on(self, stream):
         """The pool's device, and the stream the call runs on."""
+        if self.k.device.type != "cuda":
+            raise KvqError(KVQ_ERR_ARG, f"the pool is on {self.k.device}: its block methods need a GPU's")
         with torch.cuda.device(self.k.device), on_stream(stream):
             yield
 

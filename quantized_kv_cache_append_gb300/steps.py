@@ -49,6 +49,8 @@ class StepPlanner:
                 or n_new.device != self.info.device):
             raise KvqError(KVQ_ERR_ARG, "StepPlanner.plan: n_new must be a contiguous int32 [n_seq] on "
                                         f"{self.info.device}")
+        if self.info.device.type != "cuda":
+            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.plan: the planner is on {self.info.device}, not a GPU")
         with torch.cuda.device(self.info.device), on_stream(stream):
             self._before.copy_(self._after)
             check(kvq_plan_step(self.ctx_start, n_new, self.n_seq, self.block_size, self.n_blocks,
