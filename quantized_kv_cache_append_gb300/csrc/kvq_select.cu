@@ -4,10 +4,9 @@
 //
 // The score estimates the largest q . k over a block's keys: per dim the larger
 // of q lo and q hi, i.e. max(q, 0) hi + min(q, 0) lo, an upper bound for the q
-// it is computed with.  That q is rounded to int8
-// codes with a power-of-two scale per 64 dims, the bounds are int8 codes
-// with a power-of-two scale per 64 dims, so a group's sum S is a whole
-// number below 2^21 and S * scale_q * scale_k is exact in fp32; 2 or 4
+// it is computed with.  That q is rounded to int8 codes with a power-of-two
+// scale per 64 dims and the bounds are such codes, so a group's sum S is a
+// whole number below 2^21 and S * scale_q * scale_k is exact in fp32; 2 or 4
 // groups are added pairwise in fp32, and the query heads of a KV head give
 // their maximum.  No sum depends on its order, so the chosen blocks do not
 // depend on how the work is split; ties go to the lower block.
@@ -863,9 +862,12 @@ bool plan_select(int hd, int sms, SelectArgs* a) {
     // Where that leaves more than half of the SMs idle, fewer tokens a cluster
     // (their bounds are then read again, from L2): 4096 blocks x 2 heads x 256
     // dims x 4 tokens 19.5 -> 12.9 us, 256 blocks x 8 heads x 4 tokens 6.5 ->
-    // 6.2.  Long rows stop sooner (their clusters of 8 have to find places
-    // together: 4096 blocks x 8 heads x 4 tokens 12.3 us on 64 CTAs, 14.9 on
-    // 128).
+    // 6.2.  Long rows stop sooner, at two fifths of the SMs, because their
+    // clusters have to find places together.  On 64 CTAs and on 128, blocks x
+    // heads x tokens: 2048 x 8 x 4 9.5 and 10.1 us, 3000 x 8 x 4 11.5 and 12.5,
+    // 4096 x 8 x 4 12.7 and 15.0 (64 dims 11.3 and 13.1, 256 dims 15.1 and
+    // 18.9), 6000 x 8 x 4 15.4 and 19.0, 4096 x 8 x 2 11.6 and 14.9, 4096 x 4 x
+    // 8 12.7 and 15.1, 12000 x 4 x 4 18.5 and 27.1.
     const bool fills = (clusters << c) * 2 > sms || (a->n_cap >= 2048 && (clusters << c) * 5 > 2 * sms);
     if (fits && (fills || a->wg_tok == 1)) return true;
     if (a->wg_tok == 1) return false;
