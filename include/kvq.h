@@ -23,6 +23,12 @@
  *                    ranked by those bounds
  *   kvq_sparse_decode_attn
  *                    decode attention over such lists of blocks
+ *   kvq_append_rotary
+ *                    norms of each head's q and k, rotary positions, and the
+ *                    append of k and v, in one pass
+ *   kvq_verify_draft drafted tokens accepted or replaced by the target's
+ *                    probabilities, from given random numbers
+ *   kvq_trim_step    the cells of rejected drafts taken back
  *
  * Sources (page title, section):
  *   [kv-q8 PR]  "#3084 qwen35: FP16 K/V cache by default, int8 with --kv-q8
@@ -627,6 +633,147 @@ kvq_status kvq_sparse_decode_attn_lost_wait_test(const kvq_cache *cache, const f
                                                  float *out, void *workspace,
                                                  size_t workspace_bytes, uint32_t wait_limit,
                                                  uint32_t extra_tx_bytes, void *stream);
+
+/* Element types of the calls below. */
+typedef enum {
+    KVQ_T_F32 = 0,
+    KVQ_T_F16 = 1,
+    KVQ_T_BF16 = 2
+} kvq_type;
+
+/*
+ * How kvq_append_rotary treats each head of q and k:
+ *
+ *   norm      x <- x * rsqrt(mean(x^2) + eps) * w over the head's head_dim
+ *             values (w = q_norm or k_norm, fp32 [head_dim]; NULL: no norm of
+ *             that input.  A model that stores w - 1 passes w)
+ *   rotation  of the head's first rot_dim dims, pairs i = 0 .. rot_dim / 2 - 1
+ *             of dims (2i, 2i + 1) if interleaved, else (i, i + rot_dim / 2):
+ *             (a, b) <- (a cos t - b sin t, b cos t + a sin t) * gain with the
+ *             angle t = position * inv_freq[i], the position taken on axis
+ *             pair_axis[i] (NULL: axis 0).  Dims from rot_dim on stay.
+ *
+ * Arrays are device memory; inv_freq, q_norm and k_norm 16-byte aligned.
+ */
+typedef struct kvq_rotary {
+    int32_t type;        /* kvq_type of q, k and v                            */
+    int32_t rot_dim;     /* a multiple of 16 in [0, head_dim]                 */
+    int32_t interleaved; /* 0 or 1                                            */
+    int32_t n_axes;      /* axes of `positions`, 1 .. 8                       */
+    float eps;           /* >= 0                                              */
+    float gain;          /* 1, or a factor on cos and sin                     */
+    const float *inv_freq;    /* [rot_dim / 2], radians a position            */
+    const int32_t *pair_axis; /* [rot_dim / 2] or NULL; clamped to the axes   */
+    const float *q_norm;      /* [head_dim] or NULL                           */
+    const float *k_norm;      /* [head_dim] or NULL                           */
+} kvq_rotary;
+
+/*
+ * kvq_append of k and v as a projection leaves them: q and k of each token
+ * are normed and rotated, q is written out for the attention calls, k and v
+ * go into the pool in its format (kvq_append's, of the fp32 values the norm
+ * and rotation give; v is only converted).
+ *
+ *   q, k, v    device [n_tok] rows of n_q, n_kv_heads, n_kv_heads heads, of
+ *              rotary->type, 16-byte aligned; row t starts at element t *
+ *              q_stride (k_stride, v_stride), so they may be parts of one
+ *              [n_tok][(n_q + 2 n_kv_heads) head_dim] array.  Strides are at
+ *              least a row and a multiple of 16 bytes (KVQ_ERR_ARG)
+ *   n_q        query heads, any number >= 0 (0: q and q_out unread)
+ *   positions  device int32 [n_axes][n_tok] or NULL: tok_pos on every axis
+ *              (then n_axes is 1)
+ *   tok_seq, tok_pos, block_table, n_seq, max_blocks_per_seq
+ *              as kvq_append takes them
+ *   q_out      device fp32 [n_tok][n_q][head_dim], 16-byte aligned, not
+ *              overlapping an input
+ *
+ * A token whose tok_seq is outside [0, n_seq) or whose tok_pos is negative
+ * (padding) is skipped: its row of q_out stays as it was, nothing is
+ * appended.  Where only its block is out of range its q is written still.
+ * Sums, angles and rotation are fp32 or better: an angle of up to 2^22
+ * radians is reduced to within 2^-22 before its sine and cosine are taken, a
+ * larger one to within the fp64 rounding of the product (negative positions
+ * on an axis alike).  Nothing is rounded to 16 bits in between.
+ * n_tok == 0 is a no-op.  n_tok * (n_q + 2 n_kv_heads) < 2^31, else
+ * KVQ_ERR_UNSUPPORTED.  One launch, no workspace.
+ */
+kvq_status kvq_append_rotary(const kvq_cache *cache, const kvq_rotary *rotary, const void *q,
+                             const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, int n_tok, int n_q, const int32_t *tok_seq,
+                             const int32_t *tok_pos, const int32_t *positions,
+                             const int32_t *block_table, int n_seq, int max_blocks_per_seq,
+                             float *q_out, void *stream);
+
+/*
+ * Drafted tokens against the target's probabilities, by rejection sampling
+ * from given random numbers.  A verify window of W tokens (the last sampled
+ * one and up to W - 1 drafts) gives W rows of target probabilities, row i
+ * those of the token after window token i, which draft i proposes.
+ *
+ *   target       device [n_seq][W] rows of `vocab` probabilities
+ *   draft        device [n_seq][W - 1] rows, what each draft was sampled
+ *                from; NULL: drafts are certain (a lookup's, an argmax), each
+ *                with probability 1
+ *   type         kvq_type of both; aligned to it
+ *   target_stride, draft_stride
+ *                elements from row to row, >= vocab
+ *   draft_tokens device int32 [n_seq][W - 1]
+ *   n_draft      device int32 [n_seq] or NULL (W - 1): drafts of each
+ *                sequence, at most W - 1 (more count as W - 1); negative: the
+ *                sequence takes no part: 0 accepted, tokens -1, 0 dropped
+ *   u            device fp32 [n_seq][W - 1], u_sample device fp32 [n_seq]:
+ *                uniform in [0, 1)
+ *   n_accepted   device int32 [n_seq]
+ *   tokens       device int32 [n_seq][W]: the accepted drafts, one sampled
+ *                token, -1 behind it
+ *   n_dropped    device int32 [n_seq] or NULL: drafts not accepted, whose
+ *                cells kvq_trim_step takes back
+ *
+ * Draft x at place i is accepted if all before it were and u_i * draft_i(x) <
+ * target_i(x), compared exactly; a token outside [0, vocab) never is.  Behind
+ * the accepted ones (a of them) one token is sampled: from max(target_a -
+ * draft_a, 0) if a draft was rejected there (certain drafts: from target_a
+ * without x), from target_a if none was left, and from target_a too where
+ * that difference is nowhere above 0.  Sampling is by the inverse of the
+ * cumulated weights in whole numbers: a weight r (in fp32; NaN and negative
+ * ones 0, above 1 one) counts floor(r * 2^40); with S their sum and U =
+ * floor(u_sample * 2^24) (held in [0, 2^24 - 1]) the token is the first whose
+ * cumulated count is above floor(S * U / 2^24); -1 if S is 0.  The result is
+ * bit-identical to that definition.
+ *
+ * 1 <= W <= 32, n_seq <= 65535 * 8, vocab <= 2^20, else KVQ_ERR_UNSUPPORTED.
+ * One launch, no workspace.
+ */
+kvq_status kvq_verify_draft(const void *target, const void *draft, int type, int64_t target_stride,
+                            int64_t draft_stride, int n_seq, int W, int vocab,
+                            const int32_t *draft_tokens, const int32_t *n_draft, const float *u,
+                            const float *u_sample, int32_t *n_accepted, int32_t *tokens,
+                            int32_t *n_dropped, void *stream);
+
+/*
+ * The last cells of sequences taken back (rejected drafts, a rollback): the
+ * lengths shrink, blocks no longer needed go back to the free list, in
+ * (sequence, column) order.  Table entries stay as they are, unread.
+ *
+ *   ctx_in        device int32 [n_seq]: cells each sequence holds
+ *   n_drop        device int32 [n_seq]: cells to take back, 0 .. ctx_in
+ *   block_table   device int32 [n_seq][max_blocks_per_seq], read
+ *   free_list     device int32 [n_blocks], updated in place above its top
+ *   free_count_in device int32 [1]
+ *   ctx_out       device int32 [n_seq]: ctx_in - n_drop
+ *   free_count_out device int32 [1]
+ *   info          device int32 [4], 16-byte aligned: cells taken back (held at
+ *                 2^31 - 1), 0, blocks given back, status
+ *
+ * A step with a broken argument changes nothing (ctx_out = ctx_in, info 0, 0,
+ * 0, status): KVQ_PLAN_ROW for a length below 0 or beyond its row or an
+ * n_drop outside [0, ctx_in], KVQ_PLAN_LIST as in kvq_plan_step.  Limits,
+ * overlap rules and errors as there.  One launch, no workspace.
+ */
+kvq_status kvq_trim_step(const int32_t *ctx_in, const int32_t *n_drop, int n_seq, int block_size,
+                         int n_blocks, const int32_t *block_table, int max_blocks_per_seq,
+                         int32_t *free_list, const int32_t *free_count_in, int32_t *ctx_out,
+                         int32_t *free_count_out, int32_t *info, void *stream);
 
 /* Static, human-readable name of a status code. */
 const char *kvq_status_string(int status);

@@ -29,6 +29,11 @@ KVQ_ERR_UNSUPPORTED = 2
 KVQ_ERR_WORKSPACE = 3
 KVQ_ERR_CUDA = 4
 
+# kvq_type: element types of the calls that take more than fp32
+KVQ_T_F32 = 0
+KVQ_T_F16 = 1
+KVQ_T_BF16 = 2
+
 # kvq_plan_step's status (info[3]): why a step was not placed
 KVQ_PLAN_TOKENS = 1
 KVQ_PLAN_ROW = 2
@@ -56,6 +61,9 @@ EXPORTED_SYMBOLS = (
     "kvq_sparse_workspace_bytes",
     "kvq_sparse_decode_attn",
     "kvq_sparse_decode_attn_lost_wait_test",
+    "kvq_append_rotary",
+    "kvq_verify_draft",
+    "kvq_trim_step",
     "kvq_status_string",
 )
 
@@ -77,6 +85,23 @@ class kvq_cache(ctypes.Structure):
         ("v_data", ctypes.c_void_p),
         ("k_scales", ctypes.c_void_p),
         ("v_scales", ctypes.c_void_p),
+    ]
+
+
+class kvq_rotary(ctypes.Structure):
+    """Mirror of `struct kvq_rotary` (make_rotary keeps its arrays alive)."""
+
+    _fields_ = [
+        ("type", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("gain", ctypes.c_float),
+        ("inv_freq", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_void_p),
+        ("q_norm", ctypes.c_void_p),
+        ("k_norm", ctypes.c_void_p),
     ]
 
 
@@ -143,6 +168,13 @@ def load_library(path: Optional[str] = None):
     lib.kvq_sparse_decode_attn_lost_wait_test.restype = I
     lib.kvq_sparse_decode_attn_lost_wait_test.argtypes = [CP, P, I, I, I, P, P, I, ctypes.c_float, P,
                                                           P, Z, ctypes.c_uint32, ctypes.c_uint32, P]
+    L, RP = ctypes.c_int64, ctypes.POINTER(kvq_rotary)
+    lib.kvq_append_rotary.restype = I
+    lib.kvq_append_rotary.argtypes = [CP, RP, P, P, P, L, L, L, I, I, P, P, P, P, I, I, P, P]
+    lib.kvq_verify_draft.restype = I
+    lib.kvq_verify_draft.argtypes = [P, P, I, L, L, I, I, I, P, P, P, P, P, P, P, P]
+    lib.kvq_trim_step.restype = I
+    lib.kvq_trim_step.argtypes = [P, P, I, I, I, P, I, P, P, P, P, P, P]
     lib.kvq_status_string.restype = ctypes.c_char_p
     lib.kvq_status_string.argtypes = [I]
     if path is None:
@@ -350,6 +382,42 @@ def kvq_sparse_decode_attn_lost_wait_test(cache: kvq_cache, q, n_seq: int, W: in
         ctypes.byref(cache), _ptr(q), n_seq, W, n_q, _ptr(sel_blocks), _ptr(sel_lens), n_sel,
         float(sm_scale), _ptr(out), _ptr(workspace), int(workspace_bytes), wait_limit,
         extra_tx_bytes, _stream(stream))
+
+
+def make_rotary(type: int, rot_dim: int, interleaved: bool, inv_freq, pair_axis=None, n_axes: int = 1,
+                q_norm=None, k_norm=None, eps: float = 0.0, gain: float = 1.0) -> kvq_rotary:
+    """Fill a kvq_rotary from tensors (or raw device addresses); tensors stay
+    alive as long as it does."""
+    r = kvq_rotary(type, rot_dim, int(interleaved), n_axes, eps, gain, _ptr(inv_freq), _ptr(pair_axis),
+                   _ptr(q_norm), _ptr(k_norm))
+    r.held = (inv_freq, pair_axis, q_norm, k_norm)
+    return r
+
+
+def kvq_append_rotary(cache: kvq_cache, rotary: kvq_rotary, q, k, v, q_stride: int, k_stride: int,
+                      v_stride: int, n_tok: int, n_q: int, tok_seq, tok_pos, positions, block_table,
+                      n_seq: int, max_blocks_per_seq: int, q_out, stream=None) -> int:
+    return load_library().kvq_append_rotary(
+        ctypes.byref(cache), ctypes.byref(rotary), _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride,
+        n_tok, n_q, _ptr(tok_seq), _ptr(tok_pos), _ptr(positions), _ptr(block_table), n_seq,
+        max_blocks_per_seq, _ptr(q_out), _stream(stream))
+
+
+def kvq_verify_draft(target, draft, type: int, target_stride: int, draft_stride: int, n_seq: int, W: int,
+                     vocab: int, draft_tokens, n_draft, u, u_sample, n_accepted, tokens, n_dropped=None,
+                     stream=None) -> int:
+    a = _ptrs(target, u_sample, n_accepted, tokens)
+    return load_library().kvq_verify_draft(a[0], _ptr(draft), type, target_stride, draft_stride, n_seq, W,
+                                           vocab, _ptr(draft_tokens), _ptr(n_draft), _ptr(u), a[1], a[2],
+                                           a[3], _ptr(n_dropped), _stream(stream))
+
+
+def kvq_trim_step(ctx_in, n_drop, n_seq: int, block_size: int, n_blocks: int, block_table,
+                  max_blocks_per_seq: int, free_list, free_count_in, ctx_out, free_count_out, info,
+                  stream=None) -> int:
+    a = _ptrs(ctx_in, n_drop, block_table, free_list, free_count_in, ctx_out, free_count_out, info)
+    return load_library().kvq_trim_step(a[0], a[1], n_seq, block_size, n_blocks, a[2], max_blocks_per_seq,
+                                        *a[3:], _stream(stream))
 
 
 def kvq_status_string(status: int) -> str:

@@ -770,6 +770,183 @@ KVQ_API kvq_status kvq_stream_fetch(const kvq_cache* host_copy, const kvq_cache*
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
+KVQ_API kvq_status kvq_append_rotary(const kvq_cache* cache, const kvq_rotary* rotary, const void* q,
+                                     const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                                     int64_t v_stride, int n_tok, int n_q, const int32_t* tok_seq,
+                                     const int32_t* tok_pos, const int32_t* positions,
+                                     const int32_t* block_table, int n_seq, int max_blocks_per_seq,
+                                     float* q_out, void* stream) {
+  kvq_status st = check_cache(cache);
+  if (st != KVQ_OK) return st;
+  if (rotary == nullptr || n_tok < 0 || n_q < 0) return KVQ_ERR_ARG;
+  const kvq_rotary& r = *rotary;
+  const int hd = cache->head_dim, n_kv = cache->n_kv_heads;
+  if (r.type != KVQ_T_F32 && r.type != KVQ_T_F16 && r.type != KVQ_T_BF16) return KVQ_ERR_ARG;
+  if (r.rot_dim < 0 || r.rot_dim > hd || r.rot_dim % 16 != 0) return KVQ_ERR_ARG;
+  if ((r.interleaved != 0 && r.interleaved != 1) || r.n_axes < 1 || r.n_axes > 8) return KVQ_ERR_ARG;
+  if (!(r.eps >= 0.0f) || isinf(r.eps) || !(r.gain == r.gain) || isinf(r.gain)) return KVQ_ERR_ARG;
+  if (r.rot_dim > 0 && r.inv_freq == nullptr) return KVQ_ERR_ARG;
+  if (!aligned(r.inv_freq, 16) || !aligned(r.pair_axis, 4) || !aligned(r.q_norm, 16) || !aligned(r.k_norm, 16))
+    return KVQ_ERR_ARG;
+  if (positions == nullptr && r.n_axes != 1) return KVQ_ERR_ARG;
+  if (n_tok == 0) return KVQ_OK;
+  if (k == nullptr || v == nullptr || tok_seq == nullptr || tok_pos == nullptr || block_table == nullptr ||
+      (n_q > 0 && (q == nullptr || q_out == nullptr)))
+    return KVQ_ERR_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || (n_q > 0 && (!aligned(q, 16) || !aligned(q_out, 16))) ||
+      !aligned(tok_seq, 4) || !aligned(tok_pos, 4) || !aligned(positions, 4) || !aligned(block_table, 4))
+    return KVQ_ERR_ARG;
+  const int per16 = r.type == KVQ_T_F32 ? 4 : 8;   // values in 16 bytes
+  const long long kv_row = (long long)n_kv * hd, q_row = (long long)n_q * hd;
+  if (k_stride < kv_row || v_stride < kv_row || k_stride % per16 != 0 || v_stride % per16 != 0)
+    return KVQ_ERR_ARG;
+  if (n_q > 0 && (q_stride < q_row || q_stride % per16 != 0)) return KVQ_ERR_ARG;
+  if (n_seq <= 0 || max_blocks_per_seq <= 0) return KVQ_ERR_ARG;
+  constexpr int64_t kMostStride = 1LL << 31;   // token * stride stays far below 2^63
+  if (k_stride > kMostStride || v_stride > kMostStride || (n_q > 0 && q_stride > kMostStride) ||
+      (long long)n_tok * (n_q + 2LL * n_kv) >= (1LL << 31))
+    return KVQ_ERR_UNSUPPORTED;
+  if (n_q > 0) {   // what is written is not read in the same call
+    const size_t size = r.type == KVQ_T_F32 ? 4 : 2, out = 4ull * n_tok * q_row;
+    const auto span = [&](int64_t stride, long long row) { return ((size_t)(n_tok - 1) * stride + row) * size; };
+    if (overlap(q_out, out, q, span(q_stride, q_row)) || overlap(q_out, out, k, span(k_stride, kv_row)) ||
+        overlap(q_out, out, v, span(v_stride, kv_row)))
+      return KVQ_ERR_ARG;
+  }
+  RotaryArgs a;
+  a.pool = make_pool(cache);
+  a.k_dst = cache->k_data;
+  a.v_dst = cache->v_data;
+  a.ks_dst = static_cast<__half*>(cache->k_scales);
+  a.vs_dst = static_cast<__half*>(cache->v_scales);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = q_out;
+  a.tok_seq = tok_seq;
+  a.tok_pos = tok_pos;
+  a.positions = positions;
+  a.block_table = block_table;
+  a.inv_freq = r.inv_freq;
+  a.pair_axis = r.pair_axis;
+  a.q_norm = r.q_norm;
+  a.k_norm = r.k_norm;
+  a.n_tok = n_tok;
+  a.n_q = n_q;
+  a.n_seq = n_seq;
+  a.max_blocks = max_blocks_per_seq;
+  a.n_axes = r.n_axes;
+  a.rot_dim = r.rot_dim;
+  a.interleaved = r.interleaved;
+  a.eps = r.eps;
+  a.gain = r.gain;
+  const int sms = sm_count();
+  const cudaError_t e = launch_append_rotary(cache->fmt, hd, r.type, a, sms > 0 ? sms : 148,
+                                             static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+KVQ_API kvq_status kvq_verify_draft(const void* target, const void* draft, int type, int64_t target_stride,
+                                    int64_t draft_stride, int n_seq, int W, int vocab,
+                                    const int32_t* draft_tokens, const int32_t* n_draft, const float* u,
+                                    const float* u_sample, int32_t* n_accepted, int32_t* tokens,
+                                    int32_t* n_dropped, void* stream) {
+  if (type != KVQ_T_F32 && type != KVQ_T_F16 && type != KVQ_T_BF16) return KVQ_ERR_ARG;
+  if (n_seq <= 0 || W <= 0 || vocab <= 0) return KVQ_ERR_ARG;
+  if (target == nullptr || u_sample == nullptr || n_accepted == nullptr || tokens == nullptr) return KVQ_ERR_ARG;
+  if (W > 1 && (draft_tokens == nullptr || u == nullptr)) return KVQ_ERR_ARG;
+  const size_t size = type == KVQ_T_F32 ? 4 : 2;
+  if (!aligned(target, size) || !aligned(draft, size) || !aligned(draft_tokens, 4) || !aligned(n_draft, 4) ||
+      !aligned(u, 4) || !aligned(u_sample, 4) || !aligned(n_accepted, 4) || !aligned(tokens, 4) ||
+      !aligned(n_dropped, 4))
+    return KVQ_ERR_ARG;
+  if (target_stride < vocab || (draft != nullptr && draft_stride < vocab)) return KVQ_ERR_ARG;
+  if (W > 32 || n_seq > 65535 * 8 || vocab > (1 << 20) || target_stride > (1LL << 31) ||
+      (draft != nullptr && draft_stride > (1LL << 31)))
+    return KVQ_ERR_UNSUPPORTED;
+  // what is written is not read in the same call, nor written twice
+  const struct { const void* p; size_t n; } in[] = {
+      {target, (((size_t)n_seq * W - 1) * target_stride + vocab) * size},
+      {draft, draft != nullptr && W > 1 ? (((size_t)n_seq * (W - 1) - 1) * draft_stride + vocab) * size : 0},
+      {draft_tokens, 4ull * n_seq * (W - 1)}, {n_draft, 4ull * n_seq}, {u, 4ull * n_seq * (W - 1)},
+      {u_sample, 4ull * n_seq}};
+  const struct { const void* p; size_t n; } out[] = {
+      {n_accepted, 4ull * n_seq}, {tokens, 4ull * n_seq * W}, {n_dropped, 4ull * n_seq}};
+  for (const auto& o : out) {
+    for (const auto& i : in)
+      if (i.n > 0 && overlap(i.p, i.n, o.p, o.n)) return KVQ_ERR_ARG;
+    for (const auto& p : out)
+      if (&p != &o && overlap(p.p, p.n, o.p, o.n)) return KVQ_ERR_ARG;
+  }
+  VerifyArgs a;
+  a.target = target;
+  a.draft = W > 1 ? draft : nullptr;
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.draft_tokens = draft_tokens;
+  a.n_draft = n_draft;
+  a.u = u;
+  a.u_sample = u_sample;
+  a.n_accepted = n_accepted;
+  a.tokens = tokens;
+  a.n_dropped = n_dropped;
+  a.n_seq = n_seq;
+  a.W = W;
+  a.vocab = vocab;
+  a.c_log2 = 0;
+  const int sms = sm_count();
+  const cudaError_t e = launch_verify_draft(type, a, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+KVQ_API kvq_status kvq_trim_step(const int32_t* ctx_in, const int32_t* n_drop, int n_seq, int block_size,
+                                 int n_blocks, const int32_t* block_table, int max_blocks_per_seq,
+                                 int32_t* free_list, const int32_t* free_count_in, int32_t* ctx_out,
+                                 int32_t* free_count_out, int32_t* info, void* stream) {
+  if (n_seq <= 0 || n_blocks <= 0 || max_blocks_per_seq <= 0) return KVQ_ERR_ARG;
+  if (block_size < 16 || block_size > 1024 || log2_exact(block_size) < 0) return KVQ_ERR_ARG;
+  if ((long long)n_blocks * block_size >= (1LL << 31) ||
+      (long long)max_blocks_per_seq * block_size >= (1LL << 31))
+    return KVQ_ERR_ARG;
+  if (ctx_in == nullptr || n_drop == nullptr || block_table == nullptr || free_list == nullptr ||
+      free_count_in == nullptr || ctx_out == nullptr || free_count_out == nullptr || info == nullptr)
+    return KVQ_ERR_ARG;
+  if (!aligned(ctx_in, 4) || !aligned(n_drop, 4) || !aligned(block_table, 4) || !aligned(free_list, 4) ||
+      !aligned(free_count_in, 4) || !aligned(ctx_out, 4) || !aligned(free_count_out, 4) || !aligned(info, 16))
+    return KVQ_ERR_ARG;
+  const struct { const void* p; size_t n; } in[] = {
+      {ctx_in, 4ull * n_seq}, {n_drop, 4ull * n_seq}, {free_count_in, 4},
+      {block_table, 4ull * n_seq * max_blocks_per_seq}};
+  const struct { const void* p; size_t n; } out[] = {
+      {ctx_out, 4ull * n_seq}, {free_count_out, 4}, {info, 16}, {free_list, 4ull * n_blocks}};
+  for (const auto& o : out) {
+    for (const auto& i : in)
+      if (overlap(i.p, i.n, o.p, o.n)) return KVQ_ERR_ARG;
+    for (const auto& p : out)
+      if (&p != &o && overlap(p.p, p.n, o.p, o.n)) return KVQ_ERR_ARG;
+  }
+  if (n_seq > kPlanMaxSeq) return KVQ_ERR_UNSUPPORTED;
+  TrimArgs a;
+  a.ctx_in = ctx_in;
+  a.n_drop = n_drop;
+  a.block_table = block_table;
+  a.free_list = free_list;
+  a.free_count_in = free_count_in;
+  a.ctx_out = ctx_out;
+  a.free_count_out = free_count_out;
+  a.info = info;
+  a.n_seq = n_seq;
+  a.max_blocks = max_blocks_per_seq;
+  a.bs_log2 = log2_exact(block_size);
+  a.n_blocks = n_blocks;
+  const int sms = sm_count();
+  const cudaError_t e = launch_trim_step(a, sms > 0 ? sms : 148, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
 KVQ_API const char* kvq_status_string(int status) {
   switch (status) {
     case KVQ_OK: return "KVQ_OK";

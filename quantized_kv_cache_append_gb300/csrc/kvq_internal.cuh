@@ -226,6 +226,61 @@ struct PlanArgs {
 constexpr int kPlanMaxSeq = 16384;   // three prefixes of it fit a CTA's shared memory
 constexpr int plan_smem_bytes(int n_seq) { return 3 * (n_seq + 1) * 4; }
 
+// The cells of rejected drafts taken back (kvq_plan.cu).
+struct TrimArgs {
+  const int32_t* ctx_in;       // [n_seq]
+  const int32_t* n_drop;       // [n_seq]
+  const int32_t* block_table;  // [n_seq][max_blocks]
+  int32_t* free_list;          // [n_blocks], written above its old top
+  const int32_t* free_count_in;
+  int32_t* ctx_out;            // [n_seq]
+  int32_t* free_count_out;
+  int32_t* info;               // [4]
+  int n_seq, max_blocks, bs_log2, n_blocks;
+};
+
+// Norm, rotation and append (kvq_rotary.cu).
+struct RotaryArgs {
+  Pool pool;
+  void* k_dst;
+  void* v_dst;
+  __half* ks_dst;
+  __half* vs_dst;
+  const void* q;               // rows of the input type
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;  // elements from token to token
+  float* q_out;                // [n_tok][n_q][hd]
+  const int32_t* tok_seq;
+  const int32_t* tok_pos;
+  const int32_t* positions;    // [n_axes][n_tok] or null
+  const int32_t* block_table;
+  const float* inv_freq;       // [rot_dim / 2]
+  const int32_t* pair_axis;    // [rot_dim / 2] or null
+  const float* q_norm;         // [hd] or null
+  const float* k_norm;
+  int n_tok, n_q, n_seq, max_blocks, n_axes, rot_dim, interleaved;
+  int parts;                   // warps that share a token's heads
+  FastDiv div_parts;
+  float eps, gain;
+};
+
+// Drafted tokens against the target's probabilities (kvq_verify.cu).
+struct VerifyArgs {
+  const void* target;          // rows of `vocab` probabilities
+  const void* draft;           // or null
+  long long target_stride, draft_stride;
+  const int32_t* draft_tokens; // [n_seq][W - 1]
+  const int32_t* n_draft;      // [n_seq] or null
+  const float* u;              // [n_seq][W - 1]
+  const float* u_sample;       // [n_seq]
+  int32_t* n_accepted;         // [n_seq]
+  int32_t* tokens;             // [n_seq][W]
+  int32_t* n_dropped;          // [n_seq] or null
+  int n_seq, W, vocab;
+  int c_log2;                  // 2^c_log2 CTAs share a sequence's row
+};
+
 // Bounds of the touched blocks' keys (kvq_bounds.cu).
 struct BoundArgs {
   Pool pool;
@@ -265,6 +320,9 @@ constexpr int kSelMaxSmem = 200 * 1024;
 // status from the runtime.
 cudaError_t launch_append(int fmt, int hd, const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_trim_step(const TrimArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_append_rotary(int fmt, int hd, int type, RotaryArgs a, int sms, cudaStream_t s);
+cudaError_t launch_verify_draft(int type, VerifyArgs a, int sms, cudaStream_t s);
 cudaError_t launch_bound_blocks(int fmt, int hd, const BoundArgs& a, int sms, cudaStream_t s);
 // Fills in the launch shape (wg_tok, n_wg, cluster, lead_rows); false if the
 // keys of one token do not fit the shared memory.

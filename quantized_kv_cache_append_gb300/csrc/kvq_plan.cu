@@ -1,5 +1,6 @@
 // kvq_plan.cu -- block tables and slot maps of one serving step, built on
-// the GPU from the requests' lengths (kvq_plan_step).
+// the GPU from the requests' lengths (kvq_plan_step), and the cells of
+// rejected drafts taken back (kvq_trim_step).
 //
 // Sequence b holds ceil(ctx_in[b] / block_size) blocks.  With n_new[b] >= 0
 // it grows to ceil((ctx_in[b] + n_new[b]) / block_size); with n_new[b] < 0
@@ -245,6 +246,91 @@ __global__ void __launch_bounds__(kPlanThreads) plan_step_kernel(PlanArgs a) {
   }
 }
 
+// kvq_trim_step: sequence b shrinks from ctx_in[b] to ctx_in[b] - n_drop[b]
+// cells; the blocks behind its last cell are pushed on the stack in
+// (sequence, column) order, block j of them found by a binary search in the
+// prefix sums of the counts, which every CTA computes for itself as above.
+struct Two {
+  uint32_t cells, back;
+};
+constexpr uint32_t kMostCells = 0x7fffffffu;
+
+__device__ __forceinline__ Two operator+(const Two& a, const Two& b) {
+  return {min(a.cells + b.cells, kMostCells), min(a.back + b.back, kMost)};
+}
+
+__device__ __forceinline__ Two of_trim(const TrimArgs& a, int ctx, int drop, bool& bad) {
+  if (ctx < 0 || drop < 0 || drop > ctx || (long long)ctx > (long long)a.max_blocks << a.bs_log2) {
+    bad = true;
+    return {0, 0};
+  }
+  const uint32_t up = (1u << a.bs_log2) - 1u;
+  return {(uint32_t)drop, (((uint32_t)ctx + up) >> a.bs_log2) - (((uint32_t)(ctx - drop) + up) >> a.bs_log2)};
+}
+
+__global__ void __launch_bounds__(kPlanThreads) trim_step_kernel(TrimArgs a) {
+  extern __shared__ uint32_t s_back[];   // inclusive prefixes of the blocks: end[b] at [b + 1]
+  __shared__ uint2 s_warp[kPlanWarps];
+  const int n = a.n_seq, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const long long count = __ldg(a.free_count_in);
+  // the sequences' counts, read in whole lines, then summed in runs of odd
+  // length (the runs start in different banks)
+  Two sum = {0, 0};
+  bool bad = false;
+#pragma unroll 4
+  for (int b = tid; b < n; b += kPlanThreads) {
+    const Two t = of_trim(a, __ldg(a.ctx_in + b), __ldg(a.n_drop + b), bad);
+    sum.cells = min(sum.cells + t.cells, kMostCells);
+    s_back[b + 1] = t.back;
+  }
+  __syncthreads();
+  const int per = (n + kPlanThreads - 1) / kPlanThreads | 1;
+  const int b0 = min(tid * per, n), b1 = min(b0 + per, n);
+  for (int b = b0; b < b1; ++b) sum.back = min(sum.back + s_back[b + 1], kMost);
+  Two incl = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const Two y = {__shfl_up_sync(kFullMask, incl.cells, d), __shfl_up_sync(kFullMask, incl.back, d)};
+    if (lane >= d) incl = incl + y;
+  }
+  if (lane == 31) s_warp[warp] = make_uint2(incl.cells, incl.back);
+  const bool any_bad = __syncthreads_or(bad);
+  Two base = {0, 0}, total = {0, 0};
+#pragma unroll
+  for (int w = 0; w < kPlanWarps; ++w) {
+    const uint2 v = s_warp[w];
+    if (w < warp) base = base + Two{v.x, v.y};
+    total = total + Two{v.x, v.y};
+  }
+  int status = any_bad ? KVQ_PLAN_ROW : 0;
+  if (count < 0 || count + (long long)total.back > a.n_blocks) status |= KVQ_PLAN_LIST;
+  const int gtid = blockIdx.x * kPlanThreads + tid, gthreads = gridDim.x * kPlanThreads;
+  const bool ok = status == 0;
+  for (int b = gtid; b < n; b += gthreads)
+    a.ctx_out[b] = __ldg(a.ctx_in + b) - (ok ? __ldg(a.n_drop + b) : 0);
+  if (gtid == 0) {
+    *a.free_count_out = (int32_t)(ok ? count + total.back : count);
+    *reinterpret_cast<int4*>(a.info) =
+        ok ? make_int4((int)total.cells, 0, (int)total.back, 0) : make_int4(0, 0, 0, status);
+  }
+  if (!ok) return;
+  uint32_t run = base.back + incl.back - sum.back;
+  for (int b = b0; b < b1; ++b) {
+    run += s_back[b + 1];
+    s_back[b + 1] = run;
+  }
+  if (tid == 0) s_back[0] = 0;
+  __syncthreads();
+  const int up = (1 << a.bs_log2) - 1;
+  for (uint32_t j = gtid; j < total.back; j += gthreads) {
+    const int b = owner_of(s_back + 1, n, j);
+    const int kept = (__ldg(a.ctx_in + b) - __ldg(a.n_drop + b) + up) >> a.bs_log2;
+    a.free_list[count + j] = __ldg(a.block_table + (size_t)b * a.max_blocks + kept + (j - s_back[b]));
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t s) {
@@ -273,6 +359,31 @@ cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, plan_step_kernel, a);
+}
+
+cudaError_t launch_trim_step(const TrimArgs& a, int sms, cudaStream_t s) {
+  static ContextCache<int> cache;
+  int ready = 0;
+  constexpr int kMostSmem = (kPlanMaxSeq + 1) * 4;
+  if (!per_context(cache, &ready, [](int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(trim_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMostSmem) == cudaSuccess;
+      }))
+    return cudaErrorInvalidConfiguration;
+  long long ctas = (a.n_seq + kPlanSeqPerCta - 1) / kPlanSeqPerCta;
+  if (ctas > kPlanPerSm * sms) ctas = kPlanPerSm * sms;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = (a.n_seq + 1) * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, trim_step_kernel, a);
 }
 
 }  // namespace kvq

@@ -10,9 +10,13 @@ import contextlib
 
 import torch
 
-from . import (KVQ_ERR_ARG, KVQ_F16, KVQ_GROUP, KVQ_K8V4, KVQ_Q4_BLOCK, KVQ_Q8, KvqError, check, kvq_append,
-               kvq_bound_blocks, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
+from . import (KVQ_ERR_ARG, KVQ_F16, KVQ_GROUP, KVQ_K8V4, KVQ_Q4_BLOCK, KVQ_Q8, KVQ_T_BF16, KVQ_T_F16,
+               KVQ_T_F32, KvqError, check, kvq_append, kvq_append_rotary, kvq_bound_blocks, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
                kvq_select_blocks, kvq_sparse_decode_attn, kvq_sparse_workspace_bytes, make_cache)
+
+
+# torch dtypes of the calls that take more than fp32
+ELEMENT_TYPES = {torch.float32: KVQ_T_F32, torch.float16: KVQ_T_F16, torch.bfloat16: KVQ_T_BF16}
 
 
 def on_stream(stream):
@@ -84,6 +88,35 @@ class PagedPool:
         check(kvq_append(self.cache, k, v, n_tok, tok_seq, tok_pos, block_table,
                          int(block_table.shape[0]), int(block_table.shape[1]), stream),
               "kvq_append")
+
+    def append_rotary(self, rotary, q, k, v, tok_seq, tok_pos, block_table, positions=None, q_out=None,
+                      stream=None):
+        """append of k and v [n_tok][n_kv][hd] with the norms and the rotation of
+        `rotary` (make_rotary); returns q [n_tok][n_q][hd] normed and rotated,
+        fp32.  The three may be views of one wider array (heads side by side,
+        tokens evenly apart).  Padding tokens' rows of q_out stay as they were
+        (a q_out allocated here: unset)."""
+        n_tok, n_q, hd = q.shape
+        if q.dtype not in ELEMENT_TYPES or ELEMENT_TYPES[q.dtype] != rotary.type:
+            raise KvqError(KVQ_ERR_ARG, f"append_rotary: q is {q.dtype}, which is not the rotary's type")
+        for name, t, n in (("q", q, n_q), ("k", k, self.n_kv), ("v", v, self.n_kv)):
+            if (t.dtype != q.dtype or t.device != self.k.device or tuple(t.shape) != (n_tok, n, self.head_dim)
+                    or (t.numel() and (t.stride(2) != 1 or (n > 1 and t.stride(1) != hd)))):
+                raise KvqError(KVQ_ERR_ARG, f"append_rotary: {name} must be [{n_tok}][{n}][{self.head_dim}] of "
+                                            f"{q.dtype} on {self.k.device}, each token's heads contiguous")
+        i32 = torch.int32
+        stride = lambda t: t.stride(0) if n_tok > 1 else t.shape[1] * hd
+        with self._on(stream):
+            if q_out is None:
+                q_out = torch.empty((n_tok, n_q, hd), dtype=torch.float32, device=q.device)
+            self._check("append_rotary", tok_seq=(tok_seq, i32, (n_tok,)), tok_pos=(tok_pos, i32, (n_tok,)),
+                        block_table=(block_table, i32, (None, None)),
+                        positions=(positions, i32, (rotary.n_axes, n_tok)),
+                        q_out=(q_out, torch.float32, (n_tok, n_q, hd)))
+            check(kvq_append_rotary(self.cache, rotary, q, k, v, stride(q), stride(k), stride(v), n_tok, n_q,
+                                    tok_seq, tok_pos, positions, block_table, int(block_table.shape[0]),
+                                    int(block_table.shape[1]), q_out, stream), "kvq_append_rotary")
+        return q_out
 
     def workspace_bytes(self, n_seq: int, W: int, n_q: int, max_ctx: int) -> int:
         return kvq_decode_workspace_bytes(self.cache, n_seq, W, n_q, max_ctx)

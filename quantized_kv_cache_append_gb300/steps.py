@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import torch
 
-from . import KvqError, KVQ_ERR_ARG, check, kvq_plan_step
+from . import KvqError, KVQ_ERR_ARG, check, kvq_plan_step, kvq_trim_step
 from .pool import on_stream
 
 
@@ -41,16 +41,19 @@ class StepPlanner:
         self.tok_seq, self.tok_pos, self.slots = (ints(max_tok, fill=-1) for _ in range(3))
         self.info = ints(4)
 
+    def _check(self, call: str, name: str, t) -> None:
+        if (t.shape != (self.n_seq,) or t.dtype != torch.int32 or not t.is_contiguous()
+                or t.device != self.info.device):
+            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: {name} must be a contiguous int32 [n_seq] on "
+                                        f"{self.info.device}")
+        if self.info.device.type != "cuda":
+            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: the planner is on {self.info.device}, not a GPU")
+
     def plan(self, n_new, stream=None) -> None:
         """n_new int32 [n_seq] on the device: tokens each sequence gets;
         negative: it ends and gives its blocks back.  A step that cannot be
         placed changes nothing and says why in info[3]."""
-        if (n_new.shape != (self.n_seq,) or n_new.dtype != torch.int32 or not n_new.is_contiguous()
-                or n_new.device != self.info.device):
-            raise KvqError(KVQ_ERR_ARG, "StepPlanner.plan: n_new must be a contiguous int32 [n_seq] on "
-                                        f"{self.info.device}")
-        if self.info.device.type != "cuda":
-            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.plan: the planner is on {self.info.device}, not a GPU")
+        self._check("plan", "n_new", n_new)
         with torch.cuda.device(self.info.device), on_stream(stream):
             self._before.copy_(self._after)
             check(kvq_plan_step(self.ctx_start, n_new, self.n_seq, self.block_size, self.n_blocks,
@@ -58,3 +61,15 @@ class StepPlanner:
                                 self.max_tok, self.ctx_lens, self.tok_start, self.tok_seq,
                                 self.tok_pos, self.slots, self.free_count, self.info, stream),
                   "kvq_plan_step")
+
+    def trim(self, n_drop, stream=None) -> None:
+        """n_drop int32 [n_seq] on the device: cells taken back from the end of
+        each sequence (verify_draft's n_dropped).  ctx_lens shrink (ctx_start
+        are the lengths before), blocks go back; info: cells taken back, 0,
+        blocks given back, status.  The plan's token arrays stay as they are."""
+        self._check("trim", "n_drop", n_drop)
+        with torch.cuda.device(self.info.device), on_stream(stream):
+            self._before.copy_(self._after)
+            check(kvq_trim_step(self.ctx_start, n_drop, self.n_seq, self.block_size, self.n_blocks,
+                                self.block_table, self.max_blocks, self.free_list, self._count_in,
+                                self.ctx_lens, self.free_count, self.info, stream), "kvq_trim_step")
