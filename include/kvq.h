@@ -26,6 +26,9 @@
  *   kvq_append_rotary
  *                    norms of each head's q and k, rotary positions, and the
  *                    append of k and v, in one pass
+ *   kvq_decode_attn_scored
+ *                    decode attention whose scores are capped by a tanh,
+ *                    biased by the distance, or kept to a window
  *   kvq_verify_draft drafted tokens accepted or replaced by the target's
  *                    probabilities, from given random numbers
  *   kvq_trim_step    the cells of rejected drafts taken back
@@ -703,6 +706,60 @@ kvq_status kvq_append_rotary(const kvq_cache *cache, const kvq_rotary *rotary, c
                              const int32_t *tok_pos, const int32_t *positions,
                              const int32_t *block_table, int n_seq, int max_blocks_per_seq,
                              float *q_out, void *stream);
+
+/*
+ * Scores of the attention calls below.  Query head h at position i gives cell
+ * j the score
+ *
+ *   s = (q . k_j) * sm_scale
+ *   s = softcap * tanh(s / softcap)          if softcap > 0
+ *   s = s - slopes[h] * |i - j|              if slopes
+ *
+ * and sees the cells j with
+ *
+ *   max(first, i - window + 1) <= j <= max(i, last)
+ *
+ * (first 0 and last i where NULL, no window where 0), below the context's
+ * length.  A token that sees no cell gets 0.
+ */
+typedef struct kvq_scores {
+    float softcap;         /* 0: none, else in [1e-3, 1e6]                     */
+    int32_t window;        /* >= 0; 0: none                                    */
+    const float *slopes;   /* device fp32 [n_q] or NULL                        */
+    const int32_t *first;  /* device int32 or NULL: decode [n_seq], chunk [T]  */
+    const int32_t *last;   /* device int32 or NULL: chunk [T]; decode: NULL    */
+} kvq_scores;
+
+/*
+ * kvq_decode_attn with such scores: arguments, formats, limits, workspace
+ * rules and errors as there, `first` per sequence (the first cell of a
+ * request behind padding, or of its document).  Token w of the window is at
+ * position ctx_lens[b] - W + w.  Only tiles that some token of the sequence
+ * sees are read, and a window bounds the workspace too.
+ * kvq_scored_workspace_bytes returns 0 for invalid arguments.
+ *
+ * Cells that no token of the sequence sees may hold anything; the values of
+ * cells that some of its tokens see and others do not (the edges of a verify
+ * window) must be finite.  Scores, softmax and sums are fp32, q and the
+ * weights enter the tensor cores as fp16 hi + lo pairs.
+ */
+size_t kvq_scored_workspace_bytes(const kvq_cache *cache, const kvq_scores *scores, int n_seq, int W,
+                                  int n_q, int max_ctx);
+kvq_status kvq_decode_attn_scored(const kvq_cache *cache, const kvq_scores *scores, const float *q,
+                                  int n_seq, int W, int n_q, const int32_t *ctx_lens, int max_ctx,
+                                  const int32_t *block_table, int max_blocks_per_seq,
+                                  float sm_scale, float *out, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
+ * kvq_decode_attn_scored with the failure path of its copy waits exercised,
+ * for tests of that path only, as kvq_decode_attn_lost_wait_test does.
+ */
+kvq_status kvq_decode_attn_scored_lost_wait_test(
+    const kvq_cache *cache, const kvq_scores *scores, const float *q, int n_seq, int W, int n_q,
+    const int32_t *ctx_lens, int max_ctx, const int32_t *block_table, int max_blocks_per_seq,
+    float sm_scale, float *out, void *workspace, size_t workspace_bytes, uint32_t wait_limit,
+    uint32_t extra_tx_bytes, void *stream);
 
 /*
  * Drafted tokens against the target's probabilities, by rejection sampling

@@ -62,6 +62,9 @@ EXPORTED_SYMBOLS = (
     "kvq_sparse_decode_attn",
     "kvq_sparse_decode_attn_lost_wait_test",
     "kvq_append_rotary",
+    "kvq_scored_workspace_bytes",
+    "kvq_decode_attn_scored",
+    "kvq_decode_attn_scored_lost_wait_test",
     "kvq_verify_draft",
     "kvq_trim_step",
     "kvq_status_string",
@@ -102,6 +105,18 @@ class kvq_rotary(ctypes.Structure):
         ("pair_axis", ctypes.c_void_p),
         ("q_norm", ctypes.c_void_p),
         ("k_norm", ctypes.c_void_p),
+    ]
+
+
+class kvq_scores(ctypes.Structure):
+    """Mirror of `struct kvq_scores` (make_scores keeps its arrays alive)."""
+
+    _fields_ = [
+        ("softcap", ctypes.c_float),
+        ("window", ctypes.c_int32),
+        ("slopes", ctypes.c_void_p),
+        ("first", ctypes.c_void_p),
+        ("last", ctypes.c_void_p),
     ]
 
 
@@ -171,6 +186,14 @@ def load_library(path: Optional[str] = None):
     L, RP = ctypes.c_int64, ctypes.POINTER(kvq_rotary)
     lib.kvq_append_rotary.restype = I
     lib.kvq_append_rotary.argtypes = [CP, RP, P, P, P, L, L, L, I, I, P, P, P, P, I, I, P, P]
+    SP, F = ctypes.POINTER(kvq_scores), ctypes.c_float
+    lib.kvq_scored_workspace_bytes.restype = Z
+    lib.kvq_scored_workspace_bytes.argtypes = [CP, SP, I, I, I, I]
+    lib.kvq_decode_attn_scored.restype = I
+    lib.kvq_decode_attn_scored.argtypes = [CP, SP, P, I, I, I, P, I, P, I, F, P, P, Z, P]
+    lib.kvq_decode_attn_scored_lost_wait_test.restype = I
+    lib.kvq_decode_attn_scored_lost_wait_test.argtypes = [CP, SP, P, I, I, I, P, I, P, I, F, P, P, Z,
+                                                          ctypes.c_uint32, ctypes.c_uint32, P]
     lib.kvq_verify_draft.restype = I
     lib.kvq_verify_draft.argtypes = [P, P, I, L, L, I, I, I, P, P, P, P, P, P, P, P]
     lib.kvq_trim_step.restype = I
@@ -401,6 +424,40 @@ def kvq_append_rotary(cache: kvq_cache, rotary: kvq_rotary, q, k, v, q_stride: i
         ctypes.byref(cache), ctypes.byref(rotary), _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride,
         n_tok, n_q, _ptr(tok_seq), _ptr(tok_pos), _ptr(positions), _ptr(block_table), n_seq,
         max_blocks_per_seq, _ptr(q_out), _stream(stream))
+
+
+def make_scores(softcap: float = 0.0, window: int = 0, slopes=None, first=None, last=None) -> kvq_scores:
+    """Fill a kvq_scores from tensors (or raw device addresses); tensors stay
+    alive as long as it does."""
+    s = kvq_scores(softcap, window, _ptr(slopes), _ptr(first), _ptr(last))
+    s.held = (slopes, first, last)
+    return s
+
+
+def kvq_scored_workspace_bytes(cache: kvq_cache, scores: kvq_scores, n_seq: int, W: int, n_q: int,
+                               max_ctx: int) -> int:
+    return int(load_library().kvq_scored_workspace_bytes(ctypes.byref(cache), ctypes.byref(scores), n_seq, W,
+                                                         n_q, max_ctx))
+
+
+def kvq_decode_attn_scored(cache: kvq_cache, scores: kvq_scores, q, n_seq: int, W: int, n_q: int, ctx_lens,
+                           max_ctx: int, block_table, max_blocks_per_seq: int, sm_scale: float, out,
+                           workspace, workspace_bytes: int, stream=None) -> int:
+    a = _ptrs(q, ctx_lens, block_table, out, workspace)
+    return load_library().kvq_decode_attn_scored(
+        ctypes.byref(cache), ctypes.byref(scores), a[0], n_seq, W, n_q, a[1], max_ctx, a[2],
+        max_blocks_per_seq, float(sm_scale), a[3], a[4], int(workspace_bytes), _stream(stream))
+
+
+def kvq_decode_attn_scored_lost_wait_test(cache: kvq_cache, scores: kvq_scores, q, n_seq: int, W: int,
+                                          n_q: int, ctx_lens, max_ctx: int, block_table,
+                                          max_blocks_per_seq: int, sm_scale: float, out, workspace,
+                                          workspace_bytes: int, wait_limit: int, extra_tx_bytes: int,
+                                          stream=None) -> int:
+    return load_library().kvq_decode_attn_scored_lost_wait_test(
+        ctypes.byref(cache), ctypes.byref(scores), _ptr(q), n_seq, W, n_q, _ptr(ctx_lens), max_ctx,
+        _ptr(block_table), max_blocks_per_seq, float(sm_scale), _ptr(out), _ptr(workspace),
+        int(workspace_bytes), wait_limit, extra_tx_bytes, _stream(stream))
 
 
 def kvq_verify_draft(target, draft, type: int, target_stride: int, draft_stride: int, n_seq: int, W: int,

@@ -72,6 +72,9 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // sequences 35.0 / 37.0 / 41.4 us, 64 FP16 sequences 170 / 170 / 181 us).
 constexpr int kListWaves = 1;
 
+// The three compilations of the decode kernels.
+enum class Decode { kDense, kLists, kScored };
+
 // Split plan: one wave of partial CTAs (as many as are resident per SM, on
 // every SM; four times that for batches, whose ragged lengths need short
 // splits to fill the tail of the launch) over all (sequence, KV head, row
@@ -80,19 +83,22 @@ constexpr int kListWaves = 1;
 // With max_bytes set, the split count is lowered until the workspace fits
 // (false if even one split per pair does not).  use_mma is 0 when the
 // kernel's one-time setup failed.
-// Block lists (lists): the plan of their own kernels, kListWaves waves; where
+// Scored decode: max_ctx is the most cells a sequence's splits cover
+// (scored_span).  Block lists: the plan of their own kernels, kListWaves waves; where
 // the partials do not fit max_bytes (a workspace sized for a larger batch, which
 // needed none) the splits meet in clusters instead (lists of 4096 cells: 8 FP16
 // ones 8.9 -> 12.3 us, 8 int8 ones 7.9 -> 14.0, 32 FP16 ones 15.7 either way).
 bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, DecodePlan* p,
-                 size_t max_bytes = SIZE_MAX, bool lists = false) {
+                 size_t max_bytes = SIZE_MAX, Decode kind = Decode::kDense) {
+  const bool lists = kind == Decode::kLists;
   const int G = n_q / c->n_kv_heads;
   p->rows = G * W;
   const int cta_rows = mma_rows_per_cta(c->head_dim);
   p->rt_rows = p->rows < cta_rows ? p->rows : cta_rows;
   p->n_rt = (p->rows + p->rt_rows - 1) / p->rt_rows;
-  int per_sm = lists ? lists_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows)
-                     : mma_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows);
+  int per_sm = lists                      ? lists_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows)
+               : kind == Decode::kScored ? scores_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows)
+                                          : mma_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows);
   p->use_mma = per_sm > 0;
   if (!p->use_mma) per_sm = 1;   // still a plan (and a workspace size); the launch is refused
   const int tile = mma_cell_tile();
@@ -235,6 +241,24 @@ KVQ_API size_t kvq_decode_workspace_bytes(const kvq_cache* cache, int n_seq, int
 namespace kvq {
 namespace {
 
+// kvq_scores as every scored call takes it.
+kvq_status check_scores(const kvq_scores* s) {
+  if (s == nullptr) return KVQ_ERR_ARG;
+  // (a cap of less would leave fp32's range on the way to the tanh and back)
+  if (s->softcap != 0.0f && !(s->softcap >= 1e-3f && s->softcap <= 1e6f)) return KVQ_ERR_ARG;
+  if (s->window < 0) return KVQ_ERR_ARG;
+  if (!aligned(s->slopes, 4) || !aligned(s->first, 4) || !aligned(s->last, 4)) return KVQ_ERR_ARG;
+  return KVQ_OK;
+}
+
+// The most cells the splits of a sequence cover: from the tile that holds the
+// first cell its window's first token sees, to its end.
+int scored_span(const kvq_scores& s, int W, int max_ctx) {
+  if (s.window <= 0 || s.window >= max_ctx) return max_ctx;
+  const long long span = (long long)s.window + W - 1 + mma_cell_tile() - 1;
+  return span < max_ctx ? (int)span : max_ctx;
+}
+
 // Validation, plan and launch of one decode call.  fit_plan: lower the split
 // count until the plan fits workspace_bytes (the static-scratch entry
 // point); otherwise the full plan must fit.
@@ -242,7 +266,8 @@ kvq_status decode_impl(const kvq_cache* cache, const float* q, int n_seq, int W,
                        const int32_t* ctx_lens, int max_ctx, const int32_t* block_table,
                        int max_blocks_per_seq, float sm_scale, float* out, void* workspace,
                        size_t workspace_bytes, void* stream, bool fit_plan,
-                       uint32_t wait_limit = kDefaultWaitLimit, uint32_t extra_tx = 0) {
+                       uint32_t wait_limit = kDefaultWaitLimit, uint32_t extra_tx = 0,
+                       const kvq_scores* scores = nullptr) {
   kvq_status st = check_cache(cache);
   if (st != KVQ_OK) return st;
   st = check_decode_shape(cache, n_seq, W, n_q, max_ctx, max_blocks_per_seq);
@@ -254,7 +279,8 @@ kvq_status decode_impl(const kvq_cache* cache, const float* q, int n_seq, int W,
   if (!(sm_scale == sm_scale) || isinf(sm_scale)) return KVQ_ERR_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return KVQ_ERR_WORKSPACE;
   DecodePlan plan;
-  if (!plan_decode(cache, n_seq, W, n_q, max_ctx, &plan, fit_plan ? workspace_bytes : SIZE_MAX))
+  if (!plan_decode(cache, n_seq, W, n_q, scores != nullptr ? scored_span(*scores, W, max_ctx) : max_ctx, &plan,
+                   fit_plan ? workspace_bytes : SIZE_MAX, scores != nullptr ? Decode::kScored : Decode::kDense))
     return fit_plan ? KVQ_ERR_WORKSPACE : KVQ_ERR_ARG;
   if (workspace_bytes < plan.bytes) return KVQ_ERR_WORKSPACE;
   if (!plan.use_mma) return KVQ_ERR_CUDA;   // the kernels' one-time setup failed
@@ -287,8 +313,25 @@ kvq_status decode_impl(const kvq_cache* cache, const float* q, int n_seq, int W,
   a.qscale = sm_scale * 1.4426950408889634f;  // log2(e)
   a.wait_limit = wait_limit;
   a.extra_tx = extra_tx;
-  const cudaError_t e = launch_decode_mma_partial(cache->fmt, cache->head_dim, plan, a,
-                                                  static_cast<cudaStream_t>(stream));
+  a.cap2 = a.cap2_inv = 0.0f;
+  a.slopes = nullptr;
+  a.first = nullptr;
+  a.window = 0;
+  a.whole = 1;
+  cudaError_t e;
+  if (scores != nullptr) {
+    if (scores->softcap > 0.0f) {
+      a.cap2 = scores->softcap * 1.4426950408889634f;
+      a.cap2_inv = 1.0f / a.cap2;
+    }
+    a.slopes = scores->slopes;
+    a.first = scores->first;
+    a.window = scores->window < max_ctx ? scores->window : 0;   // (as wide as the context: none)
+    a.whole = a.window == 0 && a.first == nullptr;
+    e = launch_decode_scores(cache->fmt, cache->head_dim, plan, a, static_cast<cudaStream_t>(stream));
+  } else {
+    e = launch_decode_mma_partial(cache->fmt, cache->head_dim, plan, a, static_cast<cudaStream_t>(stream));
+  }
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 
@@ -317,6 +360,42 @@ KVQ_API kvq_status kvq_decode_attn_lost_wait_test(const kvq_cache* cache, const 
   return kvq::decode_impl(cache, q, n_seq, W, n_q, ctx_lens, max_ctx, block_table,
                           max_blocks_per_seq, sm_scale, out, workspace, workspace_bytes, stream,
                           false, wait_limit, extra_tx_bytes);
+}
+
+KVQ_API size_t kvq_scored_workspace_bytes(const kvq_cache* cache, const kvq_scores* scores, int n_seq, int W,
+                                          int n_q, int max_ctx) {
+  if (check_cache(cache) != KVQ_OK || check_scores(scores) != KVQ_OK || scores->last != nullptr) return 0;
+  const int max_blocks = (max_ctx + cache->block_size - 1) / cache->block_size;
+  if (check_decode_shape(cache, n_seq, W, n_q, max_ctx, max_blocks > 0 ? max_blocks : 1) != KVQ_OK) return 0;
+  DecodePlan p;
+  if (!plan_decode(cache, n_seq, W, n_q, scored_span(*scores, W, max_ctx), &p, SIZE_MAX, Decode::kScored)) return 0;
+  return p.bytes;
+}
+
+KVQ_API kvq_status kvq_decode_attn_scored(const kvq_cache* cache, const kvq_scores* scores, const float* q,
+                                          int n_seq, int W, int n_q, const int32_t* ctx_lens, int max_ctx,
+                                          const int32_t* block_table, int max_blocks_per_seq,
+                                          float sm_scale, float* out, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  const kvq_status st = kvq::check_scores(scores);
+  if (st != KVQ_OK) return st;
+  if (scores->last != nullptr) return KVQ_ERR_ARG;
+  return kvq::decode_impl(cache, q, n_seq, W, n_q, ctx_lens, max_ctx, block_table, max_blocks_per_seq, sm_scale,
+                          out, workspace, workspace_bytes, stream, false, kDefaultWaitLimit, 0, scores);
+}
+
+KVQ_API kvq_status kvq_decode_attn_scored_lost_wait_test(
+    const kvq_cache* cache, const kvq_scores* scores, const float* q, int n_seq, int W, int n_q,
+    const int32_t* ctx_lens, int max_ctx, const int32_t* block_table, int max_blocks_per_seq, float sm_scale,
+    float* out, void* workspace, size_t workspace_bytes, uint32_t wait_limit, uint32_t extra_tx_bytes,
+    void* stream) {
+  const kvq_status st = kvq::check_scores(scores);
+  if (st != KVQ_OK) return st;
+  if (scores->last != nullptr) return KVQ_ERR_ARG;
+  if (wait_limit == 0 || wait_limit > kDefaultWaitLimit) return KVQ_ERR_ARG;
+  if (extra_tx_bytes == 0 || extra_tx_bytes > 4096 || extra_tx_bytes % 16 != 0) return KVQ_ERR_ARG;
+  return kvq::decode_impl(cache, q, n_seq, W, n_q, ctx_lens, max_ctx, block_table, max_blocks_per_seq, sm_scale,
+                          out, workspace, workspace_bytes, stream, false, wait_limit, extra_tx_bytes, scores);
 }
 
 namespace kvq {
@@ -353,7 +432,7 @@ KVQ_API size_t kvq_sparse_workspace_bytes(const kvq_cache* cache, int n_seq, int
   ListShape ls;
   if (check_lists(cache, n_seq, W, n_q, n_sel, &ls) != KVQ_OK) return 0;
   DecodePlan p;
-  if (!plan_decode(&ls.one, ls.n_lists, 1, ls.G, ls.max_ctx, &p, SIZE_MAX, true)) return 0;
+  if (!plan_decode(&ls.one, ls.n_lists, 1, ls.G, ls.max_ctx, &p, SIZE_MAX, Decode::kLists)) return 0;
   return p.bytes;
 }
 
@@ -375,7 +454,7 @@ kvq_status sparse_impl(const kvq_cache* cache, const float* q, int n_seq, int W,
   if (!(sm_scale == sm_scale) || isinf(sm_scale)) return KVQ_ERR_ARG;
   if (workspace == nullptr || !aligned(workspace, 256)) return KVQ_ERR_WORKSPACE;
   DecodePlan plan;
-  if (!plan_decode(&ls.one, ls.n_lists, 1, ls.G, ls.max_ctx, &plan, workspace_bytes, true))
+  if (!plan_decode(&ls.one, ls.n_lists, 1, ls.G, ls.max_ctx, &plan, workspace_bytes, Decode::kLists))
     return KVQ_ERR_WORKSPACE;
   if (!plan.use_mma) return KVQ_ERR_CUDA;
   DecodeArgs a;

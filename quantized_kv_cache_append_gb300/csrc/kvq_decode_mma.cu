@@ -53,19 +53,26 @@
 
 #include "kvq_internal.cuh"
 #include "kvq_ptx.cuh"
+#include "kvq_tanh.cuh"
 
-// This file is compiled twice.  As it stands it is the dense decode; included
-// by kvq_decode_lists.cu with KVQ_DECODE_LISTS set it is the decode over block
-// lists (kvq_sparse_decode_attn), whose work items are described at
-// DecodeArgs.
+// This file is compiled three times.  As it stands it is the dense decode;
+// included by kvq_decode_lists.cu with KVQ_DECODE_LISTS set it is the decode
+// over block lists (kvq_sparse_decode_attn), whose work items are described at
+// DecodeArgs; included by kvq_decode_scores.cu with KVQ_DECODE_SCORES set it
+// is the dense decode with capped, biased and windowed scores
+// (kvq_decode_attn_scored).
 #ifndef KVQ_DECODE_LISTS
 #define KVQ_DECODE_LISTS 0
+#endif
+#ifndef KVQ_DECODE_SCORES
+#define KVQ_DECODE_SCORES 0
 #endif
 
 namespace kvq {
 namespace {
 
 constexpr bool kLists = KVQ_DECODE_LISTS != 0;
+constexpr bool kScores = KVQ_DECODE_SCORES != 0;
 constexpr int kConsumerWarps = 4;
 constexpr int kThreads = kConsumerWarps * 32;  // thread 0 also issues the copies
 constexpr int kTC = 64;                      // cells per pipeline stage (a piece index is
@@ -77,8 +84,8 @@ constexpr float kTau = 8.0f;                 // lazy rescale threshold (log2 uni
 // lo halves of p (times the V scale, often below 0.05) clear of fp16's
 // subnormals (int8 cache, 16 ragged lists of 4096 cells: relative output
 // error 3.2e-6 without, below 1e-6 with it) at the price of a rescale
-// whenever the maximum rises at all.
-constexpr float kBelowMax = kLists ? kTau : 0.0f;
+// whenever the maximum rises at all.  Scored decode: as block lists.
+constexpr float kBelowMax = kLists || kScores ? kTau : 0.0f;
 // int8 and K8V4 fold the V scale into p before the fp16 split: 2^kTau times a
 // scale of kScaleMost stays below fp16's 65504.  Cells with a larger one have
 // p at most 1 (see softmax).  Looking for them costs the dense decode 0-1 %
@@ -88,9 +95,9 @@ constexpr uint32_t kScaleMost = 0x5800u;   // fp16 bits of 128
 // int8 K in q.k.  Dense: as 1152 + code, the 1152 * sum(q) taken off through
 // the accumulator's start (no subtraction per element).  The sums then run
 // at 1152 times the codes' weight and leave a logit error of up to about
-// 1e-5; block lists subtract first (4 HSUB2 more per 16 x 16 tile) and keep
-// it at the FP16 cache's 1e-6.
-constexpr bool kCodesExact = kLists;
+// 1e-5; block lists and scored decode subtract first (4 HSUB2 more per 16 x
+// 16 tile) and keep it at the FP16 cache's 1e-6.
+constexpr bool kCodesExact = kLists || kScores;
 constexpr unsigned kFull = 0xffffffffu;
 
 template <int FMT, int HD, int NT>
@@ -194,6 +201,35 @@ __device__ __forceinline__ int clamp_len_mma(int L, const DecodeArgs& a) {
   return L < 0 ? 0 : (int)((long long)L < cap ? L : cap);
 }
 
+// First and last cell of a sequence's splits.  Scored decode: the first is the
+// tile that holds the first cell any of its query tokens sees (the window's
+// first token's).
+struct Span {
+  int base, end;
+};
+
+// first cell that query token w of sequence b sees
+__device__ __forceinline__ int first_seen(const DecodeArgs& a, int b, int L, int w) {
+  int lo = a.first != nullptr ? max(__ldg(a.first + b), 0) : 0;
+  if (a.window > 0) lo = (int)max((long long)lo, (long long)L - a.W + w - a.window + 1);
+  return lo;
+}
+
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int b, int L_raw) {
+  if (!kScores || a.whole) return {0, clamp_len_mma(L_raw, a)};
+  const long long cap = (long long)a.max_blocks << a.pool.bs_log2;
+  const int L = L_raw < 0 ? 0 : (int)min((long long)L_raw, cap);
+  const int base = min(first_seen(a, b, L, 0), L) & ~(kTC - 1);
+  return {base, (int)min((long long)L, base + (long long)a.nsplit * a.split_cells)};
+}
+
+// The cell count the query tokens' positions go by (span_of's end may be cut
+// short by the plan, this is not).
+__device__ __forceinline__ int context_of(const DecodeArgs& a, int L_raw) {
+  if (!kScores || a.whole) return clamp_len_mma(L_raw, a);
+  const long long cap = (long long)a.max_blocks << a.pool.bs_log2;
+  return L_raw < 0 ? 0 : (int)min((long long)L_raw, cap);
+}
 
 // Block id of cell c (-1 past the end).  Loaded a tile ahead of its use and
 // only tested when used, so the load latency stays hidden.
@@ -216,7 +252,8 @@ __device__ __forceinline__ bool item_of(const DecodeArgs& a, int c, int& b, int&
       const int bb = b0 + lane;
       int n = 0, Lb = 0;
       if (bb < a.n_seq) {
-        Lb = clamp_len_mma(__ldg(a.ctx_lens + bb), a);
+        const Span sp = span_of(a, bb, __ldg(a.ctx_lens + bb));
+        Lb = sp.end - sp.base;
         const int qs = (int)fdiv((unsigned)Lb, a.div_split);   // Lb / S (Lb >= 0)
         n = pass == 0 ? qs * nkv : (Lb - qs * S != 0 ? nkv : 0);
       }
@@ -415,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     // ids read here may still change before the wait below (the copies
     // read them again after the wait), and a prefetch of the wrong rows
     // costs bandwidth, nothing else.
-    if (a.n_seq == 1 && a.n_rt == 1 && !kLists) {
+    if (a.n_seq == 1 && a.n_rt == 1 && !kLists && (!kScores || a.whole)) {
       const int split0 = (int)fdiv(blockIdx.x, a.div_nkv), kvh0 = (int)blockIdx.x - split0 * a.n_kv;
       const int c0 = split0 * a.split_cells;
       const int pcl = a.pool.bs_log2 < 6 ? a.pool.bs_log2 : 6;
@@ -481,12 +518,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   }
   // the KV head's place in the pool
   const int pool_h = kLists ? b - (int)fdiv((unsigned)b, a.div_heads) * a.pool.n_kv : kvh;
-  const int c_begin = split * a.split_cells;
+  const Span span = kScores && !a.whole ? span_of(a, b, L_raw) : Span{0, 0};
+  const int c_begin = span.base + split * a.split_cells;
   // until the length is known (one sequence), copies stay inside the split
   // and the block table
-  int c_end = min(clamp_len_mma(single ? INT_MAX : L_raw, a), c_begin + a.split_cells);
+  int c_end = min(kScores && !a.whole ? span.end : clamp_len_mma(single ? INT_MAX : L_raw, a),
+                  c_begin + a.split_cells);
   int n_tiles = (c_end - c_begin + kTC - 1) / kTC;
-  if (kLists && n_tiles < 0) n_tiles = 0;   // (an empty split of a cluster)
+  if ((kLists || kScores) && n_tiles < 0) n_tiles = 0;   // (an empty split of a cluster, or past a window)
   const int n_first = n_tiles < C::STAGES ? n_tiles : C::STAGES;   // tiles of the first wave
   const int pc_log2 = a.pool.bs_log2 < 6 ? a.pool.bs_log2 : 6;  // cells per TMA piece
   const int n_pieces = kTC >> pc_log2;
@@ -644,9 +683,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     }
   }
   __syncthreads();
-  const int L = clamp_len_mma(L_raw, a);
+  const int L = context_of(a, L_raw);
   if (single) {
-    c_end = min(L, c_begin + a.split_cells);
+    c_end = min(kScores && !a.whole ? span.end : L, c_begin + a.split_cells);
     n_tiles = c_end > c_begin ? (c_end - c_begin + kTC - 1) / kTC : 0;
     // (a cluster's empty splits go through the merge with nothing to add)
     if (n_tiles == 0 && !clustered) {
@@ -728,6 +767,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       if (row_of(nt, j) < Rc) row_last_min = min(row_last_min, row_last[nt][j]);
+
+  // Scored: the first cell each row sees, its slope (log2 domain), and its
+  // position before the context's end
+  int row_lo[kScores ? NT : 1][2], row_lo_max = 0, lo_all = 0;
+  float row_slope[kScores ? NT : 1][2], row_back[kScores ? NT : 1][2];
+  if constexpr (kScores) {
+    lo_all = first_seen(a, b, L, 0);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = row_of(nt, j), w = div_g(a, r0 + r);
+        row_lo[nt][j] = r < Rc ? first_seen(a, b, L, w) : 0;
+        row_lo_max = max(row_lo_max, row_lo[nt][j]);
+        row_back[nt][j] = (float)(a.W - w);
+        row_slope[nt][j] = r < Rc && a.slopes != nullptr
+                               ? 1.4426950408889634f * __ldg(a.slopes + kvh * a.G + (r0 + r - w * a.G))
+                               : 0.f;
+      }
+  }
 
   float m[NT][2], l[NT][2];
   float o[KS][NT][4];
@@ -964,12 +1023,51 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
         if (g >= nvalid) x[0] = 0;
         if (g + 8 >= nvalid) x[1] = 0;
       }
+      if (kScores && lo_all > cw0) {
+        if (g < lo_all - cw0) x[0] = 0;
+        if (g + 8 < lo_all - cw0) x[1] = 0;
+      }
       large = ((x[0] | x[1]) & 0x80008000u) != 0;
     }
     const float tau = large ? 0.f : kTau;
     // padding rows never reach the output, so only a short slice or a causal
     // limit inside it needs masks
-    const bool need_mask = nvalid < kCellsPerWarp || row_last_min - cw0 < kCellsPerWarp - 1;
+    const bool need_mask = nvalid < kCellsPerWarp || row_last_min - cw0 < kCellsPerWarp - 1 ||
+                           (kScores && row_lo_max > cw0);
+    if constexpr (kScores) {
+      if (a.cap2 != 0.f) {
+        bool wide = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            z[nt][k] *= a.cap2_inv;
+            wide |= fabsf(z[nt][k]) > kTanhSmall;
+          }
+        if (__any_sync(kFull, wide)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[nt][k] = a.cap2 * tanh_any(z[nt][k]);
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[nt][k] = a.cap2 * tanh_small(z[nt][k]);
+        }
+      }
+      if (a.slopes != nullptr) {
+        const float at = (float)(cw0 + g - L);   // of cell g; a row's position is L - its row_back
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float d = at + row_back[nt][j];   // cell - position: <= 0 where it is seen
+            z[nt][j] = fmaf(row_slope[nt][j], d, z[nt][j]);
+            z[nt][2 + j] = fmaf(row_slope[nt][j], d + 8.0f, z[nt][2 + j]);
+          }
+      }
+    }
   // ---------------- masks and online softmax ----------------
   // A row's maximum over the slice (8 lanes) is needed only when the
   // reference maximum must rise; that happens only if some lane's own
@@ -995,8 +1093,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     for (int j = 0; j < 2; ++j) {
       if (need_mask) {
         const int vis = min(nvalid - 1, row_last[nt][j] - cw0);  // last visible slice index
-        if (g > vis) z[nt][j] = kNegInf;
-        if (g + 8 > vis) z[nt][2 + j] = kNegInf;
+        const int low = kScores ? row_lo[nt][j] - cw0 : 0;       // first one
+        if (g > vis || (kScores && g < low)) z[nt][j] = kNegInf;
+        if (g + 8 > vis || (kScores && g + 8 < low)) z[nt][2 + j] = kNegInf;
       }
       lmax[nt][j] = fmaxf(z[nt][j], z[nt][2 + j]);
       rise |= lmax[nt][j] > m[nt][j] + tau;  // also true for the first finite maximum
@@ -1037,7 +1136,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   };
 
   // o += V^T . P^T for one stage
-  auto pv = [&](int s, int nvalid, const float (&p)[NT][4], const uint32_t (&vw)[2][VSW]) {
+  // (scored: cells below nlow, which no row sees, may hold anything too)
+  auto pv = [&](int s, int nvalid, int nlow, const float (&p)[NT][4], const uint32_t (&vw)[2][VSW]) {
     const uint32_t st = sbase + s * C::STAGE_B;
   // ---------------- O^T += V^T . P^T ----------------
   if constexpr (FMT == KVQ_F16) {
@@ -1058,14 +1158,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       }
     }
     // V rows of cells past the valid ones may hold anything: zero them.
-    const uint32_t mlo = (2 * t < nvalid ? 0xffffu : 0u) | (2 * t + 1 < nvalid ? 0xffff0000u : 0u);
-    const uint32_t mhi =
-        (2 * t + 8 < nvalid ? 0xffffu : 0u) | (2 * t + 9 < nvalid ? 0xffff0000u : 0u);
+    const auto keeps = [&](int i) -> bool { return i < nvalid && (!kScores || i >= nlow); };
+    const uint32_t mlo = (keeps(2 * t) ? 0xffffu : 0u) | (keeps(2 * t + 1) ? 0xffff0000u : 0u);
+    const uint32_t mhi = (keeps(2 * t + 8) ? 0xffffu : 0u) | (keeps(2 * t + 9) ? 0xffff0000u : 0u);
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) {
       uint32_t af[4];
       ldsm_x4_t(af, st + vx[mt & 3] + (uint32_t)(mt >> 2) * kSpanB);
-      if (nvalid < kCellsPerWarp) {
+      if (nvalid < kCellsPerWarp || (kScores && nlow > 0)) {
         af[0] &= mlo;
         af[1] &= mlo;
         af[2] &= mhi;
@@ -1255,7 +1355,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     load_scales(sn, vn);
     float zn[NT][4];
     qk(sn, zn);
-    pv(it % C::STAGES, nv_cur, p_cur, vw);
+    pv(it % C::STAGES, nv_cur, lo_all - (c_begin + it * kTC + cl), p_cur, vw);
     release(it);
     softmax(nv_next, c_begin + (it + 1) * kTC + cl, vn, zn, p_cur);
     nv_cur = nv_next;
@@ -1263,7 +1363,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     for (int i = 0; i < 2 * VSW; ++i) vw[i / VSW][i % VSW] = vn[i / VSW][i % VSW];
   }
   if (!lost && n_tiles > 0) {  // the last tile
-    pv(it % C::STAGES, nv_cur, p_cur, vw);
+    pv(it % C::STAGES, nv_cur, lo_all - (c_begin + it * kTC + cl), p_cur, vw);
     release(it);
   }
   if (producer) {
@@ -1441,10 +1541,11 @@ __global__ void __launch_bounds__(kCombineThreads, 4) combine_partials(DecodeArg
   const int d = d0 + 4 * dv;
   // one sequence: every split slot is written (splits past the context say
   // "no cells"), so the context length need not be read
-  const int nlive = !kLists && a.n_seq == 1 ? a.nsplit
-                                 : (int)fdiv((unsigned)(clamp_len_mma(__ldg(a.ctx_lens + b), a) +
-                                                        a.split_cells - 1),
-                                             a.div_split);
+  int nlive = a.nsplit;
+  if (kLists || a.n_seq > 1) {
+    const Span sp = span_of(a, b, __ldg(a.ctx_lens + b));
+    nlive = (int)fdiv((unsigned)(sp.end - sp.base + a.split_cells - 1), a.div_split);
+  }
   const size_t base0 = ((size_t)b * a.n_kv + kvh) * a.nsplit;
 
   float M = kNegInf, lsum = 0.f;
@@ -1690,7 +1791,7 @@ cudaError_t launch_hd(int code, const DecodePlan& p, const DecodeArgs& a, cudaSt
 
 }  // namespace
 
-#if !KVQ_DECODE_LISTS
+#if !KVQ_DECODE_LISTS && !KVQ_DECODE_SCORES
 
 void* tensor_map_encoder() {
   static void* fn = nullptr;
@@ -1747,11 +1848,14 @@ int mma_rows_per_cta(int hd) { return 8 * (256 / hd); }
 
 int mma_cell_tile() { return kTC; }
 
-#endif  // !KVQ_DECODE_LISTS
+#endif  // the dense decode
 
 #if KVQ_DECODE_LISTS
 #define KVQ_CTAS_PER_SM lists_ctas_per_sm
 #define KVQ_LAUNCH launch_decode_lists
+#elif KVQ_DECODE_SCORES
+#define KVQ_CTAS_PER_SM scores_ctas_per_sm
+#define KVQ_LAUNCH launch_decode_scores
 #else
 #define KVQ_CTAS_PER_SM mma_ctas_per_sm
 #define KVQ_LAUNCH launch_decode_mma_partial

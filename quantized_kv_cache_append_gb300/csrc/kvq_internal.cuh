@@ -180,6 +180,12 @@ struct DecodeArgs {
   uint32_t wait_limit; // polls of a copy wait before it is declared lost
   uint32_t extra_tx;   // bytes added to each stage's expected count (0; >0 only
                        // in the failure-path test, where no copy delivers them)
+  // Scored decode (kvq_decode_attn_scored), unread elsewhere.
+  float cap2, cap2_inv;  // softcap * log2(e) and its inverse; 0: no cap
+  const float* slopes; // [n_q] or null
+  const int32_t* first;  // [n_seq] or null
+  int window;          // 0: none
+  int whole;           // no window and no first cells: split 0 begins at cell 0
 };
 
 struct CompactArgs {
@@ -343,6 +349,10 @@ cudaError_t launch_decode_mma_partial(int fmt, int hd, const DecodePlan& p, cons
 // The same over block lists (kvq_decode_lists.cu).
 int lists_ctas_per_sm(int fmt, int hd, int rows);
 cudaError_t launch_decode_lists(int fmt, int hd, const DecodePlan& p, const DecodeArgs& a, cudaStream_t s);
+
+// The same with capped, biased and windowed scores (kvq_decode_scores.cu).
+int scores_ctas_per_sm(int fmt, int hd, int rows);
+cudaError_t launch_decode_scores(int fmt, int hd, const DecodePlan& p, const DecodeArgs& a, cudaStream_t s);
 
 // The driver's cuTensorMapEncodeTiled (version 12000), looked up once; null
 // if the driver does not provide it.

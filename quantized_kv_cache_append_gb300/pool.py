@@ -11,7 +11,8 @@ import contextlib
 import torch
 
 from . import (KVQ_ERR_ARG, KVQ_F16, KVQ_GROUP, KVQ_K8V4, KVQ_Q4_BLOCK, KVQ_Q8, KVQ_T_BF16, KVQ_T_F16,
-               KVQ_T_F32, KvqError, check, kvq_append, kvq_append_rotary, kvq_bound_blocks, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
+               KVQ_T_F32, KvqError, check, kvq_append, kvq_append_rotary, kvq_bound_blocks, kvq_decode_attn_scored,
+               kvq_scored_workspace_bytes, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
                kvq_select_blocks, kvq_sparse_decode_attn, kvq_sparse_workspace_bytes, make_cache)
 
 
@@ -133,6 +134,29 @@ class PagedPool:
             check(kvq_decode_attn(self.cache, q, n_seq, W, n_q, ctx_lens, max_ctx, block_table,
                                   int(block_table.shape[1]), sm_scale, out, workspace,
                                   workspace.numel(), stream), "kvq_decode_attn")
+        return out
+
+    def decode_scored(self, q, ctx_lens, max_ctx: int, block_table, sm_scale: float, scores, out=None,
+                      workspace=None, stream=None):
+        """decode with capped, biased or windowed scores (make_scores)."""
+        n_seq, W, n_q, hd = q.shape
+        f32, i32 = torch.float32, torch.int32
+        with self._on(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                need = kvq_scored_workspace_bytes(self.cache, scores, n_seq, W, n_q, max_ctx)
+                workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+            slopes, first, last = getattr(scores, "held", (None, None, None))
+            held = {n: (t, dt, shape) for n, t, dt, shape in (("slopes", slopes, f32, (n_q,)),
+                                                             ("first", first, i32, (n_seq,)))
+                    if isinstance(t, torch.Tensor)}
+            self._check("decode_scored", q=(q, f32, (n_seq, W, n_q, self.head_dim)),
+                        ctx_lens=(ctx_lens, i32, (n_seq,)), block_table=(block_table, i32, (n_seq, None)),
+                        out=(out, f32, (n_seq, W, n_q, hd)), workspace=(workspace, torch.uint8, (None,)), **held)
+            check(kvq_decode_attn_scored(self.cache, scores, q, n_seq, W, n_q, ctx_lens, max_ctx, block_table,
+                                         int(block_table.shape[1]), sm_scale, out, workspace,
+                                         workspace.numel(), stream), "kvq_decode_attn_scored")
         return out
 
     def compact(self, block_table_row, n_cells: int, out_k=None, out_v=None, stream=None):
