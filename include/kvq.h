@@ -26,9 +26,9 @@
  *   kvq_append_rotary
  *                    norms of each head's q and k, rotary positions, and the
  *                    append of k and v, in one pass
- *   kvq_decode_attn_scored
- *                    decode attention whose scores are capped by a tanh,
- *                    biased by the distance, or kept to a window
+ *   kvq_decode_attn_scored / kvq_chunk_attn_scored
+ *                    attention whose scores are capped by a tanh, biased by
+ *                    the distance, or kept to a window, document or prefix
  *   kvq_verify_draft drafted tokens accepted or replaced by the target's
  *                    probabilities, from given random numbers
  *   kvq_trim_step    the cells of rejected drafts taken back
@@ -760,6 +760,32 @@ kvq_status kvq_decode_attn_scored_lost_wait_test(
     const int32_t *ctx_lens, int max_ctx, const int32_t *block_table, int max_blocks_per_seq,
     float sm_scale, float *out, void *workspace, size_t workspace_bytes, uint32_t wait_limit,
     uint32_t extra_tx_bytes, void *stream);
+
+/*
+ * kvq_chunk_attn with such scores: token t of the chunk is at position P - T
+ * + t; `first` [T] keeps it to its document, `last` [T] lets a token of a
+ * bidirectional prefix see the prefix's later tokens (up to P - 1).
+ *
+ *   out        device [T][n_q][head_dim] of out_type (kvq_type), 16-byte
+ *              aligned
+ *
+ * Keys no row of a 128-row tile sees are not read.  The values of the whole
+ * staging must be finite.  Everything else as kvq_chunk_attn; the weights
+ * enter the tensor cores as one fp16 value each.
+ */
+kvq_status kvq_chunk_attn_scored(const void *k16, const void *v16, int n_kv_heads, int P,
+                                 int head_dim, const kvq_scores *scores, const float *q, int T,
+                                 int n_q, float sm_scale, void *out, int out_type, void *stream);
+
+/*
+ * kvq_chunk_attn_scored with the failure path of its waits exercised, for
+ * tests of that path only, as kvq_chunk_attn_lost_wait_test does.
+ */
+kvq_status kvq_chunk_attn_scored_lost_wait_test(const void *k16, const void *v16, int n_kv_heads,
+                                                int P, int head_dim, const kvq_scores *scores,
+                                                const float *q, int T, int n_q, float sm_scale,
+                                                void *out, int out_type, uint32_t wait_limit,
+                                                uint32_t extra_tx_bytes, void *stream);
 
 /*
  * Drafted tokens against the target's probabilities, by rejection sampling

@@ -65,6 +65,8 @@ EXPORTED_SYMBOLS = (
     "kvq_scored_workspace_bytes",
     "kvq_decode_attn_scored",
     "kvq_decode_attn_scored_lost_wait_test",
+    "kvq_chunk_attn_scored",
+    "kvq_chunk_attn_scored_lost_wait_test",
     "kvq_verify_draft",
     "kvq_trim_step",
     "kvq_status_string",
@@ -194,6 +196,11 @@ def load_library(path: Optional[str] = None):
     lib.kvq_decode_attn_scored_lost_wait_test.restype = I
     lib.kvq_decode_attn_scored_lost_wait_test.argtypes = [CP, SP, P, I, I, I, P, I, P, I, F, P, P, Z,
                                                           ctypes.c_uint32, ctypes.c_uint32, P]
+    lib.kvq_chunk_attn_scored.restype = I
+    lib.kvq_chunk_attn_scored.argtypes = [P, P, I, I, I, SP, P, I, I, F, P, I, P]
+    lib.kvq_chunk_attn_scored_lost_wait_test.restype = I
+    lib.kvq_chunk_attn_scored_lost_wait_test.argtypes = [P, P, I, I, I, SP, P, I, I, F, P, I, ctypes.c_uint32,
+                                                         ctypes.c_uint32, P]
     lib.kvq_verify_draft.restype = I
     lib.kvq_verify_draft.argtypes = [P, P, I, L, L, I, I, I, P, P, P, P, P, P, P, P]
     lib.kvq_trim_step.restype = I
@@ -458,6 +465,21 @@ def kvq_decode_attn_scored_lost_wait_test(cache: kvq_cache, scores: kvq_scores, 
         ctypes.byref(cache), ctypes.byref(scores), _ptr(q), n_seq, W, n_q, _ptr(ctx_lens), max_ctx,
         _ptr(block_table), max_blocks_per_seq, float(sm_scale), _ptr(out), _ptr(workspace),
         int(workspace_bytes), wait_limit, extra_tx_bytes, _stream(stream))
+
+
+def kvq_chunk_attn_scored(k16, v16, n_kv_heads: int, P: int, head_dim: int, scores: kvq_scores, q, T: int,
+                          n_q: int, sm_scale: float, out, out_type: int = KVQ_T_F32, stream=None) -> int:
+    a = _ptrs(k16, v16, q, out)
+    return load_library().kvq_chunk_attn_scored(a[0], a[1], n_kv_heads, P, head_dim, ctypes.byref(scores), a[2],
+                                                T, n_q, float(sm_scale), a[3], out_type, _stream(stream))
+
+
+def kvq_chunk_attn_scored_lost_wait_test(k16, v16, n_kv_heads: int, P: int, head_dim: int, scores: kvq_scores,
+                                         q, T: int, n_q: int, sm_scale: float, out, out_type: int,
+                                         wait_limit: int, extra_tx_bytes: int, stream=None) -> int:
+    return load_library().kvq_chunk_attn_scored_lost_wait_test(
+        _ptr(k16), _ptr(v16), n_kv_heads, P, head_dim, ctypes.byref(scores), _ptr(q), T, n_q, float(sm_scale),
+        _ptr(out), out_type, wait_limit, extra_tx_bytes, _stream(stream))
 
 
 def kvq_verify_draft(target, draft, type: int, target_stride: int, draft_stride: int, n_seq: int, W: int,

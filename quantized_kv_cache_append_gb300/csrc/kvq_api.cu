@@ -748,8 +748,10 @@ KVQ_API kvq_status kvq_scatter_cells(const kvq_cache* cache, const int32_t* bloc
 namespace kvq {
 namespace {
 kvq_status chunk_impl(const void* k16, const void* v16, int n_kv_heads, int P, int head_dim,
-                      const float* q, int T, int n_q, float sm_scale, float* out, void* stream,
-                      uint32_t wait_limit = kDefaultWaitLimit, uint32_t extra_tx = 0) {
+                      const float* q, int T, int n_q, float sm_scale, void* out, void* stream,
+                      uint32_t wait_limit = kDefaultWaitLimit, uint32_t extra_tx = 0,
+                      const kvq_scores* scores = nullptr, int out_type = KVQ_T_F32) {
+  if (out_type != KVQ_T_F32 && out_type != KVQ_T_F16 && out_type != KVQ_T_BF16) return KVQ_ERR_ARG;
   if (k16 == nullptr || v16 == nullptr || q == nullptr || out == nullptr) return KVQ_ERR_ARG;
   if (!aligned(k16, 16) || !aligned(v16, 16) || !aligned(q, 16) || !aligned(out, 16))
     return KVQ_ERR_ARG;
@@ -764,7 +766,7 @@ kvq_status chunk_impl(const void* k16, const void* v16, int n_kv_heads, int P, i
   a.k16 = static_cast<const __half*>(k16);
   a.v16 = static_cast<const __half*>(v16);
   a.q = q;
-  a.out = out;
+  a.out = static_cast<float*>(out);
   a.n_kv = n_kv_heads;
   a.P = P;
   a.T = T;
@@ -773,7 +775,24 @@ kvq_status chunk_impl(const void* k16, const void* v16, int n_kv_heads, int P, i
   a.qscale = sm_scale * 1.4426950408889634f;  // log2(e)
   a.wait_limit = wait_limit;
   a.extra_tx = extra_tx;
-  const cudaError_t e = launch_chunk_attn(head_dim, a, static_cast<cudaStream_t>(stream));
+  a.out_any = out;
+  a.out_type = out_type;
+  a.cap2 = a.cap2_inv = 0.0f;
+  a.slopes = nullptr;
+  a.first = a.last = nullptr;
+  a.window = 0;
+  if (scores != nullptr) {
+    if (scores->softcap > 0.0f) {
+      a.cap2 = scores->softcap * 1.4426950408889634f;
+      a.cap2_inv = 1.0f / a.cap2;
+    }
+    a.slopes = scores->slopes;
+    a.first = scores->first;
+    a.last = scores->last;
+    a.window = scores->window < P ? scores->window : 0;   // (as wide as the context: none)
+  }
+  const cudaError_t e = scores != nullptr ? launch_chunk_scores(head_dim, a, static_cast<cudaStream_t>(stream))
+                                          : launch_chunk_attn(head_dim, a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 }  // namespace
@@ -793,6 +812,28 @@ KVQ_API kvq_status kvq_chunk_attn_lost_wait_test(const void* k16, const void* v1
   if (extra_tx_bytes == 0 || extra_tx_bytes > 4096 || extra_tx_bytes % 16 != 0) return KVQ_ERR_ARG;
   return kvq::chunk_impl(k16, v16, n_kv_heads, P, head_dim, q, T, n_q, sm_scale, out, stream,
                          wait_limit, extra_tx_bytes);
+}
+
+KVQ_API kvq_status kvq_chunk_attn_scored(const void* k16, const void* v16, int n_kv_heads, int P,
+                                         int head_dim, const kvq_scores* scores, const float* q, int T,
+                                         int n_q, float sm_scale, void* out, int out_type, void* stream) {
+  const kvq_status st = kvq::check_scores(scores);
+  if (st != KVQ_OK) return st;
+  return kvq::chunk_impl(k16, v16, n_kv_heads, P, head_dim, q, T, n_q, sm_scale, out, stream,
+                         kDefaultWaitLimit, 0, scores, out_type);
+}
+
+KVQ_API kvq_status kvq_chunk_attn_scored_lost_wait_test(const void* k16, const void* v16, int n_kv_heads,
+                                                        int P, int head_dim, const kvq_scores* scores,
+                                                        const float* q, int T, int n_q, float sm_scale,
+                                                        void* out, int out_type, uint32_t wait_limit,
+                                                        uint32_t extra_tx_bytes, void* stream) {
+  const kvq_status st = kvq::check_scores(scores);
+  if (st != KVQ_OK) return st;
+  if (wait_limit == 0 || wait_limit > kDefaultWaitLimit) return KVQ_ERR_ARG;
+  if (extra_tx_bytes == 0 || extra_tx_bytes > 4096 || extra_tx_bytes % 16 != 0) return KVQ_ERR_ARG;
+  return kvq::chunk_impl(k16, v16, n_kv_heads, P, head_dim, q, T, n_q, sm_scale, out, stream, wait_limit,
+                         extra_tx_bytes, scores, out_type);
 }
 
 KVQ_API kvq_status kvq_stream_plan(int n_host_blocks, int n_slots, int32_t* slot_of_block,

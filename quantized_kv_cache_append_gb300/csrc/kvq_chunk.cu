@@ -21,10 +21,20 @@
 #include "kvq_internal.cuh"
 #include "kvq_key_splits.h"
 #include "kvq_ptx.cuh"
+#include "kvq_tanh.cuh"
 #include "kvq_tc.cuh"
+
+// This file is compiled twice: as it stands, and included by
+// kvq_chunk_scores.cu with KVQ_CHUNK_SCORES set, for capped, biased and masked
+// scores (kvq_chunk_attn_scored).
+#ifndef KVQ_CHUNK_SCORES
+#define KVQ_CHUNK_SCORES 0
+#endif
 
 namespace kvq {
 namespace {
+
+constexpr bool kScores = KVQ_CHUNK_SCORES != 0;
 
 constexpr float kTauC = 8.0f;     // lazy rescale threshold (log2 units)
 constexpr unsigned kAll = 0xffffffffu;
@@ -122,6 +132,33 @@ __device__ __forceinline__ uint32_t sw(int r, int b) {
 }
 }  // namespace tcc
 
+// What a token sees (scored): cells [lo, hi], hi < lo: none.
+struct Seen {
+  int lo, hi;
+};
+
+__device__ __forceinline__ Seen seen_by(const ChunkArgs& a, int tok) {
+  const int pos = a.P - a.T + tok;
+  Seen s = {a.first != nullptr ? max(__ldg(a.first + tok), 0) : 0, pos};
+  if (a.window > 0) s.lo = max(s.lo, pos - a.window + 1);   // (both below 2^31)
+  if (a.last != nullptr) s.hi = min(max(pos, __ldg(a.last + tok)), a.P - 1);
+  return s;
+}
+
+// 4 output values of a row, at value index i (a multiple of 4)
+__device__ __forceinline__ void store4(const ChunkArgs& a, size_t i, float4 v) {
+  if (!kScores || a.out_type == KVQ_T_F32) {
+    *reinterpret_cast<float4*>((kScores ? static_cast<float*>(a.out_any) : a.out) + i) = v;
+  } else if (a.out_type == KVQ_T_F16) {
+    *reinterpret_cast<uint2*>(static_cast<__half*>(a.out_any) + i) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+  } else {
+    uint2 u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(v.y), "f"(v.x));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(v.w), "f"(v.z));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out_any) + i) = u;
+  }
+}
+
 // LW: the lost-wait test's instantiation, whose waits take their poll limit
 // from the call and whose stages expect a.extra_tx bytes more than any copy
 // delivers; the ordinary one keeps the constant limit in its hot loops.
@@ -152,13 +189,46 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   const int n_rows = a.T * a.G;
   const int P0 = a.P - a.T;                 // cells before the chunk
   const int t_last = min(a.T - 1, (min(r0 + BM, n_rows) - 1) / a.G);
-  const int n_all = (P0 + t_last + 1 + BN - 1) / BN;     // key tiles the CTA's rows see
+  int n_all = (P0 + t_last + 1 + BN - 1) / BN;     // key tiles the CTA's rows see
+  int tile0 = 0;                                   // and the first of them
+  if constexpr (kScores) {
+    // the union of what the tile's tokens see (windows and documents move
+    // forward with the tokens, so it has no holes to speak of)
+    __shared__ int s_seen[2][8];
+    const int t_first = r0 / a.G;
+    int lo = 0x7fffffff, hi = -1;
+    if (a.first == nullptr && a.last == nullptr) {
+      lo = seen_by(a, t_first).lo;
+      hi = P0 + t_last;
+    } else {
+      for (int t = t_first + (int)threadIdx.x; t <= t_last; t += (int)blockDim.x) {
+        const Seen s = seen_by(a, t);
+        if (s.lo <= s.hi) {
+          lo = min(lo, s.lo);
+          hi = max(hi, s.hi);
+        }
+      }
+      lo = __reduce_min_sync(kAll, lo);
+      hi = __reduce_max_sync(kAll, hi);
+      if (lane == 0) {
+        s_seen[0][warp] = lo;
+        s_seen[1][warp] = hi;
+      }
+      __syncthreads();
+      for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        lo = min(lo, s_seen[0][w]);
+        hi = max(hi, s_seen[1][w]);
+      }
+    }
+    tile0 = lo <= hi ? lo / BN : 0;
+    n_all = lo <= hi ? hi / BN + 1 - tile0 : 0;
+  }
   // key splits: the gridDim.z CTAs of a (row tile, KV head) form a cluster,
   // each takes a contiguous share of the key tiles, and they merge at the end
   const int n_split = (int)gridDim.z;
   const int per = (n_all + n_split - 1) / n_split;
-  const int j0 = min(n_all, (int)blockIdx.z * per);     // this CTA's first key tile
-  const int n_tiles = min(n_all, j0 + per) - j0;         // and its count (0 possible)
+  const int j0 = tile0 + min(n_all, (int)blockIdx.z * per);     // this CTA's first key tile
+  const int n_tiles = min(tile0 + n_all, j0 + per) - j0;         // and its count (0 possible)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -291,7 +361,17 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
     }
   } else {
     // ---------------- softmax warps: thread = query row ----------------
-    const int lim = valid ? P0 + tok : -1;                  // last key this row sees
+    int lim = valid ? P0 + tok : -1;                  // last key this row sees
+    int lo = 0;                                       // and the first (scored)
+    float slope = 0.f;
+    if constexpr (kScores) {
+      if (valid) {
+        const Seen s = seen_by(a, tok);
+        lo = s.lo;
+        lim = s.hi;
+        if (a.slopes != nullptr) slope = -1.4426950408889634f * __ldg(a.slopes + kvh * a.G + gg);
+      }
+    }
     {
       // q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand
       const float* qrow = a.q + ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
@@ -324,6 +404,33 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         tmem_ld32(tmem + lane_base + (uint32_t)(b * BN) + c0, *reinterpret_cast<uint32_t(*)[32]>(sv + c0));
       tmem_wait_ld();
       const int key0 = (j0 + j) * BN;
+      if constexpr (kScores) {
+        if (a.cap2 != 0.f) {
+          float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < BN; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = max3f(top[e], fabsf(sv[c + e]), fabsf(sv[c + 4 + e]));
+          const bool wide = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.cap2_inv > kTanhSmall;
+          if (__any_sync(kAll, wide)) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) sv[c] = a.cap2 * tanh_any(sv[c] * a.cap2_inv);
+          } else {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) sv[c] = a.cap2 * tanh_small(sv[c] * a.cap2_inv);
+          }
+        }
+        if (a.slopes != nullptr) {
+          const float d0 = (float)(P0 + tok - key0);
+#pragma unroll
+          for (int c = 0; c < BN; ++c) sv[c] = fmaf(slope, fabsf(d0 - (float)c), sv[c]);
+        }
+        if (key0 < lo) {   // keys before this row's first
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (key0 + c < lo) sv[c] = kNegInf;
+        }
+      }
       if (key0 + BN - 1 > lim) {   // keys past this row's causal limit
 #pragma unroll
         for (int c = 0; c < BN; ++c)
@@ -392,7 +499,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const bool soft = warp < kSoftWarps;
-  float* orow = a.out + ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
+  const size_t orow = ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
   const float nan = __int_as_float(0x7fc00000);
   if (n_split == 1) {
     if (soft) {
@@ -403,12 +510,16 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         tmem_ld32(tmem + lane_base + COL_O + c0, ov);
         tmem_wait_ld();
         if (valid) {
+          if (kScores && l == 0.f) {   // the row sees no key (O may not even have been written)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = 0u;
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             float4 r4 = make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
                                     __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
             if (lost) r4 = make_float4(nan, nan, nan, nan);
-            *reinterpret_cast<float4*>(orow + c0 + e) = r4;
+            store4(a, orow + c0 + e, r4);
           }
         }
       }
@@ -434,7 +545,9 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         const float mz = ld_dsmem_f32(smem_u32(&s_ml[row].x), z), lz = ld_dsmem_f32(smem_u32(&s_ml[row].y), z);
         L += lz * fast_exp2(mz - M);
       }
-      const float c = fast_exp2(m - M) / L;   // this split's weight (rows that see no key: unused)
+      // this split's weight (rows that see no key: 0; unscored chunks have none)
+      const bool none = kScores && L == 0.f;
+      const float c = none ? 0.f : fast_exp2(m - M) / L;
 #pragma unroll
       for (int c0 = 0; c0 < HD; c0 += 32) {
         uint32_t ov[32];
@@ -444,7 +557,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 r4 = n_tiles > 0
+          const float4 r4 = n_tiles > 0 && !none
               ? make_float4(__uint_as_float(ov[e]) * c, __uint_as_float(ov[e + 1]) * c,
                             __uint_as_float(ov[e + 2]) * c, __uint_as_float(ov[e + 3]) * c)
               : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -467,7 +580,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
           acc.z += v4.z;
           acc.w += v4.w;
         }
-        *reinterpret_cast<float4*>(orow + 4 * ch) = acc;
+        store4(a, orow + 4 * ch, acc);
       }
     }
     cluster_sync_all();   // no CTA leaves while a peer reads its shared memory
@@ -571,7 +684,12 @@ cudaError_t launch_tc_kernel(const ChunkArgs& a, cudaStream_t s) {
   }
   const long long row_tiles = ((long long)a.T * a.G + tcc::BM - 1) / tcc::BM;
   if (row_tiles > 0x7fffffffLL || a.n_kv > 65535) return cudaErrorInvalidValue;
-  const int n_split = tc_key_splits<HD, LW>(row_tiles * a.n_kv, (a.P + Lay::BN - 1) / Lay::BN);
+  int n_all = (a.P + Lay::BN - 1) / Lay::BN;
+  if (kScores && a.window > 0 && a.last == nullptr) {   // the window of a row tile's tokens, and the tiles it cuts
+    const long long cells = (long long)a.window + (tcc::BM + a.G - 1) / a.G;
+    n_all = (int)min((long long)n_all, cells / Lay::BN + 2);
+  }
+  const int n_split = tc_key_splits<HD, LW>(row_tiles * a.n_kv, n_all);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       tc_config<HD>(dim3((unsigned)row_tiles, (unsigned)a.n_kv, (unsigned)n_split), n_split, s, attr);
@@ -585,7 +703,11 @@ cudaError_t launch_tc(const ChunkArgs& a, cudaStream_t s) {
 
 }  // namespace
 
+#if KVQ_CHUNK_SCORES
+cudaError_t launch_chunk_scores(int hd, const ChunkArgs& a, cudaStream_t s) {
+#else
 cudaError_t launch_chunk_attn(int hd, const ChunkArgs& a, cudaStream_t s) {
+#endif
   switch (hd) {
     case 64: return launch_tc<64>(a, s);
     case 128: return launch_tc<128>(a, s);

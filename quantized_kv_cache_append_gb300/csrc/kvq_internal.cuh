@@ -406,7 +406,17 @@ struct ChunkArgs {
   uint32_t wait_limit; // polls of an mbarrier wait before it is declared lost
   uint32_t extra_tx;   // bytes added to each K / V stage's expected count (0; >0 only
                        // in the lost-wait test, which makes every copy wait run out)
+  // Scored (kvq_chunk_attn_scored), unread elsewhere.
+  void* out_any;       // out, of out_type
+  int out_type;        // kvq_type
+  float cap2, cap2_inv;  // softcap * log2(e) and its inverse; 0: no cap
+  const float* slopes; // [n_q] or null
+  const int32_t* first;  // [T] or null: first cell a token sees
+  const int32_t* last;   // [T] or null: last one, if behind its own
+  int window;          // 0: none
 };
 cudaError_t launch_chunk_attn(int hd, const ChunkArgs& a, cudaStream_t s);
+// The same with capped, biased and masked scores (kvq_chunk_scores.cu).
+cudaError_t launch_chunk_scores(int hd, const ChunkArgs& a, cudaStream_t s);
 
 }  // namespace kvq

@@ -7,20 +7,20 @@ import numpy as np
 
 
 def rows(q, k, v, places, pos, low, high, sm_scale, cap=0.0, slopes=None, p_step=2.0 ** -22,
-         code=None, top=2.0 ** 8):
+         code=None, top=2.0 ** 8, dot=2.0 ** -18, sums=64):
     """One KV head: q [T][G][hd] at positions pos [T]; k, v [n][hd], cells
     `places` [n]; low, high [T] first and last cell seen; slopes [G] ->
     (out [T][G][hd], tolerance [T][G][hd]).
 
     Tolerance.  A score's error dz (natural-log units): q enters as fp16 hi +
-    lo and is summed in fp32, below 2^-18 of sm_scale * sum |q k|
-    (plain_blocks.attention); the tanh's argument, value and product with the
+    lo and is summed in fp32, below `dot` of sm_scale * sum |q k|
+    (plain_blocks.attention: hd / 16 <= 16 steps at 2^-23); the tanh's argument, value and product with the
     cap below 2^-19 of the capped score (its approximation 2^-21, the rest half
     steps; the slope of the tanh is at most 1); slope * log2(e), distance and
     their fma below 2^-22 of the bias; the log2 domain's own roundings 2^-22 of
     the score.  The output moves by at most sum p dz |v| + |o| sum p dz.  p
     itself: 2^-21 of the exponential and p_step of its rounding; the sum over
-    the cells in fp32, n / 64 steps at 2^-23 of sum p |v|.
+    the cells in fp32, n / sums steps at 2^-23 of sum p |v|.
 
     code: the largest |v| in the units that meet p in the tensor core (int8
     and K8V4 fold the scale into p: 127 and 8; FP16: the values).  p's lo half
@@ -37,7 +37,7 @@ def rows(q, k, v, places, pos, low, high, sm_scale, cap=0.0, slopes=None, p_step
         ks, vs, d = k[seen], v[seen], np.abs(pos[t] - places[seen])
         Q = q[t].astype(np.float64)
         z = sm_scale * (Q @ ks.T)
-        dz = 2.0 ** -18 * abs(sm_scale) * (np.abs(Q) @ np.abs(ks).T)
+        dz = dot * abs(sm_scale) * (np.abs(Q) @ np.abs(ks).T)
         if cap:
             z = cap * np.tanh(z / cap)
             dz = dz + 2.0 ** -19 * np.abs(z)
@@ -51,7 +51,7 @@ def rows(q, k, v, places, pos, low, high, sm_scale, cap=0.0, slopes=None, p_step
         o = p @ vs
         out[t] = o
         tol[t] = ((p * dz) @ np.abs(vs) + np.abs(o) * (p * dz).sum(1, keepdims=True)
-                  + (2.0 ** -20 + p_step + (seen.sum() / 64 + 32) * 2.0 ** -23) * (p @ np.abs(vs)) + 1e-30
+                  + (2.0 ** -20 + p_step + (seen.sum() / sums + 32) * 2.0 ** -23) * (p @ np.abs(vs)) + 1e-30
                   + len(ks) * 2.0 ** -25 * (np.abs(vs).max() if code is None else code) / top)
     return out, tol
 
@@ -83,3 +83,29 @@ def decode(K, V, q, ctx, table, bs, sm_scale, cap=0.0, window=0, slopes=None, fi
                 o, e = o @ rotated / hd, np.broadcast_to(2 * e.max(-1, keepdims=True), e.shape)
             out[b, :, s], tol[b, :, s] = o, e
     return out, tol
+
+
+def chunk(k16, v16, q, sm_scale, cap=0.0, window=0, slopes=None, first=None, last=None, out_step=0.0):
+    """k16, v16 [n_kv][P][hd], q [T][n_q][hd] -> (out, tolerance).  Sums of hi and
+    lo halves in turn: 2 hd / 16 <= 32 steps at 2^-23 and q's 2^-22, below
+    2^-17; p is one fp16 value (2^-11; its reference maximum is at most the
+    row's, so the largest p is at least 1), 16 cells a step of the fp32 sum;
+    out_step: half a step of the output type."""
+    n_kv, P, hd = k16.shape
+    T, n_q, _ = q.shape
+    G = n_q // n_kv
+    pos = P - T + np.arange(T)
+    low, high = np.zeros(T, np.int64), pos
+    if first is not None:
+        low = np.maximum(first, 0)
+    if window:
+        low = np.maximum(low, pos - window + 1)
+    if last is not None:
+        high = np.minimum(np.maximum(pos, last), P - 1)
+    out, tol = np.zeros(q.shape), np.zeros(q.shape)
+    for h in range(n_kv):
+        s = slice(h * G, (h + 1) * G)
+        out[:, s], tol[:, s] = rows(q[:, s], k16[h], v16[h], np.arange(P), pos, low, high, sm_scale, cap,
+                                    None if slopes is None else slopes[s], 2.0 ** -11, top=1.0, dot=2.0 ** -17,
+                                    sums=16)
+    return out, tol + out_step * (np.abs(out) + tol) + (2.0 ** -25 if out_step else 0)

@@ -62,3 +62,27 @@ def test_workspace_sizes():
     assert kvq.kvq_scored_workspace_bytes(cache(), kvq.make_scores(window=6400), 1, 1, 32, 6400) == whole
     for bad in ((0, 1, 32, 100), (1, 0, 32, 100), (1, 1, 30, 100), (1, 1, 32, 0), (1, 1, 8 * 33, 100)):
         assert kvq.kvq_scored_workspace_bytes(cache(), kvq.make_scores(), *bad) == 0
+
+
+def chunk(scores, **bad):
+    a = dict(k=A, v=2 * A, n_kv=8, P=1000, hd=128, q=3 * A, T=100, n_q=32, sm=0.1, out=4 * A, type=kvq.KVQ_T_BF16)
+    a.update(bad)
+    return kvq.kvq_chunk_attn_scored(a["k"], a["v"], a["n_kv"], a["P"], a["hd"], scores, a["q"], a["T"], a["n_q"],
+                                     a["sm"], a["out"], a["type"], 0)
+
+
+@no_gpu_only
+@pytest.mark.parametrize("bad", BAD_SCORES)
+def test_chunk_refuses_scores(bad):
+    assert chunk(kvq.make_scores(**bad)) == ARG
+
+
+@no_gpu_only
+@pytest.mark.parametrize("bad,status", [
+    *[(dict([(k, None)]), ARG) for k in ("k", "v", "q", "out")], (dict(k=A + 8), ARG), (dict(out=4 * A + 8), ARG),
+    (dict(type=3), ARG), (dict(type=-1), ARG), (dict(P=0), ARG), (dict(T=0), ARG), (dict(T=1001), ARG),
+    (dict(n_q=30), ARG), (dict(n_kv=0), ARG), (dict(sm=float("inf")), ARG), (dict(hd=96), UNSUPPORTED),
+    (dict(P=1 << 28), UNSUPPORTED),
+])
+def test_chunk_refuses(bad, status):
+    assert chunk(kvq.make_scores(softcap=30.0, window=100, slopes=A, first=A, last=A), **bad) == status
