@@ -21,7 +21,6 @@
 #include "kvq_internal.cuh"
 #include "kvq_key_splits.h"
 #include "kvq_ptx.cuh"
-#include "kvq_tanh.cuh"
 #include "kvq_tc.cuh"
 
 // This file is compiled twice: as it stands, and included by
@@ -74,14 +73,26 @@ struct ChunkMaps {
 // q * sm_scale * log2(e) enters as fp16 hi + lo (about 22 significant bits:
 // K's large channels magnify q's rounding), K and V as the exact staging
 // values, p as one fp16 value.
+//
+// Scored (kvq_chunk_attn_scored): 8 softmax warps, two for each 32 rows, each
+// thread with half of its row's columns of every tile (the roles above start
+// at warp 8).  The two threads of a row agree on its maximum by a barrier of
+// their two warps, which carries one bit, whether the maximum must rise; only
+// then do they exchange it.  With 4 warps the cap's arithmetic, a chain per
+// column with one warp a scheduler and 128 logits in registers, took 2673 us
+// where 8 took 1204 and, in packed pairs, 1055 (4096 tokens over 16384 cells, 32/8
+// heads, head_dim 128; uncapped 870).  The key tiles run from the newest to
+// the oldest: a bias that falls with the distance then sets the maximum in
+// the first tile, where the other way round every tile would raise it and
+// rescale O.
 // ---------------------------------------------------------------------------
 namespace tcc {
 constexpr int BM = 128;
-constexpr int kSoftWarps = 4;
-constexpr int kProdWarp = 4;    // K tiles (and V tiles unless a warp of their own)
-constexpr int kMmaWarp = 5;     // S MMAs; owns the tensor memory
-constexpr int kPvWarp = 6;      // P V MMAs
-constexpr int kProdWarpV = 7;   // V tiles, when V has a single stage
+constexpr int kSoftWarps = kScores ? 8 : 4;
+constexpr int kProdWarp = kSoftWarps;        // K tiles (and V tiles unless a warp of their own)
+constexpr int kMmaWarp = kSoftWarps + 1;     // S MMAs; owns the tensor memory
+constexpr int kPvWarp = kSoftWarps + 2;      // P V MMAs
+constexpr int kProdWarpV = kSoftWarps + 3;   // V tiles, when V has a single stage
 constexpr int QSPAN_B = BM * 128;   // one 128-byte span of the 128 q rows
 // barriers.  SFREE[b] completes when the P V product that read S buffer b
 // has (so the rescale of O before tile j's P waits on SFREE[(j - 1) % 3]:
@@ -107,7 +118,7 @@ struct TcLayout {
   static constexpr int BN = HD == 256 ? 64 : 128;     // keys per tile
   static constexpr int KST = 2, VST = HD == 256 ? 1 : 2;
   static constexpr bool SPLIT_PROD = VST == 1;        // V from warp 7
-  static constexpr int THREADS = SPLIT_PROD ? 256 : 224;
+  static constexpr int THREADS = (kSoftWarps + (SPLIT_PROD ? 4 : 3)) * 32;
   static constexpr int NSP = HD / 64;                 // 128-byte spans per row
   static constexpr int QTILE_B = NSP * QSPAN_B;       // 128 q rows x 2 HD bytes
   static constexpr int KSPAN_B = BN * 128;            // one span of a key tile
@@ -159,6 +170,205 @@ __device__ __forceinline__ void store4(const ChunkArgs& a, size_t i, float4 v) {
   }
 }
 
+// cap * tanh(z / cap) where |z| <= 0.45 cap: z + z t P(t), t = z^2, P of degree 2
+// fitted to (tanh(y) / y - 1) / y^2 (weighted least squares on Chebyshev nodes, relative
+// error of the whole 2.9e-7, far below the half step of p, 2^-11), its
+// coefficients scaled by the cap's powers.
+constexpr float kCapSmall = 0.45f, kCapC1 = -0.33330485f, kCapC2 = 0.1324665f, kCapC3 = -0.046321902f;
+
+__device__ __forceinline__ void cap_pair(float& d0, float& d1, float z0, float z1, float c1, float c2, float c3) {
+  float t0, t1, p0, p1;
+  mul_f32x2(t0, t1, z0, z1, z0, z1);
+  fma_f32x2(p0, p1, t0, t1, c3, c3, c2, c2);
+  fma_f32x2(p0, p1, p0, p1, t0, t1, c1, c1);
+  mul_f32x2(p0, p1, p0, p1, t0, t1);
+  fma_f32x2(d0, d1, z0, z1, p0, p1, z0, z1);
+}
+
+// A barrier of the two warps that share 32 rows (w and w + 4), carrying the
+// "or" of a predicate.  Both warps come here once per tile, whatever they
+// lost, so neither waits alone.
+__device__ __forceinline__ bool pair_any(int warp, bool x) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 64, p;\n selp.s32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(1 + (warp & 3)), "r"(x ? 1 : 0)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void pair_sync(int warp) {
+  asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + (warp & 3)) : "memory");
+}
+
+struct Key {
+  int j0, n_tiles, P0;   // the CTA's first key tile, its tiles, the cells before the chunk
+};
+
+// The softmax of a scored chunk: thread = (query row, half of the columns).
+// Returns whether a wait was lost; m (the same in a row's two threads) and l
+// (each its own columns') are left for the output.
+template <int HD>
+__device__ __forceinline__ bool softmax_scored(const ChunkArgs& a, unsigned char* smem, uint32_t sbase, uint32_t tmem,
+                                               const Key key, int row, int tok, int kvh, int gg, bool valid, uint32_t wl,
+                                               float (*s_pair)[tcc::BM], int* s_flag, float& m, float& l) {
+  using namespace tcc;
+  using Lay = TcLayout<HD>;
+  constexpr int BN = Lay::BN, HC = BN / 2;
+  constexpr float kNegInf = -INFINITY;
+  auto bar = [&](int i) -> uint32_t { return sbase + Lay::OFF_BAR + 8 * i; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2;
+  const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  const Seen sees = valid ? seen_by(a, tok) : Seen{0, -1};
+  const int pos = key.P0 + tok;
+  const float slope =
+      valid && a.slopes != nullptr ? 1.4426950408889634f * __ldg(a.slopes + kvh * a.G + gg) : 0.f;
+  {
+    // this half of the row's q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand
+    const float* qrow = a.q + ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
+#pragma unroll 4
+    for (int i = 0; i < HD / 16; ++i) {
+      const int c = half * (HD / 16) + i;
+      float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
+      if (valid) {
+        x0 = __ldg(reinterpret_cast<const float4*>(qrow + 8 * c));
+        x1 = __ldg(reinterpret_cast<const float4*>(qrow + 8 * c + 4));
+      }
+      const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) split_pair(x[2 * e] * a.qscale, x[2 * e + 1] * a.qscale, hi[e], lo[e]);
+      *reinterpret_cast<uint4*>(smem + Lay::OFF_QH + sw(row, c * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(smem + Lay::OFF_QL + sw(row, c * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(QREADY)) : "memory");
+  }
+  bool lost = false;
+  for (int j = 0; j < key.n_tiles; ++j) {
+    const int b = j % 3;
+    float z[HC];
+    float base = 0.f, mx = kNegInf;   // a score is z + base
+    if (!lost) lost = __any_sync(kAll, !mbar_wait(bar(SFULL + b), (j / 3) & 1, wl));
+    if (!lost) {
+      tc_fence_after();
+#pragma unroll
+      for (int c0 = 0; c0 < HC; c0 += 32)
+        tmem_ld32(lanes + (uint32_t)(b * BN + half * HC) + c0, *reinterpret_cast<uint32_t(*)[32]>(z + c0));
+      tmem_wait_ld();
+      tc_fence_before();
+      const int key0 = (key.j0 + key.n_tiles - 1 - j) * BN + half * HC;   // this thread's first key
+      if (a.cap2 != 0.f) {
+        float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < HC; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top[e] = max3f(top[e], fabsf(z[c + e]), fabsf(z[c + 4 + e]));
+        const float small = kCapSmall * a.cap2;
+        const bool wide = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > small;
+        const float i2 = a.cap2_inv * a.cap2_inv, c1 = kCapC1 * i2, c2 = kCapC2 * (i2 * i2), c3 = kCapC3 * (i2 * i2) * i2;
+        if (__any_sync(kAll, wide)) {
+          const float k2 = 2.8853900817779268f * a.cap2_inv;
+#pragma unroll
+          for (int c = 0; c < HC; c += 2) {
+            float y[2];
+            cap_pair(y[0], y[1], z[c], z[c + 1], c1, c2, c3);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {   // cap (1 - 2 / (1 + e^(2 |z| / cap))), the cancellation harmless here
+              float r;
+              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + fast_exp2(k2 * fabsf(z[c + e]))));
+              if (fabsf(z[c + e]) > small) y[e] = copysignf(fmaf(-2.0f * a.cap2, r, a.cap2), z[c + e]);
+              z[c + e] = y[e];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < HC; c += 2) cap_pair(z[c], z[c + 1], z[c], z[c + 1], c1, c2, c3);
+        }
+      }
+      if (a.slopes != nullptr) {
+        if (sees.hi > pos && key0 + HC - 1 > pos) {   // keys behind the token, which a prefix may show it
+          const float d0 = (float)(pos - key0);
+#pragma unroll
+          for (int c = 0; c < HC; ++c) z[c] = fmaf(-slope, fabsf(d0 - (float)c), z[c]);
+        } else {   // the distance to key0 leaves with the maximum, one fma a column stays
+          base = slope * (float)(key0 - pos);
+#pragma unroll
+          for (int c = 0; c < HC; ++c) z[c] = fmaf(slope, (float)c, z[c]);
+        }
+      }
+      if (key0 < sees.lo || key0 + HC - 1 > sees.hi) {
+        const int c_lo = sees.lo - key0, c_hi = sees.hi - key0;
+#pragma unroll
+        for (int c = 0; c < HC; ++c)
+          if (c < c_lo || c > c_hi) z[c] = kNegInf;
+      }
+      float mx4[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(z[e], z[4 + e]);
+#pragma unroll
+      for (int c = 8; c < HC; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx4[e] = max3f(mx4[e], z[c + e], z[c + 4 + e]);
+      mx = fmaxf(max3f(mx4[0], mx4[1], mx4[2]), mx4[3]) + base;
+    }
+    // (behind this barrier both warps have read their S too, over which P goes)
+    if (pair_any(warp, lost || mx > m + kTauC)) {
+      s_pair[half][row] = mx;
+      if (lane == 0) s_flag[warp] = lost;
+      pair_sync(warp);
+      mx = fmaxf(mx, s_pair[half ^ 1][row]);
+      lost = lost || s_flag[warp ^ 4] != 0;
+      if (lost) break;   // both warps
+      const bool rise = mx > m + kTauC;
+      float alpha = 1.f;
+      if (rise) {
+        alpha = fast_exp2(m - mx);   // 0 from the finite start
+        m = mx;
+        l *= alpha;
+      }
+      if (j > 0 && __any_sync(kAll, rise)) {
+        // O holds P V of the tiles so far: wait for the last one, rescale
+        // (a lost wait here is told to the other warp at the next barrier)
+        lost = __any_sync(kAll, !mbar_wait(bar(SFREE + (j - 1) % 3), ((j - 1) / 3) & 1, wl));
+        if (lost) continue;
+        tc_fence_after();
+#pragma unroll
+        for (int c0 = 0; c0 < HD / 2; c0 += 32) {
+          uint32_t ov[32];
+          tmem_ld32(lanes + Lay::COL_O + half * (HD / 2) + c0, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+          tmem_st32(lanes + Lay::COL_O + half * (HD / 2) + c0, ov);
+        }
+      }
+    }
+    tc_fence_after();
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const float nm = base - m;
+    uint32_t pk[HC / 2];
+#pragma unroll
+    for (int e = 0; e < HC / 2; ++e) {
+      float x0, x1;
+      add_f32x2(x0, x1, z[2 * e], z[2 * e + 1], nm, nm);
+      const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+      const int c = 2 * (e & 1);
+      add_f32x2(sum[c], sum[c + 1], sum[c], sum[c + 1], p0, p1);
+      pk[e] = pack_half2(p0, p1);
+    }
+    if constexpr (HC == 64) tmem_st32(lanes + (uint32_t)(b * BN + half * 32), *reinterpret_cast<uint32_t(*)[32]>(pk));
+    else tmem_st16(lanes + (uint32_t)(b * BN + half * 16), *reinterpret_cast<uint32_t(*)[16]>(pk));
+    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    tmem_wait_st();
+    tc_fence_before();
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(PFULL + b)) : "memory");
+  }
+  if (!lost && key.n_tiles > 0) lost = __any_sync(kAll, !mbar_wait(bar(ALLDONE), 0, wl));
+  return lost;
+}
+
 // LW: the lost-wait test's instantiation, whose waits take their poll limit
 // from the call and whose stages expect a.extra_tx bytes more than any copy
 // delivers; the ordinary one keeps the constant limit in its hot loops.
@@ -194,14 +404,14 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   if constexpr (kScores) {
     // the union of what the tile's tokens see (windows and documents move
     // forward with the tokens, so it has no holes to speak of)
-    __shared__ int s_seen[2][8];
+    __shared__ int s_seen[2][Lay::THREADS / 32];
     const int t_first = r0 / a.G;
     int lo = 0x7fffffff, hi = -1;
     if (a.first == nullptr && a.last == nullptr) {
       lo = seen_by(a, t_first).lo;
       hi = P0 + t_last;
     } else {
-      for (int t = t_first + (int)threadIdx.x; t <= t_last; t += (int)blockDim.x) {
+      for (int t = t_first + (int)threadIdx.x; t <= t_last; t += Lay::THREADS) {
         const Seen s = seen_by(a, t);
         if (s.lo <= s.hi) {
           lo = min(lo, s.lo);
@@ -215,7 +425,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         s_seen[1][warp] = hi;
       }
       __syncthreads();
-      for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+      for (int w = 0; w < Lay::THREADS / 32; ++w) {
         lo = min(lo, s_seen[0][w]);
         hi = max(hi, s_seen[1][w]);
       }
@@ -253,15 +463,17 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TSLOT);
+  __shared__ float s_pair[kScores ? 2 : 1][BM];   // scored: what a row's two threads tell each other
+  __shared__ int s_flag[kScores ? 8 : 1];
   bool lost = false;
   // softmax threads: thread = query row (TMEM lane); the running maximum m
   // and sum l outlive the softmax section for the output and the merge
-  const int row = threadIdx.x;
+  const int row = kScores ? threadIdx.x & (BM - 1) : threadIdx.x;
   const int gr = r0 + row;
-  const bool valid = row < BM && gr < n_rows;
+  const bool valid = warp < kSoftWarps && gr < n_rows;
   const int tok = valid ? gr / a.G : 0;
   const int gg = valid ? gr - tok * a.G : 0;
-  const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+  const uint32_t lane_base = (uint32_t)((kScores ? warp & 3 : warp) * 32) << 16;
   float m = -1e30f, l = 0.f;
 
   if (warp == kProdWarp || (Lay::SPLIT_PROD && warp == kProdWarpV)) {
@@ -274,7 +486,8 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
       int k_issued = 0, v_issued = 0;
       for (int j = 0; j < n_tiles; ++j) {
         const int ks = j % KST, vs = j % VST;
-        const int krow = kvh * a.P + (j0 + j) * BN;   // first staging row of the tile
+        // first staging row of the tile (scored: the newest keys first)
+        const int krow = kvh * a.P + (j0 + (kScores ? n_tiles - 1 - j : j)) * BN;
         if (do_k) {
           if (j >= KST && !mbar_wait(bar(KEMPTY + ks), (j / KST - 1) & 1, wl)) break;
           mbar_expect_tx(bar(KFULL + ks), (uint32_t)KTILE_B + extra_tx);
@@ -359,19 +572,11 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
       umma_commit(bar(PDRAIN));
       (void)mbar_wait(bar(PDRAIN), 0, wl);
     }
+  } else if constexpr (kScores) {
+    lost = softmax_scored<HD>(a, smem, sbase, tmem, Key{j0, n_tiles, P0}, row, tok, kvh, gg, valid, wl, s_pair, s_flag, m, l);
   } else {
     // ---------------- softmax warps: thread = query row ----------------
-    int lim = valid ? P0 + tok : -1;                  // last key this row sees
-    int lo = 0;                                       // and the first (scored)
-    float slope = 0.f;
-    if constexpr (kScores) {
-      if (valid) {
-        const Seen s = seen_by(a, tok);
-        lo = s.lo;
-        lim = s.hi;
-        if (a.slopes != nullptr) slope = -1.4426950408889634f * __ldg(a.slopes + kvh * a.G + gg);
-      }
-    }
+    const int lim = valid ? P0 + tok : -1;                  // last key this row sees
     {
       // q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand
       const float* qrow = a.q + ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
@@ -404,33 +609,6 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         tmem_ld32(tmem + lane_base + (uint32_t)(b * BN) + c0, *reinterpret_cast<uint32_t(*)[32]>(sv + c0));
       tmem_wait_ld();
       const int key0 = (j0 + j) * BN;
-      if constexpr (kScores) {
-        if (a.cap2 != 0.f) {
-          float top[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < BN; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top[e] = max3f(top[e], fabsf(sv[c + e]), fabsf(sv[c + 4 + e]));
-          const bool wide = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.cap2_inv > kTanhSmall;
-          if (__any_sync(kAll, wide)) {
-#pragma unroll
-            for (int c = 0; c < BN; ++c) sv[c] = a.cap2 * tanh_any(sv[c] * a.cap2_inv);
-          } else {
-#pragma unroll
-            for (int c = 0; c < BN; ++c) sv[c] = a.cap2 * tanh_small(sv[c] * a.cap2_inv);
-          }
-        }
-        if (a.slopes != nullptr) {
-          const float d0 = (float)(P0 + tok - key0);
-#pragma unroll
-          for (int c = 0; c < BN; ++c) sv[c] = fmaf(slope, fabsf(d0 - (float)c), sv[c]);
-        }
-        if (key0 < lo) {   // keys before this row's first
-#pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (key0 + c < lo) sv[c] = kNegInf;
-        }
-      }
       if (key0 + BN - 1 > lim) {   // keys past this row's causal limit
 #pragma unroll
         for (int c = 0; c < BN; ++c)
@@ -495,17 +673,26 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
     if (!lost && n_tiles > 0) lost = __any_sync(kAll, !mbar_wait(bar(ALLDONE), 0, wl));
   }
   // every copy and MMA of the CTA has completed (each role drained its own)
+  const bool soft = warp < kSoftWarps;
+  if (kScores && soft) s_pair[warp >> 2][row] = lost ? __int_as_float(0x7fc00000) : l;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const bool soft = warp < kSoftWarps;
+  if constexpr (kScores) {
+    if (soft) l = s_pair[0][row] + s_pair[1][row];
+    lost = l != l;   // (a NaN logit's row too: its output is NaN either way)
+  }
+  // a thread's columns of O
+  constexpr int OC = kScores ? HD / 2 : HD;
+  const int oc0 = kScores ? (warp >> 2) * OC : 0;
   const size_t orow = ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
   const float nan = __int_as_float(0x7fc00000);
   if (n_split == 1) {
     if (soft) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-      for (int c0 = 0; c0 < HD; c0 += 32) {
+      for (int c1 = 0; c1 < OC; c1 += 32) {
+        const int c0 = oc0 + c1;
         uint32_t ov[32];
         tmem_ld32(tmem + lane_base + COL_O + c0, ov);
         tmem_wait_ld();
@@ -535,7 +722,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
     auto o_chunk = [&](int r, int ch) -> uint32_t {          // byte offset of chunk ch of row r
       return (uint32_t)(r * HD * 4) + ((uint32_t)(ch ^ (r & 7)) << 4);
     };
-    if (soft) s_ml[row] = make_float2(m, lost ? nan : l);   // a lost wait: NaN through L
+    if (soft && (!kScores || warp < 4)) s_ml[row] = make_float2(m, lost ? nan : l);   // a lost wait: NaN through L
     cluster_sync_all();
     if (soft) {
       float M = -INFINITY;
@@ -549,7 +736,8 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
       const bool none = kScores && L == 0.f;
       const float c = none ? 0.f : fast_exp2(m - M) / L;
 #pragma unroll
-      for (int c0 = 0; c0 < HD; c0 += 32) {
+      for (int c1 = 0; c1 < OC; c1 += 32) {
+        const int c0 = oc0 + c1;
         uint32_t ov[32];
         if (n_tiles > 0) {
           tmem_ld32(tmem + lane_base + COL_O + c0, ov);
@@ -571,7 +759,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
       constexpr int NCH = HD / 4;
       const int z0 = (int)blockIdx.z;
       const int ch_b = z0 * NCH / n_split, ch_e = (z0 + 1) * NCH / n_split;
-      for (int ch = ch_b; ch < ch_e; ++ch) {
+      for (int ch = ch_b + (kScores ? warp >> 2 : 0); ch < ch_e; ch += kScores ? 2 : 1) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int z = 0; z < n_split; ++z) {
           const float4 v4 = ld_dsmem_v4(s_o + o_chunk(row, ch), z);
