@@ -227,7 +227,7 @@ __device__ __forceinline__ bool softmax_scored(const ChunkArgs& a, unsigned char
   {
     // this half of the row's q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand
     const float* qrow = a.q + ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < HD / 16; ++i) {
       const int c = half * (HD / 16) + i;
       float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
@@ -395,7 +395,10 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   // row tiles in descending order: the last ones (later tokens) see the
   // most keys, so the longest CTAs start first and the grid's last, partial
   // wave holds the shortest
-  const int r0 = (int)(gridDim.x - 1 - blockIdx.x) * BM;
+  // (with first cells given, the tokens that go on with an older document are
+  // the chunk's first and see the most: ascending)
+  const bool ascending = kScores && a.first != nullptr;
+  const int r0 = (int)(ascending ? blockIdx.x : gridDim.x - 1 - blockIdx.x) * BM;
   const int n_rows = a.T * a.G;
   const int P0 = a.P - a.T;                 // cells before the chunk
   const int t_last = min(a.T - 1, (min(r0 + BM, n_rows) - 1) / a.G);
