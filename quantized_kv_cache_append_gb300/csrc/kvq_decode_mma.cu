@@ -128,7 +128,7 @@ struct Cfg {
   // (the merge at the end reuses the stages for 4 warp slabs of RP x HD
   // fp32, which takes a fourth stage for 32-row int8 HD 64 tiles)
   static constexpr int SLAB_B = kConsumerWarps * NT * 8 * HD * 4;
-  static constexpr int STAGES = (SLAB_B + STAGE_B - 1) / STAGE_B > 3 ? (SLAB_B + STAGE_B - 1) / STAGE_B : 3;
+  static constexpr int STAGES = kScores && HD == 256 && V4 ? 2 : (SLAB_B + STAGE_B - 1) / STAGE_B > 3 ? (SLAB_B + STAGE_B - 1) / STAGE_B : 3;
   static constexpr int OFF_V = TILE_B;
   static constexpr int SMEM_SC = STAGES * STAGE_B;  // [STAGES]{K [64][NG], V [64][VNS]} fp16
   // q as fp16 hi / lo rows, padded by 16 bytes so ldmatrix rows hit distinct banks

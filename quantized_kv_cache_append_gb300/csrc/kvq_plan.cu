@@ -371,7 +371,10 @@ cudaError_t launch_trim_step(const TrimArgs& a, int sms, cudaStream_t s) {
                                     kMostSmem) == cudaSuccess;
       }))
     return cudaErrorInvalidConfiguration;
+  // a CTA for every 128 sequences, or 512 blocks that may come back
   long long ctas = (a.n_seq + kPlanSeqPerCta - 1) / kPlanSeqPerCta;
+  const long long most = (long long)a.n_seq * a.max_blocks < a.n_blocks ? (long long)a.n_seq * a.max_blocks : a.n_blocks;
+  if (ctas < (most + 511) / 512) ctas = (most + 511) / 512;
   if (ctas > kPlanPerSm * sms) ctas = kPlanPerSm * sms;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);

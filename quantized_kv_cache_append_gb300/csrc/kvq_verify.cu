@@ -11,9 +11,12 @@
 // answer does not depend on how the row is split, and it equals the
 // definition's bit for bit.
 //
-// A cluster of CTAs shares a row, tile by tile of 1024 values: each warp
-// keeps its tiles' sums in shared memory, the CTAs exchange their totals, the
-// one that holds the place finds the tile and reads it once more (from L2).
+// A cluster of CTAs shares a row, tile by tile of 512 or 1024 values: each warp
+// keeps its tiles' sums in shared memory, the CTAs send each other their
+// totals, the one that holds the place finds the tile and reads it once more
+// (from L2).  Rows start at any element (a vocabulary is rarely a multiple of
+// 16 bytes): lanes load the 16-byte granules their 4 or 8 values lie in, the
+// second half of one is the next lane's, and shift them into place.
 #include <cuda_bf16.h>
 
 #include "kvq_internal.cuh"
@@ -23,10 +26,12 @@
 namespace kvq {
 namespace {
 
-constexpr int kVerThreads = 512;
+constexpr int kVerThreads = 256;
 constexpr int kVerWarps = kVerThreads / 32;
-constexpr int kTile = 1024;
-constexpr int kMostTiles = (1 << 20) / kTile;
+constexpr int kGranules = 4;   // 16-byte loads of a row a lane has in flight: a tile
+template <class E>
+constexpr int kTile = kGranules * 32 * 16 / (int)sizeof(E);
+constexpr int kMostCtas = 8;
 constexpr unsigned kFullMask = 0xffffffffu;
 
 template <int T>
@@ -48,78 +53,130 @@ __device__ __forceinline__ float wide(float x) { return x; }
 __device__ __forceinline__ float wide(__half x) { return __half2float(x); }
 __device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// floor(min(max(r, 0), 1) * 2^40) = h * 2^20 + l: adding 2^23 with rounding
-// down leaves the whole part in the mantissa, everything else is exact.
-// (fmaxf takes 0 for NaN.)
-__device__ __forceinline__ void add_units(float r, uint32_t& h, uint32_t& l) {
-  const float x = fminf(fmaxf(r, 0.0f), 1.0f) * 1048576.0f;
-  const float a = __fadd_rd(x, 8388608.0f);
-  const float b = __fadd_rd((x - (a - 8388608.0f)) * 1048576.0f, 8388608.0f);
-  h += __float_as_uint(a) & 0x7fffffu;
-  l += __float_as_uint(b) & 0x7fffffu;
+// value e of a granule
+template <class E>
+__device__ __forceinline__ float value(const uint4& g, int e) {
+  const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+  if constexpr (sizeof(E) == 4) return __uint_as_float(w[e]);
+  else if constexpr (sizeof(E) == 2 && !__is_same(E, __half))
+    return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+  else return e & 1 ? half_hi(w[e >> 1]) : half_lo(w[e >> 1]);
 }
 
-__device__ __forceinline__ unsigned long long units(float r) {
-  uint32_t h = 0, l = 0;
-  add_units(r, h, l);
-  return ((unsigned long long)h << 20) + l;
+// A sum of weights in whole numbers: floor(r * 2^40) = h * 2^20 + l for r in
+// [0, 1].  Adding 2^23 with rounding down leaves the whole part in the low
+// mantissa bits, everything else is exact; the exponent bits that come along
+// are taken off once (sums mod 2^32: a tile's values keep h and l below 2^31).
+struct Count {
+  uint32_t h, l;
+};
+constexpr uint32_t kMagicBits = 0x4b000000u;   // 2^23
+
+__device__ __forceinline__ void add_weight(Count& c, float r) {
+  constexpr float k20 = 1048576.0f, k23 = 8388608.0f;
+  const float a = __fmaf_rd(r, k20, k23);
+  const float rest = __fmaf_rn(r, k20, k23 - a);
+  c.h += __float_as_uint(a);
+  c.l += __float_as_uint(__fmaf_rd(rest, k20, k23));
+}
+__device__ __forceinline__ unsigned long long total_of(const Count& c, int n) {   // n values in it
+  return ((unsigned long long)(c.h - (uint32_t)n * kMagicBits) << 20) + (c.l - (uint32_t)n * kMagicBits);
 }
 
-// The row that is sampled: weights p, p - q, or p without one token.
+// The row that is sampled: weights p, p - q, or p without one token, held in
+// [0, 1] (NaN: 0).  [p_lo, p_hi) and [q_lo, q_hi) are the whole arrays.
 template <class E>
 struct Row {
   const E* p;
   const E* q;      // or null
   int without;     // -1: none
   int vocab;
-
-  __device__ __forceinline__ float weight(int i) const {
-    const float x = wide(p[i]);
-    return q != nullptr ? x - wide(q[i]) : i == without ? 0.0f : x;
-  }
+  const char *p_lo, *p_hi, *q_lo, *q_hi;
 };
 
-// VEC values of a 16-byte load each (rows 16-byte aligned); VEC 1: scalar.
-template <class E, int VEC>
-__device__ __forceinline__ unsigned long long tile_sum(const Row<E>& row, int tile, int lane) {
-  constexpr int N = kTile / 32 / VEC;   // loads a lane
-  uint32_t h = 0, l = 0;
-  const int i0 = tile * kTile + lane * VEC;
-  if ((tile + 1) * kTile <= row.vocab) {
-    if constexpr (VEC > 1) {
-      uint4 pw[N];
+// The granule at g, what of it lies in [lo, hi).
+template <class E>
+__device__ __forceinline__ uint4 granule(const char* g, const char* lo, const char* hi) {
+  if (g >= lo && g + 16 <= hi) return __ldg(reinterpret_cast<const uint4*>(g));
+  uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < N; ++k) pw[k] = __ldg(reinterpret_cast<const uint4*>(row.p + i0 + 32 * VEC * k));
-      if (row.q != nullptr) {
-        uint4 qw[N];
-#pragma unroll
-        for (int k = 0; k < N; ++k) qw[k] = __ldg(reinterpret_cast<const uint4*>(row.q + i0 + 32 * VEC * k));
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            add_units(wide(reinterpret_cast<const E*>(&pw[k])[e]) - wide(reinterpret_cast<const E*>(&qw[k])[e]), h, l);
-      } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            add_units(i0 + 32 * VEC * k + e == row.without ? 0.0f : wide(reinterpret_cast<const E*>(&pw[k])[e]), h, l);
-      }
-    } else {
-#pragma unroll 16
-      for (int k = 0; k < N; ++k) add_units(row.weight(i0 + 32 * k), h, l);
+  for (int b = 0; b < 16; b += (int)sizeof(E))
+    if (g + b >= lo && g + b < hi) {
+      if constexpr (sizeof(E) == 4) w[b / 4] = __ldg(reinterpret_cast<const uint32_t*>(g + b));
+      else w[b / 4] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(g + b)) << (8 * (b & 3));
     }
-  } else {
-    for (int k = 0; k < N; ++k)
-      for (int e = 0; e < VEC; ++e) {
-        const int i = i0 + 32 * VEC * k + e;
-        if (i < row.vocab) add_units(row.weight(i), h, l);
-      }
-  }
-  // 1024 values: h and l stay below 2^31
-  return ((unsigned long long)__reduce_add_sync(kFullMask, h) << 20) + __reduce_add_sync(kFullMask, l);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// The 16 bytes that start s bytes into v0 | v1.
+__device__ __forceinline__ uint4 shifted(const uint4& v0, const uint4& v1, int s) {
+  uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  if (s & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (s & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const int bits = 8 * (s & 3);
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// Values i0 + (32 k + lane) NV .. + NV - 1 of a row, k < kGranules, for all lanes.
+template <class E>
+__device__ __forceinline__ void load_tile(const E* row, const char* lo, const char* hi, int i0, int lane, uint4 (&v)[kGranules]) {
+  const char* p = reinterpret_cast<const char*>(row + i0) + lane * 16;
+  const int s = (int)(reinterpret_cast<uintptr_t>(row) & 15);   // (i0 is a multiple of NV)
+#pragma unroll
+  for (int k = 0; k < kGranules; ++k) v[k] = granule<E>(p - s + 512 * k, lo, hi);
+  if (s != 0) {
+    uint4 last[kGranules];
+#pragma unroll
+    for (int k = 0; k < kGranules; ++k)
+      last[k] = lane == 31 ? granule<E>(p - s + 512 * k + 16, lo, hi) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kGranules; ++k) {
+      uint4 n = make_uint4(__shfl_down_sync(kFullMask, v[k].x, 1), __shfl_down_sync(kFullMask, v[k].y, 1),
+                           __shfl_down_sync(kFullMask, v[k].z, 1), __shfl_down_sync(kFullMask, v[k].w, 1));
+      if (lane == 31) n = last[k];
+      v[k] = shifted(v[k], n, s);
+    }
+  }
+}
+
+// Weight e of granule k of a lane's share of a tile (behind the row's end: 0).
+template <class E>
+struct Tile {
+  static constexpr int NV = 16 / (int)sizeof(E);
+  uint4 p[kGranules], q[kGranules];
+  int i0, left, without, lane;   // left: values from i0 to the row's end
+  bool has_q;
+
+  __device__ __forceinline__ Tile(const Row<E>& row, int tile, int lane_) : lane(lane_) {
+    i0 = tile * kTile<E>;
+    left = row.vocab - i0;
+    without = row.without;
+    has_q = row.q != nullptr;
+    load_tile<E>(row.p, row.p_lo, row.p_hi, i0, lane, p);
+    if (has_q) load_tile<E>(row.q, row.q_lo, row.q_hi, i0, lane, q);
+  }
+  __device__ __forceinline__ float weight(int k, int e) const {
+    const float x = value<E>(p[k], e);
+    const int at = (32 * k + lane) * NV + e;
+    float r = has_q ? __saturatef(x - value<E>(q[k], e)) : __saturatef(x);
+    if (without >= 0 && i0 + at == without) r = 0.f;
+    if (left < kTile<E> && at >= left) r = 0.f;
+    return r;
+  }
+  __device__ __forceinline__ Count sum(int k) const {
+    Count c = {0, 0};
+#pragma unroll
+    for (int e = 0; e < NV; ++e) add_weight(c, weight(k, e));
+    return c;
+  }
+};
 
 __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, int lane) {
 #pragma unroll
@@ -130,19 +187,18 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, in
   return v;
 }
 
-__device__ __forceinline__ unsigned long long ld_dsmem_u64(uint32_t addr, int rank) {
+__device__ __forceinline__ void st_dsmem_u64(uint32_t addr, int rank, unsigned long long v) {
   uint32_t remote;
-  unsigned long long v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
 }
 
-template <int T, bool VEC>
+template <int T>
 __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
   using E = typename Prob<T>::type;
-  __shared__ unsigned long long s_tile[kMostTiles];
-  __shared__ unsigned long long s_total[2];   // of this CTA: the residual's, the row's
+  constexpr int NV = 16 / (int)sizeof(E), N = kGranules;
+  __shared__ unsigned long long s_tile[(1 << 20) / kTile<E>];
+  __shared__ unsigned long long s_total[2][kMostCtas];   // [residual, row][CTA], sent by each of them
   __shared__ int s_a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -152,7 +208,16 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
   const int W = a.W;
   const E* target = static_cast<const E*>(a.target);
   const E* draft = static_cast<const E*>(a.draft);
-  const int n_given = a.n_draft != nullptr ? min(__ldg(a.n_draft + b), W - 1) : W - 1;
+  // the small loads together: lane i of every warp looks at draft i
+  const int n_raw = a.n_draft != nullptr ? __ldg(a.n_draft + b) : W - 1;
+  const float us = __ldg(a.u_sample + b);
+  int x = -1;
+  float u = 0.f;
+  if (lane < W - 1) {
+    x = __ldg(a.draft_tokens + (size_t)b * (W - 1) + lane);
+    u = __ldg(a.u + (size_t)b * (W - 1) + lane);
+  }
+  const int n_given = min(n_raw, W - 1);
   int* tokens = a.tokens + (size_t)b * W;
   if (n_given < 0) {   // takes no part (the same in every CTA of the cluster)
     if (rank == 0) {
@@ -164,21 +229,17 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
     }
     return;
   }
-  // how many drafts stand: lane i of warp 0 looks at draft i
+  // how many drafts stand
   if (warp == 0) {
     bool ok = false;
-    if (lane < n_given) {
-      const int x = __ldg(a.draft_tokens + (size_t)b * (W - 1) + lane);
-      if (x >= 0 && x < a.vocab) {
-        const float p = wide(target[((long long)b * W + lane) * a.target_stride + x]);
-        const float q =
-            draft != nullptr ? wide(draft[((long long)b * (W - 1) + lane) * a.draft_stride + x]) : 1.0f;
-        ok = (double)__ldg(a.u + (size_t)b * (W - 1) + lane) * (double)q < (double)p;
-      }
+    if (lane < W - 1 && x >= 0 && x < a.vocab) {
+      const float p = wide(target[((long long)b * W + lane) * a.target_stride + x]);
+      const float q =
+          draft != nullptr ? wide(draft[((long long)b * (W - 1) + lane) * a.draft_stride + x]) : 1.0f;
+      ok = lane < n_given && (double)u * (double)q < (double)p;
     }
-    const unsigned no = __ballot_sync(kFullMask, !ok);
-    const int n = no != 0 ? __ffs(no) - 1 : 32;
-    if (lane == 0) s_a = n;
+    const unsigned no = __ballot_sync(kFullMask, !ok);   // (lane 31 never is: W <= 32)
+    if (lane == 0) s_a = __ffs(no) - 1;
   }
   __syncthreads();
   const int n_acc = s_a;
@@ -186,17 +247,30 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
   Row<E> row;
   row.p = target + ((long long)b * W + n_acc) * a.target_stride;
   row.q = rejected && draft != nullptr ? draft + ((long long)b * (W - 1) + n_acc) * a.draft_stride : nullptr;
-  row.without = rejected && draft == nullptr ? __ldg(a.draft_tokens + (size_t)b * (W - 1) + n_acc) : -1;
+  row.without = __shfl_sync(kFullMask, x, n_acc);
+  if (!rejected || draft != nullptr) row.without = -1;
   row.vocab = a.vocab;
+  row.p_lo = static_cast<const char*>(a.target);
+  row.p_hi = reinterpret_cast<const char*>(target + ((long long)a.n_seq * W - 1) * a.target_stride + a.vocab);
+  row.q_lo = static_cast<const char*>(a.draft);
+  row.q_hi = reinterpret_cast<const char*>(draft + ((long long)a.n_seq * (W - 1) - 1) * a.draft_stride + a.vocab);
 
-  const int tiles = (a.vocab + kTile - 1) / kTile, per = (tiles + n_cta - 1) >> a.c_log2;
+  const int tiles = (a.vocab + kTile<E> - 1) / kTile<E>, per = (tiles + n_cta - 1) >> a.c_log2;
   const int t0 = min(rank * per, tiles), n_mine = min(t0 + per, tiles) - t0;
-  const uint32_t total_addr = smem_u32(s_total);
   unsigned long long S = 0, before = 0, mine = 0;
   for (int pass = 0; pass < 2; ++pass) {
     for (int t = warp; t < n_mine; t += kVerWarps) {
-      const unsigned long long v = tile_sum<E, VEC ? 16 / (int)sizeof(E) : 1>(row, t0 + t, lane);
-      if (lane == 0) s_tile[t] = v;
+      const Tile<E> tile(row, t0 + t, lane);
+      Count c = {0, 0};
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const Count ck = tile.sum(k);
+        c.h += ck.h;
+        c.l += ck.l;
+      }
+      c.h = __reduce_add_sync(kFullMask, c.h);
+      c.l = __reduce_add_sync(kFullMask, c.l);
+      if (lane == 0) s_tile[t] = total_of(c, kTile<E>);
     }
     __syncthreads();
     if (warp == 0) {
@@ -204,12 +278,12 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
       for (int t = lane; t < n_mine; t += 32) v += s_tile[t];
 #pragma unroll
       for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFullMask, v, d);
-      if (lane == 0) s_total[pass] = v;
+      if (lane < n_cta) st_dsmem_u64(smem_u32(&s_total[pass][rank]), lane, v);
     }
-    cluster_sync_all();
+    cluster_sync_all();   // (a CTA's shared memory is written by its peers before this only)
     S = before = 0;
     for (int r = 0; r < n_cta; ++r) {
-      const unsigned long long v = ld_dsmem_u64(total_addr + 8 * pass, r);
+      const unsigned long long v = s_total[pass][r];
       if (r < rank) before += v;
       if (r == rank) mine = v;
       S += v;
@@ -220,20 +294,18 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
     row.q = nullptr;
     row.without = -1;
   }
-  const float us = __ldg(a.u_sample + b);
   const unsigned long long U =
       (unsigned long long)fminf(fmaxf(us * 16777216.0f, 0.0f), 16777215.0f);   // (truncates; NaN: 0)
   const unsigned long long mark = (S >> 24) * U + (((S & 0xffffffu) * U) >> 24);
-  if (rank == 0) {
-    if (tid < W && (tid != n_acc || S == 0))
-      tokens[tid] = tid < n_acc ? __ldg(a.draft_tokens + (size_t)b * (W - 1) + tid) : -1;
-    if (tid == 0) {
+  if (rank == 0 && warp == 0) {
+    if (lane < W && (lane != n_acc || S == 0)) tokens[lane] = lane < n_acc ? x : -1;
+    if (lane == 0) {
       a.n_accepted[b] = n_acc;
       if (a.n_dropped != nullptr) a.n_dropped[b] = n_given - n_acc;
     }
   }
   if (warp == 0 && S != 0 && mark >= before && mark - before < mine) {
-    // the tile that holds the place, then the value in it
+    // the tile that holds the place, its granules' row, the lane, the value
     unsigned long long left = mark - before;   // counts to pass before the place
     int t = 0;
     for (int c = 0; c < n_mine; c += 32) {
@@ -248,28 +320,42 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
       }
       left -= __shfl_sync(kFullMask, incl, 31);
     }
-    constexpr int N = kTile / 32;
-    const int i0 = (t0 + t) * kTile + lane * N;
-    unsigned long long sum = 0;
-#pragma unroll 8
-    for (int k = 0; k < N; ++k) sum += i0 + k < a.vocab ? units(row.weight(i0 + k)) : 0;
-    const unsigned long long incl = warp_scan(sum, lane);
-    const unsigned hit = __ballot_sync(kFullMask, incl > left);
-    if (hit != 0 && lane == __ffs(hit) - 1) {
-      left -= incl - sum;
-      int i = i0;
-      for (; i < i0 + N - 1; ++i) {
-        const unsigned long long w = units(row.weight(i));
-        if (w > left) break;
-        left -= w;
+    const Tile<E> tile(row, t0 + t, lane);
+    Count c[N];
+    int at = -1;
+#pragma unroll
+    for (int k = 0; k < N; ++k) c[k] = tile.sum(k);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const Count all = {__reduce_add_sync(kFullMask, c[k].h), __reduce_add_sync(kFullMask, c[k].l)};
+      const unsigned long long sum = total_of(all, 32 * NV);
+      if (at < 0 && sum > left) {   // (the same in all lanes)
+        const unsigned long long v = total_of(c[k], NV);
+        const unsigned long long incl = warp_scan(v, lane);
+        const int src = __ffs(__ballot_sync(kFullMask, incl > left)) - 1;
+        if (lane == src) {
+          left -= incl - v;
+          bool found = false;
+#pragma unroll
+          for (int e = 0; e < NV; ++e) {
+            Count one = {0, 0};
+            add_weight(one, tile.weight(k, e));
+            const unsigned long long w = total_of(one, 1);
+            if (!found && w > left) {
+              found = true;
+              tokens[n_acc] = (t0 + t) * kTile<E> + (32 * k + lane) * NV + e;
+            }
+            if (!found) left -= w;
+          }
+        }
+        at = k;
       }
-      tokens[n_acc] = i;
+      if (at < 0) left -= sum;
     }
   }
-  cluster_sync_all();   // no CTA leaves while a peer reads its totals
 }
 
-template <int T, bool VEC>
+template <int T>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.n_seq << a.c_log2);
@@ -284,16 +370,7 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, a);
-}
-
-template <int T>
-cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
-  constexpr int E = T == KVQ_T_F32 ? 4 : 2;
-  const bool vec = (reinterpret_cast<uintptr_t>(a.target) | reinterpret_cast<uintptr_t>(a.draft) |
-                    (uintptr_t)(a.target_stride * E) | (uintptr_t)(a.draft != nullptr ? a.draft_stride * E : 0)) %
-                       16 == 0;
-  return vec ? launch<T, true>(a, s) : launch<T, false>(a, s);
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
 }
 
 }  // namespace
@@ -301,12 +378,13 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
 cudaError_t launch_verify_draft(int type, VerifyArgs a, int sms, cudaStream_t s) {
   // CTAs of a row: as many as fill the SMs, each with a tile at least
   a.c_log2 = 0;
-  const int tiles = (a.vocab + kTile - 1) / kTile;
-  while (a.c_log2 < 3 && ((long long)a.n_seq << a.c_log2) < 2LL * sms && (2 << a.c_log2) <= tiles) ++a.c_log2;
+  const int tiles = (a.vocab + 1023) / 1024;
+  while ((2 << a.c_log2) <= kMostCtas && ((long long)a.n_seq << a.c_log2) < 2LL * sms && (2 << a.c_log2) <= tiles)
+    ++a.c_log2;
   switch (type) {
-    case KVQ_T_F32: return launch_type<KVQ_T_F32>(a, s);
-    case KVQ_T_F16: return launch_type<KVQ_T_F16>(a, s);
-    case KVQ_T_BF16: return launch_type<KVQ_T_BF16>(a, s);
+    case KVQ_T_F32: return launch<KVQ_T_F32>(a, s);
+    case KVQ_T_F16: return launch<KVQ_T_F16>(a, s);
+    case KVQ_T_BF16: return launch<KVQ_T_BF16>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }
