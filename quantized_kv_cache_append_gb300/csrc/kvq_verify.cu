@@ -15,8 +15,9 @@
 // keeps its tiles' sums in shared memory, the CTAs send each other their
 // totals, the one that holds the place finds the tile and reads it once more
 // (from L2).  Rows start at any element (a vocabulary is rarely a multiple of
-// 16 bytes): lanes load the 16-byte granules their 4 or 8 values lie in, the
-// second half of one is the next lane's, and shift them into place.
+// 16 bytes): the tiles count from the 16-byte boundary before the target's
+// row, and the draft's values are shifted into place out of two 16-byte loads
+// (the second from L1).
 #include <cuda_bf16.h>
 
 #include "kvq_internal.cuh"
@@ -84,99 +85,119 @@ __device__ __forceinline__ unsigned long long total_of(const Count& c, int n) { 
 }
 
 // The row that is sampled: weights p, p - q, or p without one token, held in
-// [0, 1] (NaN: 0).  [p_lo, p_hi) and [q_lo, q_hi) are the whole arrays.
+// [0, 1] (NaN: 0).  Places count from `pad` values before the row, where the
+// target's address is a multiple of 16; weights there and behind the row
+// are 0.  [p_lo, p_hi) and [q_lo, q_hi) are the whole arrays.
 template <class E>
 struct Row {
-  const E* p;
-  const E* q;      // or null
-  int without;     // -1: none
-  int vocab;
+  const E* p;      // of place 0
+  const E* q;      // of place 0, or null
+  int without;     // a place, or -1
+  int pad, end;    // the row: places [pad, end)
   const char *p_lo, *p_hi, *q_lo, *q_hi;
 };
 
-// The granule at g, what of it lies in [lo, hi).
-template <class E>
-__device__ __forceinline__ uint4 granule(const char* g, const char* lo, const char* hi) {
-  if (g >= lo && g + 16 <= hi) return __ldg(reinterpret_cast<const uint4*>(g));
-  uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int b = 0; b < 16; b += (int)sizeof(E))
-    if (g + b >= lo && g + b < hi) {
-      if constexpr (sizeof(E) == 4) w[b / 4] = __ldg(reinterpret_cast<const uint32_t*>(g + b));
-      else w[b / 4] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(g + b)) << (8 * (b & 3));
-    }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// The 16 bytes that start 4 WORDS + bits / 8 bytes into v0 | v1.
+template <int WORDS>
+__device__ __forceinline__ uint4 shifted(const uint4& v0, const uint4& v1, int bits) {
+  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+  return make_uint4(__funnelshift_r(w[WORDS], w[WORDS + 1], bits), __funnelshift_r(w[WORDS + 1], w[WORDS + 2], bits),
+                    __funnelshift_r(w[WORDS + 2], w[WORDS + 3], bits),
+                    __funnelshift_r(w[WORDS + 3], w[WORDS + 4], bits));
 }
 
-// The 16 bytes that start s bytes into v0 | v1.
-__device__ __forceinline__ uint4 shifted(const uint4& v0, const uint4& v1, int s) {
-  uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-  if (s & 8) {
+// Bytes p + 512 k + 0 .. 15, k < kGranules; the granules that hold them are
+// all in the array.
+__device__ __forceinline__ void load_tile(const char* p, uint4 (&v)[kGranules]) {
+  const int s = (int)(reinterpret_cast<uintptr_t>(p) & 15);   // (the same in all lanes)
+  const uint4* g = reinterpret_cast<const uint4*>(p - s);
 #pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (s & 4) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  const int bits = 8 * (s & 3);
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
-// Values i0 + (32 k + lane) NV .. + NV - 1 of a row, k < kGranules, for all lanes.
-template <class E>
-__device__ __forceinline__ void load_tile(const E* row, const char* lo, const char* hi, int i0, int lane, uint4 (&v)[kGranules]) {
-  const char* p = reinterpret_cast<const char*>(row + i0) + lane * 16;
-  const int s = (int)(reinterpret_cast<uintptr_t>(row) & 15);   // (i0 is a multiple of NV)
-#pragma unroll
-  for (int k = 0; k < kGranules; ++k) v[k] = granule<E>(p - s + 512 * k, lo, hi);
+  for (int k = 0; k < kGranules; ++k) v[k] = __ldg(g + 32 * k);
   if (s != 0) {
-    uint4 last[kGranules];
+    uint4 n[kGranules];
+    const int bits = 8 * (s & 3);
+#pragma unroll
+    for (int k = 0; k < kGranules; ++k) n[k] = __ldg(g + 32 * k + 1);
+    switch (s >> 2) {
+      case 0:
+#pragma unroll
+        for (int k = 0; k < kGranules; ++k) v[k] = shifted<0>(v[k], n[k], bits);
+        break;
+      case 1:
+#pragma unroll
+        for (int k = 0; k < kGranules; ++k) v[k] = shifted<1>(v[k], n[k], bits);
+        break;
+      case 2:
+#pragma unroll
+        for (int k = 0; k < kGranules; ++k) v[k] = shifted<2>(v[k], n[k], bits);
+        break;
+      default:
+#pragma unroll
+        for (int k = 0; k < kGranules; ++k) v[k] = shifted<3>(v[k], n[k], bits);
+    }
+  }
+}
+
+// Whether a tile's granules lie in the array (t: its first byte).
+__device__ __forceinline__ bool inside(const char* t, const char* lo, const char* hi) {
+  const int s = (int)(reinterpret_cast<uintptr_t>(t) & 15);
+  return t - s >= lo && t - s + 512 * kGranules + (s != 0 ? 16 : 0) <= hi;
+}
+
+// A lane's weights of a tile: r[k NV + e] is that of place (32 k + lane) NV + e
+// of it.
+template <class E>
+__device__ __forceinline__ void tile_weights(const Row<E>& row, int tile, int lane, float (&r)[kTile<E> / 32]) {
+  constexpr int NV = 16 / (int)sizeof(E);
+  const int i0 = tile * kTile<E>, at0 = i0 + lane * NV;
+  const char *tp = reinterpret_cast<const char*>(row.p + i0), *tq = reinterpret_cast<const char*>(row.q + i0);
+  const bool has_q = row.q != nullptr;
+  if (inside(tp, row.p_lo, row.p_hi) && (!has_q || inside(tq, row.q_lo, row.q_hi))) {
+    uint4 p[kGranules], q[kGranules];
+    load_tile(tp + 16 * lane, p);
+    if (has_q) {
+      load_tile(tq + 16 * lane, q);
+#pragma unroll
+      for (int k = 0; k < kGranules; ++k)
+#pragma unroll
+        for (int e = 0; e < NV; ++e) r[k * NV + e] = __saturatef(value<E>(p[k], e) - value<E>(q[k], e));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kGranules; ++k)
+#pragma unroll
+        for (int e = 0; e < NV; ++e) r[k * NV + e] = __saturatef(value<E>(p[k], e));
+    }
+  } else {   // at an array's ends, value by value
 #pragma unroll
     for (int k = 0; k < kGranules; ++k)
-      last[k] = lane == 31 ? granule<E>(p - s + 512 * k + 16, lo, hi) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int k = 0; k < kGranules; ++k) {
-      uint4 n = make_uint4(__shfl_down_sync(kFullMask, v[k].x, 1), __shfl_down_sync(kFullMask, v[k].y, 1),
-                           __shfl_down_sync(kFullMask, v[k].z, 1), __shfl_down_sync(kFullMask, v[k].w, 1));
-      if (lane == 31) n = last[k];
-      v[k] = shifted(v[k], n, s);
-    }
+      for (int e = 0; e < NV; ++e) {
+        const int i = at0 + 32 * NV * k + e;
+        const bool in = i >= row.pad && i < row.end;
+        float x = in ? wide(row.p[i]) : 0.f;
+        if (in && has_q) x -= wide(row.q[i]);
+        r[k * NV + e] = __saturatef(x);
+      }
+  }
+  // the places outside the row, and the one left out: in few tiles
+  if (i0 < row.pad || i0 + kTile<E> > row.end || (unsigned)(row.without - i0) < (unsigned)kTile<E>) {
+#pragma unroll
+    for (int k = 0; k < kGranules; ++k)
+#pragma unroll
+      for (int e = 0; e < NV; ++e) {
+        const int i = at0 + 32 * NV * k + e;
+        if (i < row.pad || i >= row.end || i == row.without) r[k * NV + e] = 0.f;
+      }
   }
 }
 
-// Weight e of granule k of a lane's share of a tile (behind the row's end: 0).
-template <class E>
-struct Tile {
-  static constexpr int NV = 16 / (int)sizeof(E);
-  uint4 p[kGranules], q[kGranules];
-  int i0, left, without, lane;   // left: values from i0 to the row's end
-  bool has_q;
-
-  __device__ __forceinline__ Tile(const Row<E>& row, int tile, int lane_) : lane(lane_) {
-    i0 = tile * kTile<E>;
-    left = row.vocab - i0;
-    without = row.without;
-    has_q = row.q != nullptr;
-    load_tile<E>(row.p, row.p_lo, row.p_hi, i0, lane, p);
-    if (has_q) load_tile<E>(row.q, row.q_lo, row.q_hi, i0, lane, q);
-  }
-  __device__ __forceinline__ float weight(int k, int e) const {
-    const float x = value<E>(p[k], e);
-    const int at = (32 * k + lane) * NV + e;
-    float r = has_q ? __saturatef(x - value<E>(q[k], e)) : __saturatef(x);
-    if (without >= 0 && i0 + at == without) r = 0.f;
-    if (left < kTile<E> && at >= left) r = 0.f;
-    return r;
-  }
-  __device__ __forceinline__ Count sum(int k) const {
-    Count c = {0, 0};
+template <int N>
+__device__ __forceinline__ Count count_of(const float* r) {
+  Count c = {0, 0};
 #pragma unroll
-    for (int e = 0; e < NV; ++e) add_weight(c, weight(k, e));
-    return c;
-  }
-};
+  for (int e = 0; e < N; ++e) add_weight(c, r[e]);
+  return c;
+}
 
 __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, int lane) {
 #pragma unroll
@@ -193,11 +214,13 @@ __device__ __forceinline__ void st_dsmem_u64(uint32_t addr, int rank, unsigned l
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote), "l"(v) : "memory");
 }
 
+// 4 CTAs an SM: 256 sequences of 131075 bf16 tokens 24.8 us, and a few spilled
+// words in the rare paths (2 or 3 CTAs 32 us, 5 31 us; half tiles 28 to 39 us).
 template <int T>
-__global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
   using E = typename Prob<T>::type;
   constexpr int NV = 16 / (int)sizeof(E), N = kGranules;
-  __shared__ unsigned long long s_tile[(1 << 20) / kTile<E>];
+  __shared__ unsigned long long s_tile[(1 << 20) / kTile<E> + 1];
   __shared__ unsigned long long s_total[2][kMostCtas];   // [residual, row][CTA], sent by each of them
   __shared__ int s_a;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -245,29 +268,26 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
   const int n_acc = s_a;
   const bool rejected = n_acc < n_given;
   Row<E> row;
-  row.p = target + ((long long)b * W + n_acc) * a.target_stride;
-  row.q = rejected && draft != nullptr ? draft + ((long long)b * (W - 1) + n_acc) * a.draft_stride : nullptr;
+  const E* first = target + ((long long)b * W + n_acc) * a.target_stride;
+  row.pad = (int)((reinterpret_cast<uintptr_t>(first) & 15) / sizeof(E));
+  row.end = row.pad + a.vocab;
+  row.p = first - row.pad;
+  row.q = rejected && draft != nullptr ? draft + ((long long)b * (W - 1) + n_acc) * a.draft_stride - row.pad : nullptr;
   row.without = __shfl_sync(kFullMask, x, n_acc);
-  if (!rejected || draft != nullptr) row.without = -1;
-  row.vocab = a.vocab;
+  row.without = rejected && draft == nullptr && row.without >= 0 && row.without < a.vocab ? row.without + row.pad : -1;
   row.p_lo = static_cast<const char*>(a.target);
   row.p_hi = reinterpret_cast<const char*>(target + ((long long)a.n_seq * W - 1) * a.target_stride + a.vocab);
   row.q_lo = static_cast<const char*>(a.draft);
   row.q_hi = reinterpret_cast<const char*>(draft + ((long long)a.n_seq * (W - 1) - 1) * a.draft_stride + a.vocab);
 
-  const int tiles = (a.vocab + kTile<E> - 1) / kTile<E>, per = (tiles + n_cta - 1) >> a.c_log2;
+  const int tiles = (row.end + kTile<E> - 1) / kTile<E>, per = (tiles + n_cta - 1) >> a.c_log2;
   const int t0 = min(rank * per, tiles), n_mine = min(t0 + per, tiles) - t0;
   unsigned long long S = 0, before = 0, mine = 0;
   for (int pass = 0; pass < 2; ++pass) {
     for (int t = warp; t < n_mine; t += kVerWarps) {
-      const Tile<E> tile(row, t0 + t, lane);
-      Count c = {0, 0};
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const Count ck = tile.sum(k);
-        c.h += ck.h;
-        c.l += ck.l;
-      }
+      float r[kTile<E> / 32];
+      tile_weights<E>(row, t0 + t, lane, r);
+      Count c = count_of<kTile<E> / 32>(r);
       c.h = __reduce_add_sync(kFullMask, c.h);
       c.l = __reduce_add_sync(kFullMask, c.l);
       if (lane == 0) s_tile[t] = total_of(c, kTile<E>);
@@ -320,11 +340,12 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
       }
       left -= __shfl_sync(kFullMask, incl, 31);
     }
-    const Tile<E> tile(row, t0 + t, lane);
+    float r[kTile<E> / 32];
+    tile_weights<E>(row, t0 + t, lane, r);
     Count c[N];
     int at = -1;
 #pragma unroll
-    for (int k = 0; k < N; ++k) c[k] = tile.sum(k);
+    for (int k = 0; k < N; ++k) c[k] = count_of<NV>(r + k * NV);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const Count all = {__reduce_add_sync(kFullMask, c[k].h), __reduce_add_sync(kFullMask, c[k].l)};
@@ -339,11 +360,11 @@ __global__ void __launch_bounds__(kVerThreads) verify_kernel(const __grid_consta
 #pragma unroll
           for (int e = 0; e < NV; ++e) {
             Count one = {0, 0};
-            add_weight(one, tile.weight(k, e));
+            add_weight(one, r[k * NV + e]);
             const unsigned long long w = total_of(one, 1);
             if (!found && w > left) {
               found = true;
-              tokens[n_acc] = (t0 + t) * kTile<E> + (32 * k + lane) * NV + e;
+              tokens[n_acc] = (t0 + t) * kTile<E> + (32 * k + lane) * NV + e - row.pad;
             }
             if (!found) left -= w;
           }
