@@ -266,8 +266,7 @@ struct RotaryArgs {
   const float* q_norm;         // [hd] or null
   const float* k_norm;
   int n_tok, n_q, n_seq, max_blocks, n_axes, rot_dim, interleaved;
-  int parts;                   // warps that share a token's heads
-  FastDiv div_parts;
+  int mod_k, mod_v;            // blocks of heads before the keys and the values, modulo the warps of a token
   float eps, gain;
 };
 
