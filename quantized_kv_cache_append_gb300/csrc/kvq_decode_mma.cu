@@ -595,6 +595,44 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     }
   };
 
+  // Scored: the same by a whole warp, a copy a lane (a stage of blocks of 16 cells
+  // is up to 32 copies).
+  auto issue_warp = [&](int it, bool from_smem) {
+    constexpr int NC = C::NCH + C::VNCH + (C::KI8 ? 2 : 0);   // copies of a piece
+    static_assert(!kScores || MAXP * NC <= 32, "a copy a lane");
+    const int s = it % C::STAGES;
+    const int pc = 1 << pc_log2, bsz = 1 << a.pool.bs_log2;
+    const int p = lane / NC, c = lane - p * NC;
+    int row = -1;
+    uint32_t bytes = 0;
+    if (p < n_pieces) {
+      const int blk = piece_blk(it, p, from_smem), cell = c_begin + it * kTC + (p << pc_log2);
+      if (blk >= 0 && blk < a.pool.n_blocks) {
+        row = (blk * a.pool.n_kv + pool_h) * bsz + (cell & (bsz - 1));
+        bytes = (uint32_t)pc * (c < C::NCH ? C::SWB : c < C::NCH + C::VNCH ? C::VSWB
+                                                    : c == NC - 2          ? C::NG * 2
+                                                                           : C::VNS * 2);
+      }
+    }
+    const uint32_t full = bar_full + 8 * s, total = __reduce_add_sync(kFull, bytes);
+    if (lane == 0) mbar_expect_tx(full, total + a.extra_tx);
+    __syncwarp();
+    if (row >= 0) {
+      const uint32_t st = sbase + s * C::STAGE_B;
+      if (c < C::NCH) {
+        tma_load_2d_hint(st + (uint32_t)(c * kTC + (p << pc_log2)) * C::SWB, &maps.k[c], 0, row, full, pol);
+      } else if (c < C::NCH + C::VNCH) {
+        const int sp = c - C::NCH;
+        tma_load_2d_hint(st + C::OFF_V + (uint32_t)(sp * kTC + (p << pc_log2)) * C::VSWB, &maps.v[sp], 0, row, full, pol);
+      } else if constexpr (C::KI8) {
+        const uint32_t sc = sbase + C::SMEM_SC + (uint32_t)s * C::SC_STAGE_B;
+        if (c == NC - 2) bulk_load_hint(sc + (uint32_t)p * bytes, a.pool.ks + (size_t)row * C::NG, bytes, full, pol);
+        else bulk_load_hint(sc + C::KSCALE_B + (uint32_t)p * bytes, a.pool.vs + (size_t)row * C::VNS, bytes, full, pol);
+      }
+    }
+    __syncwarp();
+  };
+
   // Prologue.  Every small load (q, the split's block ids) is issued first,
   // into registers; only then does thread 0 start the first stages' bulk
   // copies.  Issued the other way round, these few latency-critical loads
@@ -635,7 +673,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
                 : -1;
   }
   bool lost = false;
-  if (producer) {
+  if constexpr (kScores) {
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+          mbar_init(bar_full + 8 * s, 1);
+          s_rel[s] = 0;
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      }
+      __syncwarp();
+      if (n_first > 0) issue_warp(0, false);
+    }
+  } else if (producer) {
     // the block ids of every first-wave piece are loaded together, before
     // the first copy is issued
     int fb[C::STAGES][MAXP];
@@ -697,7 +747,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       return;
     }
   }
-  if (producer) {
+  if (kScores && warp == 0) {
+    for (int it = 1; it < n_first; ++it) issue_warp(it, blk_in_smem);
+  }
+  if (!kScores && producer) {
     for (int it = 1; it < n_first; ++it) {
       int nb[MAXP];
       tile_blks(it, blk_in_smem, nb);
@@ -1299,6 +1352,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   auto release = [&](int it) {
     // the last warp to let the stage go issues its refill
     __syncwarp();
+    if constexpr (kScores) {
+      const int s = it % C::STAGES;
+      int prev = 0;
+      if (lane == 0) {
+        asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;"
+                     : "=r"(prev)
+                     : "r"(smem_u32(s_rel + s))
+                     : "memory");
+        if (prev == kConsumerWarps - 1) s_rel[s] = 0;
+      }
+      prev = __shfl_sync(kFull, prev, 0);
+      if (prev == kConsumerWarps - 1 && it + C::STAGES < n_tiles) {
+        __syncwarp();   // (lane 0's acquire holds for the lanes that issue)
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        issue_warp(it + C::STAGES, blk_in_smem);
+      }
+      return;
+    }
     if (lane == 0) {
       const int s = it % C::STAGES;
       // acquire-release: this warp's reads of the stage happen before the
