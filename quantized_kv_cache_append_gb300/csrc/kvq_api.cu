@@ -93,7 +93,7 @@ bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, Dec
   const bool lists = kind == Decode::kLists;
   const int G = n_q / c->n_kv_heads;
   p->rows = G * W;
-  const int cta_rows = mma_rows_per_cta(c->head_dim);
+  const int cta_rows = kind == Decode::kScored ? scores_rows_per_cta(c->head_dim) : mma_rows_per_cta(c->head_dim);
   p->rt_rows = p->rows < cta_rows ? p->rows : cta_rows;
   p->n_rt = (p->rows + p->rt_rows - 1) / p->rt_rows;
   int per_sm = lists                      ? lists_ctas_per_sm(c->fmt, c->head_dim, p->rt_rows)

@@ -389,7 +389,10 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return sbase + OFF_BAR + 8 * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int kvh = blockIdx.y;
+  // (scored: the KV heads of a row tile are neighbours in the grid, so the long
+  // row tiles of all heads start first)
+  const int row_tile = kScores ? (int)blockIdx.x / a.n_kv : (int)blockIdx.x;
+  const int kvh = kScores ? (int)blockIdx.x - row_tile * a.n_kv : (int)blockIdx.y;
   const uint32_t wl = LW ? a.wait_limit : kDefaultWaitLimit;   // polls before a wait is lost
   const uint32_t extra_tx = LW ? a.extra_tx : 0u;
   // row tiles in descending order: the last ones (later tokens) see the
@@ -398,7 +401,8 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   // (with first cells given, the tokens that go on with an older document are
   // the chunk's first and see the most: ascending)
   const bool ascending = kScores && a.first != nullptr;
-  const int r0 = (int)(ascending ? blockIdx.x : gridDim.x - 1 - blockIdx.x) * BM;
+  const int n_row_tiles = kScores ? (a.T * a.G + BM - 1) / BM : (int)gridDim.x;
+  const int r0 = (ascending ? row_tile : n_row_tiles - 1 - row_tile) * BM;
   const int n_rows = a.T * a.G;
   const int P0 = a.P - a.T;                 // cells before the chunk
   const int t_last = min(a.T - 1, (min(r0 + BM, n_rows) - 1) / a.G);
@@ -874,7 +878,7 @@ cudaError_t launch_tc_kernel(const ChunkArgs& a, cudaStream_t s) {
       return cudaErrorInvalidValue;
   }
   const long long row_tiles = ((long long)a.T * a.G + tcc::BM - 1) / tcc::BM;
-  if (row_tiles > 0x7fffffffLL || a.n_kv > 65535) return cudaErrorInvalidValue;
+  if (row_tiles * (kScores ? a.n_kv : 1) > 0x7fffffffLL || a.n_kv > 65535) return cudaErrorInvalidValue;
   int n_all = (a.P + Lay::BN - 1) / Lay::BN;
   if (kScores && a.window > 0 && a.last == nullptr) {   // the window of a row tile's tokens, and the tiles it cuts
     const long long cells = (long long)a.window + (tcc::BM + a.G - 1) / a.G;
@@ -883,7 +887,9 @@ cudaError_t launch_tc_kernel(const ChunkArgs& a, cudaStream_t s) {
   const int n_split = tc_key_splits<HD, LW>(row_tiles * a.n_kv, n_all);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
-      tc_config<HD>(dim3((unsigned)row_tiles, (unsigned)a.n_kv, (unsigned)n_split), n_split, s, attr);
+      tc_config<HD>(kScores ? dim3((unsigned)(row_tiles * a.n_kv), 1, (unsigned)n_split)
+                            : dim3((unsigned)row_tiles, (unsigned)a.n_kv, (unsigned)n_split),
+                    n_split, s, attr);
   return cudaLaunchKernelEx(&cfg, chunk_attn_tc<HD, LW>, maps, a);
 }
 

@@ -128,7 +128,11 @@ struct Cfg {
   // (the merge at the end reuses the stages for 4 warp slabs of RP x HD
   // fp32, which takes a fourth stage for 32-row int8 HD 64 tiles)
   static constexpr int SLAB_B = kConsumerWarps * NT * 8 * HD * 4;
-  static constexpr int STAGES = kScores && HD == 256 && V4 ? 2 : (SLAB_B + STAGE_B - 1) / STAGE_B > 3 ? (SLAB_B + STAGE_B - 1) / STAGE_B : 3;
+  // Scored, head_dim 256 of int8 keys: two stages where that is one more CTA an SM
+  // (K8V4 with 8 rows: 3; int8 with 16: 2), since the instructions, not the
+  // copies, bound them (2 x 98000 cells, 2 heads, 32 rows, blocks of 256: int8
+  // 160 us with 8 rows a CTA and 3 stages, 202 with 16 and 3, 144 with 16 and 2).
+  static constexpr int STAGES = kScores && HD == 256 && (V4 ? NT == 1 : KI8 && NT == 2) ? 2 : (SLAB_B + STAGE_B - 1) / STAGE_B > 3 ? (SLAB_B + STAGE_B - 1) / STAGE_B : 3;
   static constexpr int OFF_V = TILE_B;
   static constexpr int SMEM_SC = STAGES * STAGE_B;  // [STAGES]{K [64][NG], V [64][VNS]} fp16
   // q as fp16 hi / lo rows, padded by 16 bytes so ldmatrix rows hit distinct banks
@@ -1843,7 +1847,7 @@ int ctas_per_sm_hd(int code) {
   switch (code) {
     case 0: return ctas_per_sm_impl<FMT, HD, 1, true>();
     case 1: return ctas_per_sm_impl<FMT, HD, 1, false>();
-    case 2: if constexpr (HD <= 128) return ctas_per_sm_impl<FMT, HD, 2, false>(); break;
+    case 2: if constexpr (HD <= 128 || kScores) return ctas_per_sm_impl<FMT, HD, 2, false>(); break;
     case 4: if constexpr (HD <= 64) return ctas_per_sm_impl<FMT, HD, 4, false>(); break;
   }
   return 0;
@@ -1854,7 +1858,7 @@ cudaError_t launch_hd(int code, const DecodePlan& p, const DecodeArgs& a, cudaSt
   switch (code) {
     case 0: return launch_impl<FMT, HD, 1, true>(p, a, s);
     case 1: return launch_impl<FMT, HD, 1, false>(p, a, s);
-    case 2: if constexpr (HD <= 128) return launch_impl<FMT, HD, 2, false>(p, a, s); break;
+    case 2: if constexpr (HD <= 128 || kScores) return launch_impl<FMT, HD, 2, false>(p, a, s); break;
     case 4: if constexpr (HD <= 64) return launch_impl<FMT, HD, 4, false>(p, a, s); break;
   }
   return cudaErrorInvalidValue;
@@ -1916,6 +1920,11 @@ bool mma_decode_supported(int fmt, int hd, int rows) {
 // (HD / 16 m-tiles x 4 floats per tile and thread) stay at 32 per thread
 // or fewer -- 32 rows at head_dim 64, 16 at 128, 8 at 256.
 int mma_rows_per_cta(int hd) { return 8 * (256 / hd); }
+// Scored: 16 at 256 too, twice the accumulators, but half of the widening and of
+// the copies a row (2 x 98000 cells, 2 heads, 32 rows of 256 dims, blocks of 16 /
+// 256: FP16 317 / 217 -> 219 / 173 us, int8 202 / 160 -> 164 / 144, K8V4 180 / 147 ->
+// 169 / 152).
+int scores_rows_per_cta(int hd) { return hd == 256 ? 16 : mma_rows_per_cta(hd); }
 
 int mma_cell_tile() { return kTC; }
 

@@ -351,6 +351,7 @@ cudaError_t launch_decode_lists(int fmt, int hd, const DecodePlan& p, const Deco
 
 // The same with capped, biased and windowed scores (kvq_decode_scores.cu).
 int scores_ctas_per_sm(int fmt, int hd, int rows);
+int scores_rows_per_cta(int hd);
 cudaError_t launch_decode_scores(int fmt, int hd, const DecodePlan& p, const DecodeArgs& a, cudaStream_t s);
 
 // The driver's cuTensorMapEncodeTiled (version 12000), looked up once; null
