@@ -775,6 +775,7 @@ kvq_status chunk_impl(const void* k16, const void* v16, int n_kv_heads, int P, i
   a.qscale = sm_scale * 1.4426950408889634f;  // log2(e)
   a.wait_limit = wait_limit;
   a.extra_tx = extra_tx;
+  a.div_g = make_fastdiv((unsigned)a.G);
   a.out_any = out;
   a.out_type = out_type;
   a.cap2 = a.cap2_inv = 0.0f;

@@ -203,7 +203,7 @@ __device__ __forceinline__ void pair_sync(int warp) {
 }
 
 struct Key {
-  int j0, n_tiles, P0;   // the CTA's first key tile, its tiles, the cells before the chunk
+  int j0, n_tiles, P0, r0;   // the CTA's first key tile, its tiles, the cells before the chunk, its first row
 };
 
 // The softmax of a scored chunk: thread = (query row, half of the columns).
@@ -225,22 +225,33 @@ __device__ __forceinline__ bool softmax_scored(const ChunkArgs& a, unsigned char
   const float slope =
       valid && a.slopes != nullptr ? 1.4426950408889634f * __ldg(a.slopes + kvh * a.G + gg) : 0.f;
   {
-    // this half of the row's q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand
-    const float* qrow = a.q + ((size_t)tok * a.n_q + (size_t)kvh * a.G + gg) * HD;
-#pragma unroll 8
-    for (int i = 0; i < HD / 16; ++i) {
-      const int c = half * (HD / 16) + i;
-      float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
-      if (valid) {
-        x0 = __ldg(reinterpret_cast<const float4*>(qrow + 8 * c));
-        x1 = __ldg(reinterpret_cast<const float4*>(qrow + 8 * c + 4));
+    // q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand, 8 dims a step,
+    // neighbours of a row by neighbouring lanes (row by row a thread, as the plain
+    // kernel does it, these loads took 3.9 us of a CTA)
+    constexpr int CH = HD / 8, N = tcc::BM * CH / (kSoftWarps * 32);
+    const int n_rows = a.T * a.G;
+    float4 x0[N], x1[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (int)threadIdx.x + i * kSoftWarps * 32, gr = key.r0 + at / CH, c = at % CH;
+      x0[i] = x1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (gr < n_rows) {
+        const int t = (int)fdiv((unsigned)gr, a.div_g);
+        const float4* src = reinterpret_cast<const float4*>(
+            a.q + ((size_t)t * a.n_q + (size_t)kvh * a.G + (gr - t * a.G)) * HD + 8 * c);
+        x0[i] = __ldg(src);
+        x1[i] = __ldg(src + 1);
       }
-      const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (int)threadIdx.x + i * kSoftWarps * 32, r = at / CH, c = at % CH;
+      const float x[8] = {x0[i].x, x0[i].y, x0[i].z, x0[i].w, x1[i].x, x1[i].y, x1[i].z, x1[i].w};
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) split_pair(x[2 * e] * a.qscale, x[2 * e + 1] * a.qscale, hi[e], lo[e]);
-      *reinterpret_cast<uint4*>(smem + Lay::OFF_QH + sw(row, c * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(smem + Lay::OFF_QL + sw(row, c * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint4*>(smem + Lay::OFF_QH + sw(r, c * 16)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(smem + Lay::OFF_QL + sw(r, c * 16)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar(QREADY)) : "memory");
@@ -367,6 +378,22 @@ __device__ __forceinline__ bool softmax_scored(const ChunkArgs& a, unsigned char
   }
   if (!lost && key.n_tiles > 0) lost = __any_sync(kAll, !mbar_wait(bar(ALLDONE), 0, wl));
   return lost;
+}
+
+// 8 output values of a row, at value index i (a multiple of 8)
+__device__ __forceinline__ void store8(const ChunkArgs& a, size_t i, const float (&v)[8]) {
+  if (!kScores || a.out_type == KVQ_T_F32) {
+    store4(a, i, make_float4(v[0], v[1], v[2], v[3]));
+    store4(a, i + 4, make_float4(v[4], v[5], v[6], v[7]));
+    return;
+  }
+  uint32_t u[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (a.out_type == KVQ_T_F16) u[e] = pack_half2(v[2 * e], v[2 * e + 1]);
+    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_any) + i) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
 // LW: the lost-wait test's instantiation, whose waits take their poll limit
@@ -580,7 +607,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
       (void)mbar_wait(bar(PDRAIN), 0, wl);
     }
   } else if constexpr (kScores) {
-    lost = softmax_scored<HD>(a, smem, sbase, tmem, Key{j0, n_tiles, P0}, row, tok, kvh, gg, valid, wl, s_pair, s_flag, m, l);
+    lost = softmax_scored<HD>(a, smem, sbase, tmem, Key{j0, n_tiles, P0, r0}, row, tok, kvh, gg, valid, wl, s_pair, s_flag, m, l);
   } else {
     // ---------------- softmax warps: thread = query row ----------------
     const int lim = valid ? P0 + tok : -1;                  // last key this row sees
@@ -704,9 +731,19 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         tmem_ld32(tmem + lane_base + COL_O + c0, ov);
         tmem_wait_ld();
         if (valid) {
-          if (kScores && l == 0.f) {   // the row sees no key (O may not even have been written)
+          if constexpr (kScores) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = 0u;
+            for (int e = 0; e < 32; e += 8) {
+              float v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                // (a row that sees no key: 0; O may not even have been written)
+                v[k] = l == 0.f ? 0.f : __uint_as_float(ov[e + k]) * inv;
+                if (lost) v[k] = nan;
+              }
+              store8(a, orow + c0 + e, v);
+            }
+            continue;
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {

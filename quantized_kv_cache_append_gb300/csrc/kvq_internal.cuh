@@ -409,6 +409,7 @@ struct ChunkArgs {
   // Scored (kvq_chunk_attn_scored), unread elsewhere.
   void* out_any;       // out, of out_type
   int out_type;        // kvq_type
+  FastDiv div_g;       // G
   float cap2, cap2_inv;  // softcap * log2(e) and its inverse; 0: no cap
   const float* slopes; // [n_q] or null
   const int32_t* first;  // [T] or null: first cell a token sees
