@@ -11,6 +11,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "kvq_batch_splits.h"
 #include "kvq_internal.cuh"
 
 #define KVQ_API extern "C" __attribute__((visibility("default")))
@@ -109,6 +110,10 @@ bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, Dec
   const long long capacity = (long long)per_sm * sms;
   const long long target = capacity * (lists ? kListWaves : n_seq > 1 ? 4 : 1);
   p->c_log2 = -1;
+  p->batch_items = 0;
+  p->off_base = 0;
+  if (kind == Decode::kScored && (long long)n_seq * (tiles + 1) < (1LL << 30))   // (summed in 32 bits)
+    p->batch_items = batch_items(capacity, c->n_kv_heads * p->n_rt, n_seq);
   DecodePlan in_cluster = *p;
   if (lists) {
     // Splits of a row tile in one cluster of up to 8, merged there, if that
@@ -139,10 +144,14 @@ bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, Dec
     const int split_tiles = (int)((tiles + ns - 1) / ns);
     p->split_cells = split_tiles * tile;
     p->nsplit = (max_ctx + p->split_cells - 1) / p->split_cells;
-    const size_t parts = (size_t)n_seq * c->n_kv_heads * p->nsplit * p->rows;
+    const size_t parts = (size_t)c->n_kv_heads * (p->batch_items > 0 ? p->batch_items : (size_t)n_seq * p->nsplit) * p->rows;
     p->off_o = 0;
     p->off_ml = round_up(parts * c->head_dim * sizeof(float), 256);
     p->bytes = p->off_ml + round_up(parts * 2 * sizeof(float), 256);
+    if (p->batch_items > 0) {
+      p->off_base = p->bytes;
+      p->bytes += round_up((n_seq + 1) * sizeof(int), 256);
+    }
     if (p->bytes <= max_bytes) return true;
     if (lists) {
       *p = in_cluster;
@@ -318,6 +327,8 @@ kvq_status decode_impl(const kvq_cache* cache, const float* q, int n_seq, int W,
   a.first = nullptr;
   a.window = 0;
   a.whole = 1;
+  a.batch_items = plan.batch_items;
+  a.ws_base = reinterpret_cast<int*>(static_cast<char*>(workspace) + plan.off_base);
   cudaError_t e;
   if (scores != nullptr) {
     if (scores->softcap > 0.0f) {

@@ -51,6 +51,7 @@
 
 #include <mutex>
 
+#include "kvq_batch_splits.h"
 #include "kvq_internal.cuh"
 #include "kvq_ptx.cuh"
 #include "kvq_tanh.cuh"
@@ -289,6 +290,74 @@ __device__ __forceinline__ bool item_of(const DecodeArgs& a, int c, int& b, int&
   return false;
 }
 
+// Scored batches: the tiles of sequences lane + 32 i, the split length chosen
+// from them, and the item of CTA c (false: past the last): full splits first,
+// as above; slot: its number among the splits of its KV head.
+struct Batch {
+  int tiles[kBatchMaxSeq / 32];
+  int split;   // tiles
+};
+
+__device__ __forceinline__ int sum_splits(const DecodeArgs& a, const Batch& t, int split, int below) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kBatchMaxSeq / 32; ++i)
+    if (32 * i < a.n_seq && lane + 32 * i < below) n += (t.tiles[i] + split - 1) / split;
+  return __reduce_add_sync(kFull, n);
+}
+
+__device__ __forceinline__ Batch batch_of(const DecodeArgs& a) {
+  const int lane = threadIdx.x & 31;
+  Batch t;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kBatchMaxSeq / 32; ++i) {
+    const int b = lane + 32 * i;
+    t.tiles[i] = 0;
+    if (b < a.n_seq) {
+      const Span sp = span_of(a, b, __ldg(a.ctx_lens + b));
+      t.tiles[i] = (sp.end - sp.base + kTC - 1) / kTC;
+    }
+    n += t.tiles[i];
+  }
+  t.split = batch_split((long long)__reduce_add_sync(kFull, n), a.batch_items, a.n_seq,
+                        [&](int s) { return sum_splits(a, t, s, a.n_seq); });
+  return t;
+}
+
+__device__ __forceinline__ bool batch_item(const DecodeArgs& a, const Batch& t, int c, int& b, int& kvh, int& split,
+                                           int& slot) {
+  const int lane = threadIdx.x & 31;
+  int k = (int)fdiv((unsigned)c, a.div_nkv);
+  kvh = c - k * a.n_kv;
+  for (int pass = 0; pass < 2; ++pass) {   // 0: full splits, 1: last partial splits
+#pragma unroll
+    for (int i = 0; i < kBatchMaxSeq / 32; ++i) {
+      if (32 * i >= a.n_seq) break;
+      const int full = t.tiles[i] / t.split;
+      const int n = pass == 0 ? full : t.tiles[i] - full * t.split != 0;
+      int incl = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(kFull, incl, off);
+        if (lane >= off) incl += y;
+      }
+      const unsigned m = __ballot_sync(kFull, incl > k);
+      if (m != 0) {
+        const int src = __ffs(m) - 1;
+        const int before = __shfl_sync(kFull, incl - n, src), q = __shfl_sync(kFull, full, src);
+        b = 32 * i + src;
+        split = pass == 0 ? k - before : q;
+        slot = sum_splits(a, t, t.split, b) + split;
+        return true;
+      }
+      k -= __shfl_sync(kFull, incl, 31);
+    }
+  }
+  return false;
+}
+
 // ---------------------------------------------------------------------------
 // Block lists, the splits of a row tile in one thread-block cluster: the CTAs'
 // rows meet through distributed shared memory and the output is written
@@ -503,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   const int Rc = min(a.RT, a.R - r0);                         // and its row count
   int b, kvh, split;
   int L_raw = 0;
+  int slot = 0, split_cells = a.split_cells;   // scored batches: chosen below
   // (lists too: their block ids are copied ahead of the length, -1 past the end)
   const bool single = kLists || a.n_seq == 1;
   if (single && !kLists) {
@@ -516,6 +586,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     b = clustered ? item : item - split * a.n_seq;
     kvh = 0;
     L_raw = __ldg(a.ctx_lens + b);
+  } else if (kScores && a.batch_items > 0) {
+    const Batch t = batch_of(a);
+    split_cells = t.split * kTC;
+    if (blockIdx.x == 0) {   // where each sequence's splits begin, for the combine
+      for (int s = threadIdx.x >> 5; s <= a.n_seq; s += kConsumerWarps) {
+        const int first = sum_splits(a, t, t.split, s);
+        if ((threadIdx.x & 31) == 0) a.ws_base[s] = first;
+      }
+    }
+    if (!batch_item(a, t, item, b, kvh, split, slot)) return;
+    L_raw = __ldg(a.ctx_lens + b);
   } else {
     if (!item_of(a, item, b, kvh, split)) return;
     L_raw = __ldg(a.ctx_lens + b);
@@ -523,11 +604,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   // the KV head's place in the pool
   const int pool_h = kLists ? b - (int)fdiv((unsigned)b, a.div_heads) * a.pool.n_kv : kvh;
   const Span span = kScores && !a.whole ? span_of(a, b, L_raw) : Span{0, 0};
-  const int c_begin = span.base + split * a.split_cells;
+  const int c_begin = span.base + split * split_cells;
   // until the length is known (one sequence), copies stay inside the split
   // and the block table
   int c_end = min(kScores && !a.whole ? span.end : clamp_len_mma(single ? INT_MAX : L_raw, a),
-                  c_begin + a.split_cells);
+                  c_begin + split_cells);
   int n_tiles = (c_end - c_begin + kTC - 1) / kTC;
   if ((kLists || kScores) && n_tiles < 0) n_tiles = 0;   // (an empty split of a cluster, or past a window)
   const int n_first = n_tiles < C::STAGES ? n_tiles : C::STAGES;   // tiles of the first wave
@@ -739,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   __syncthreads();
   const int L = context_of(a, L_raw);
   if (single) {
-    c_end = min(kScores && !a.whole ? span.end : L, c_begin + a.split_cells);
+    c_end = min(kScores && !a.whole ? span.end : L, c_begin + split_cells);
     n_tiles = c_end > c_begin ? (c_end - c_begin + kTC - 1) / kTC : 0;
     // (a cluster's empty splits go through the merge with nothing to add)
     if (n_tiles == 0 && !clustered) {
@@ -1520,7 +1601,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     }
   }
   // this CTA's rows of the split's partial
-  const size_t row0 = (((size_t)b * a.n_kv + kvh) * a.nsplit + split) * a.R + r0;
+  const size_t row0 = (kScores && a.batch_items > 0 ? (size_t)kvh * a.batch_items + slot
+                                                    : ((size_t)b * a.n_kv + kvh) * a.nsplit + split) * a.R + r0;
   if constexpr (C::V4) {
     // K8V4: the merged rows are in the rotated basis; one warp per row sums
     // the slabs, rotates the row back (Walsh-Hadamard, divided by HD) and
@@ -1617,11 +1699,15 @@ __global__ void __launch_bounds__(kCombineThreads, 4) combine_partials(DecodeArg
   // one sequence: every split slot is written (splits past the context say
   // "no cells"), so the context length need not be read
   int nlive = a.nsplit;
-  if (kLists || a.n_seq > 1) {
+  size_t base0 = ((size_t)b * a.n_kv + kvh) * a.nsplit;
+  if (kScores && a.batch_items > 0) {
+    const int first = __ldcg(a.ws_base + b);
+    nlive = __ldcg(a.ws_base + b + 1) - first;
+    base0 = (size_t)kvh * a.batch_items + first;
+  } else if (kLists || a.n_seq > 1) {
     const Span sp = span_of(a, b, __ldg(a.ctx_lens + b));
     nlive = (int)fdiv((unsigned)(sp.end - sp.base + a.split_cells - 1), a.div_split);
   }
-  const size_t base0 = ((size_t)b * a.n_kv + kvh) * a.nsplit;
 
   float M = kNegInf, lsum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1744,7 +1830,8 @@ cudaError_t launch_combine_dv(const DecodeArgs& a, cudaStream_t s) {
 // slot in one batch of loads; 4 columns (64 slices) when none does.
 template <int HD>
 cudaError_t launch_combine(const DecodeArgs& a, cudaStream_t s) {
-  const int need_js = (a.nsplit + kCombineBatch - 1) / kCombineBatch;
+  const int most = kScores && a.batch_items > 0 ? a.batch_items / a.n_seq + 1 : a.nsplit;   // (a batch's mean)
+  const int need_js = (most + kCombineBatch - 1) / kCombineBatch;
   constexpr int MAXDV = HD / 4 < 32 ? HD / 4 : 32;
   if (need_js <= kCombineThreads / 32 && MAXDV >= 32) return launch_combine_dv<HD, MAXDV>(a, s);
   if (need_js <= kCombineThreads / 16 && MAXDV >= 16) return launch_combine_dv<HD, 16>(a, s);
@@ -1814,7 +1901,8 @@ cudaError_t launch_impl(const DecodePlan& p, const DecodeArgs& a, cudaStream_t s
   for (int sp = 0; sp < C::VNCH; ++sp)
     if (!make_map(&maps.v[sp], a.pool.v, C::VSWB, C::VROWB, sp, rows, piece)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  const long long items = (long long)p.nsplit * a.n_kv * a.n_seq * a.n_rt;
+  const long long items =
+      kScores && a.batch_items > 0 ? (long long)a.batch_items * a.n_kv * a.n_rt : (long long)p.nsplit * a.n_kv * a.n_seq * a.n_rt;
   if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
   cfg.gridDim = dim3((unsigned)items);
   cfg.blockDim = dim3(kThreads);

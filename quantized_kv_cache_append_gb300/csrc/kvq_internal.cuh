@@ -129,6 +129,8 @@ struct DecodePlan {
   int nsplit;          // splits per (sequence, KV head), one partial each
   size_t off_o, off_ml, bytes;  // workspace layout
   int c_log2;          // block lists: see DecodeArgs
+  int batch_items;     // scored batches: splits per (KV head, row tile), 0: nsplit per sequence
+  size_t off_base;     // and their table in the workspace
 };
 
 // Division of a 32-bit x by a divisor d fixed per call: q = x / d is the
@@ -186,6 +188,11 @@ struct DecodeArgs {
   const int32_t* first;  // [n_seq] or null
   int window;          // 0: none
   int whole;           // no window and no first cells: split 0 begins at cell 0
+  // Batches (kvq_batch_splits.h): the split length is found on the device, the
+  // splits of all sequences are numbered through; ws_o and ws_ml are
+  // [n_kv][batch_items][R].  0: nsplit slots a sequence.
+  int batch_items;
+  int* ws_base;        // [n_seq + 1]: each sequence's first split
 };
 
 struct CompactArgs {

@@ -223,6 +223,26 @@ def test_long_max_ctx_short_sequences():
     c.check(first=[5, 8000, 0, 600])
 
 
+@pytest.mark.parametrize("n_seq,hi,n_kv,G,W,fmt", [
+    (2, 9000, 1, 1, 1, "f16"), (7, 3000, 2, 2, 2, "q8"), (31, 500, 1, 4, 1, "k8v4"), (33, 700, 1, 1, 1, "f16"),
+    (100, 300, 2, 1, 1, "q8"), (128, 200, 1, 2, 1, "f16"), (129, 200, 1, 2, 1, "f16"), (90, 150, 7, 1, 1, "f16"),
+    (300, 70, 1, 1, 1, "q8"),
+])
+def test_ragged_batches(n_seq, hi, n_kv, G, W, fmt):
+    # lengths of one cell to hi, some empty, one many times the others'
+    rng = np.random.default_rng(n_seq)
+    lens = np.exp(rng.uniform(0, np.log(hi), n_seq)).astype(int)
+    lens[rng.random(n_seq) < 0.1] = 0
+    lens[n_seq // 2] = hi
+    c = Case(rng, fmt, n_kv, G, 64, W, 16, lens, max_ctx=hi + 40)
+    c.check(cap=20.0)
+    c.check(window=90, first=rng.integers(0, np.maximum(lens, 1)))
+    lens[:] = 0
+    c.lens = lens
+    got, _ = c.check(cap=20.0)
+    assert not got.any()
+
+
 def test_streams_and_two_graphs():
     rng = np.random.default_rng(9)
     c = Case(rng, "q8", 2, 4, 128, 1, 64, [3000, 700])
