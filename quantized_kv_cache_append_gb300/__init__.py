@@ -427,10 +427,10 @@ def make_rotary(type: int, rot_dim: int, interleaved: bool, inv_freq, pair_axis=
 def kvq_append_rotary(cache: kvq_cache, rotary: kvq_rotary, q, k, v, q_stride: int, k_stride: int,
                       v_stride: int, n_tok: int, n_q: int, tok_seq, tok_pos, positions, block_table,
                       n_seq: int, max_blocks_per_seq: int, q_out, stream=None) -> int:
+    a = _ptrs(q, k, v, tok_seq, tok_pos, block_table, q_out)
     return load_library().kvq_append_rotary(
-        ctypes.byref(cache), ctypes.byref(rotary), _ptr(q), _ptr(k), _ptr(v), q_stride, k_stride, v_stride,
-        n_tok, n_q, _ptr(tok_seq), _ptr(tok_pos), _ptr(positions), _ptr(block_table), n_seq,
-        max_blocks_per_seq, _ptr(q_out), _stream(stream))
+        ctypes.byref(cache), ctypes.byref(rotary), a[0], a[1], a[2], q_stride, k_stride, v_stride, n_tok, n_q,
+        a[3], a[4], _ptr(positions), a[5], n_seq, max_blocks_per_seq, a[6], _stream(stream))
 
 
 def make_scores(softcap: float = 0.0, window: int = 0, slopes=None, first=None, last=None) -> kvq_scores:
@@ -485,10 +485,10 @@ def kvq_chunk_attn_scored_lost_wait_test(k16, v16, n_kv_heads: int, P: int, head
 def kvq_verify_draft(target, draft, type: int, target_stride: int, draft_stride: int, n_seq: int, W: int,
                      vocab: int, draft_tokens, n_draft, u, u_sample, n_accepted, tokens, n_dropped=None,
                      stream=None) -> int:
-    a = _ptrs(target, u_sample, n_accepted, tokens)
+    a = _ptrs(target, draft_tokens, u, u_sample, n_accepted, tokens)
     return load_library().kvq_verify_draft(a[0], _ptr(draft), type, target_stride, draft_stride, n_seq, W,
-                                           vocab, _ptr(draft_tokens), _ptr(n_draft), _ptr(u), a[1], a[2],
-                                           a[3], _ptr(n_dropped), _stream(stream))
+                                           vocab, a[1], _ptr(n_draft), *a[2:], _ptr(n_dropped),
+                                           _stream(stream))
 
 
 def kvq_trim_step(ctx_in, n_drop, n_seq: int, block_size: int, n_blocks: int, block_table,
