@@ -1174,24 +1174,26 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
                            (kScores && row_lo_max > cw0);
     if constexpr (kScores) {
       if (a.cap2 != 0.f) {
-        bool wide = false;
+        float most = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            z[nt][k] *= a.cap2_inv;
-            wide |= fabsf(z[nt][k]) > kTanhSmall;
-          }
-        if (__any_sync(kFull, wide)) {
+          for (int k = 0; k < 4; k += 2) most = max3f(most, fabsf(z[nt][k]), fabsf(z[nt][k + 1]));
+        if (__any_sync(kFull, most > kTanhSmall * a.cap2)) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) z[nt][k] = a.cap2 * tanh_any(z[nt][k]);
+            for (int k = 0; k < 4; k += 2) {
+              float s0 = z[nt][k], s1 = z[nt][k + 1];
+              cap_small(s0, s1, a.cap2_inv);
+              z[nt][k] = cap_any(z[nt][k], s0, a.cap2, a.cap2_inv);
+              z[nt][k + 1] = cap_any(z[nt][k + 1], s1, a.cap2, a.cap2_inv);
+            }
         } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) z[nt][k] = a.cap2 * tanh_small(z[nt][k]);
+            for (int k = 0; k < 4; k += 2) cap_small(z[nt][k], z[nt][k + 1], a.cap2_inv);
         }
       }
       if (a.slopes != nullptr) {
