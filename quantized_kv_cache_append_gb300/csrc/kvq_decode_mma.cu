@@ -630,6 +630,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   // load on that path.
   const int n_entries = n_tiles * n_pieces;
   const bool blk_in_smem = n_entries <= C::ROWS_CAP;
+  // Scored, with a distance bias: the newest tiles first, whose scores set the
+  // maximum (the other way round every tile would raise it).  A split whose length
+  // is not known when its first copies go out starts at its beginning.
+  const bool newest_first = kScores && a.slopes != nullptr && (!single || !a.whole);
+  auto tile_of = [&](int it) -> int { return newest_first ? n_tiles - 1 - it : it; };
   auto piece_blk = [&](int it, int p, bool from_smem) -> int {
     return from_smem ? s_blk[it * n_pieces + p]
                      : block_of(a, bt, c_begin + it * kTC + (p << pc_log2), c_end);
@@ -691,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     int row = -1;
     uint32_t bytes = 0;
     if (p < n_pieces) {
-      const int blk = piece_blk(it, p, from_smem), cell = c_begin + it * kTC + (p << pc_log2);
+      const int blk = piece_blk(tile_of(it), p, from_smem), cell = c_begin + tile_of(it) * kTC + (p << pc_log2);
       if (blk >= 0 && blk < a.pool.n_blocks) {
         row = (blk * a.pool.n_kv + pool_h) * bsz + (cell & (bsz - 1));
         bytes = (uint32_t)pc * (c < C::NCH ? C::SWB : c < C::NCH + C::VNCH ? C::VSWB
@@ -941,11 +946,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   const int cl = warp * kCellsPerWarp;  // first cell of this warp's slice in a stage
   auto slice_blk = [&](int it) -> int {
     if (it >= n_tiles) return -1;
-    if (blk_in_smem) return c_begin + it * kTC + cl < c_end ? s_blk[it * n_pieces + (cl >> pc_log2)] : -1;
-    return block_of(a, bt, c_begin + it * kTC + cl, c_end);
+    const int t = tile_of(it);
+    if (blk_in_smem) return c_begin + t * kTC + cl < c_end ? s_blk[t * n_pieces + (cl >> pc_log2)] : -1;
+    return block_of(a, bt, c_begin + t * kTC + cl, c_end);
   };
   auto slice_nvalid = [&](int it, int blk) -> int {
-    return (blk >= 0 && blk < a.pool.n_blocks) ? min(kCellsPerWarp, c_end - (c_begin + it * kTC + cl)) : 0;
+    return (blk >= 0 && blk < a.pool.n_blocks) ? min(kCellsPerWarp, c_end - (c_begin + tile_of(it) * kTC + cl)) : 0;
   };
 
   // Swizzled shared-memory addresses.  With a 128-byte swizzle the XOR term
@@ -1497,7 +1503,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
       load_scales(0, vw);
       float z[NT][4];
       qk(0, z);
-      softmax(nv_cur, c_begin + cl, vw, z, p_cur);
+      softmax(nv_cur, c_begin + tile_of(0) * kTC + cl, vw, z, p_cur);
     }
   }
   int it = 0;
@@ -1513,15 +1519,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     load_scales(sn, vn);
     float zn[NT][4];
     qk(sn, zn);
-    pv(it % C::STAGES, nv_cur, lo_all - (c_begin + it * kTC + cl), p_cur, vw);
+    pv(it % C::STAGES, nv_cur, lo_all - (c_begin + tile_of(it) * kTC + cl), p_cur, vw);
     release(it);
-    softmax(nv_next, c_begin + (it + 1) * kTC + cl, vn, zn, p_cur);
+    softmax(nv_next, c_begin + tile_of(it + 1) * kTC + cl, vn, zn, p_cur);
     nv_cur = nv_next;
 #pragma unroll
     for (int i = 0; i < 2 * VSW; ++i) vw[i / VSW][i % VSW] = vn[i / VSW][i % VSW];
   }
   if (!lost && n_tiles > 0) {  // the last tile
-    pv(it % C::STAGES, nv_cur, lo_all - (c_begin + it * kTC + cl), p_cur, vw);
+    pv(it % C::STAGES, nv_cur, lo_all - (c_begin + tile_of(it) * kTC + cl), p_cur, vw);
     release(it);
   }
   if (producer) {
