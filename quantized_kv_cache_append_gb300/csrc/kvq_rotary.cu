@@ -116,11 +116,11 @@ __device__ __forceinline__ void turn(int pos, float f, float& c, float& s) {
 }
 
 // 28 warps an SM and 2 blocks of queries in flight a warp: 4096 bf16 tokens of
-// 32 + 2 x 8 heads of 128 dims 28.1 us (4.5 TB/s; 16384 tokens 5.0 TB/s), 16381
+// 32 + 2 x 8 heads of 128 dims 25.6 us (4.9 TB/s; 16384 tokens 5.6 TB/s), 16381
 // fp32 tokens of 16 + 2 x 2 heads of 256 dims with 3 axes 95 us (97 % of the copy
-// rate).  CTAs of 1 warp 33 and 106 us, of 4 warps 32 and 109; 4 blocks and 20 warps
-// 28.4 and 101.  A first form with 12 blocks a warp, each warp taking its own
-// sines, ran 235 instructions a block and 29.3 and 106 us.
+// rate).  CTAs of 1 warp 33 and 106 us, of 4 warps 32 and 109; 20 warps an SM 28.5
+// and 100, 32 27.5 and 110.  A first form with 12 blocks a warp, each warp taking
+// its own sines, ran 235 instructions a block and 29.3 and 106 us.
 template <int FMT, int HD, int T>
 __global__ void __launch_bounds__(kRotWarps * 32, 14) append_rotary_kernel(const __grid_constant__ RotaryArgs a) {
   constexpr int LPR = HD / VPL;   // lanes of a head
@@ -229,6 +229,16 @@ __global__ void __launch_bounds__(kRotWarps * 32, 14) append_rotary_kernel(const
       }
     }
     while (true) {
+      // 16-bit types: the next blocks are on the way while these are worked on (4096
+      // bf16 tokens 28.4 -> 25.6 us; fp32 has no registers for it, 34 -> 42)
+      constexpr bool kAhead = T != KVQ_T_F32;
+      Raw<T> next[U];
+      auto fetch = [&](int b1) {
+        const E* p = at(rows, stride, b1);
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u] = load8<T>(p, u * step * HD, b1 * RPW + sub + u * step < n);
+      };
+      if constexpr (kAhead) fetch(b + U * n_parts);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (b * RPW >= n) break;   // warp-uniform
@@ -273,9 +283,9 @@ __global__ void __launch_bounds__(kRotWarps * 32, 14) append_rotary_kernel(const
         b += n_parts;
       }
       if (b * RPW >= n) return;
-      const E* p = at(rows, stride, b);
+      if constexpr (!kAhead) fetch(b);
 #pragma unroll
-      for (int u = 0; u < U; ++u) r[u] = load8<T>(p, u * step * HD, b * RPW + sub + u * step < n);
+      for (int u = 0; u < U; ++u) r[u] = next[u];
     }
   };
 
