@@ -26,7 +26,9 @@ namespace kvq {
 namespace {
 
 constexpr int kRotWarps = 2;
-constexpr int kRotCtas = 16;   // CTAs an SM that few tokens are spread over
+// CTAs an SM that few tokens are spread over, half of what is resident: 512 tokens
+// of 32/8 heads 5.25 us, 256 4.0 (4: 6.9 and 4.5, 14: 6.1 and 5.2, 20: 7.7 and 5.9).
+constexpr int kRotCtas = 7;
 constexpr int VPL = 8;
 
 template <int T>
@@ -331,7 +333,7 @@ cudaError_t launch(RotaryArgs a, int sms, cudaStream_t s) {
   // one CTA a token, or for few tokens as many as fill the SMs, down to one head
   // block a warp
   const int most = (nb + kRotWarps - 1) / kRotWarps;
-  const long long want = ((long long)sms * kRotCtas + a.n_tok - 1) / a.n_tok;
+  const long long fill = (long long)sms * kRotCtas / a.n_tok, want = fill > 1 ? fill : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.n_tok, (unsigned)(want < most ? want : most));
   const int n_parts = (int)cfg.gridDim.y * kRotWarps, qb = (a.n_q + RPW - 1) / RPW, kb = (a.pool.n_kv + RPW - 1) / RPW;
