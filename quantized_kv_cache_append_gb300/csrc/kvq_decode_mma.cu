@@ -148,7 +148,8 @@ struct Cfg {
   static constexpr int SMEM_BAR = SMEM_WML + kConsumerWarps * NT * 8 * 2 * 4;
   // block ids of the split's pieces, staged once so any warp can issue a refill
   static constexpr int ROWS_CAP = 128;
-  static constexpr int SMEM_REL = SMEM_BAR + STAGES * 8;        // release counters [STAGES]
+  // (scored: room for a barrier for each warp's slice of each stage)
+  static constexpr int SMEM_REL = SMEM_BAR + STAGES * 8 * (kScores ? kConsumerWarps : 1);  // release counters [STAGES]
   static constexpr int SMEM_BLK = SMEM_REL + 16 * 4;            // block ids [ROWS_CAP]
   static constexpr int SMEM = SMEM_BLK + ROWS_CAP * 4 + 1024 /*align*/;
   static constexpr int FIT = (228 * 1024) / (SMEM + 1024);  // 1 KB reserved per CTA
@@ -489,6 +490,25 @@ __device__ __forceinline__ void merge_cluster(const DecodeArgs& a, unsigned char
 // ---------------------------------------------------------------------------
 // The kernel
 // ---------------------------------------------------------------------------
+// Who fetches a stage of the scored kernel.  With few rows of short heads the
+// four warps keep step, and the last to let a stage go refills all of it in
+// pieces of up to 64 cells.  Where a warp has more to do for a tile (more than 4
+// query rows, or heads of 256) the warps drift apart, and each refills its own
+// slice of 16 cells as soon as it has read it, at four times the copies.
+// Sixteen ragged sequences, device us, shared stages against own slices:
+//   4 rows, head_dim 128, blocks of 64:  q8 76.1, 78.6; f16 99, 107; k8v4 77, 84
+//                         blocks of 16:  q8 86.2, 79.9; f16 114, 109; k8v4 87, 85
+//                         (one choice for all block sizes; the larger ones decide)
+//   8 rows, head_dim 128, blocks of 64:  48.0, 48.0; 55.6, 55.6; 48.7, 50.0
+//                         blocks of 16:  51.8, 47.9; 66.5, 57.0; 53.8, 50.3
+//   16 rows, head_dim 128, blocks of 64: 143, 141; 134, 130; 151, 149
+//                         blocks of 16:  154, 140; 158, 133; 161, 149
+// Two sequences of 65536 to 131072 cells, head_dim 256, blocks of 64:
+//   32 rows:  117, 104; 181, 139; 124, 113       8 rows:  44.7, 41.8; 55, 53; 45.6, 42
+//   (blocks of 16: 145, 112; 239, 155; 151, 122           53.7, 43.5; 84, 58; 52, 45)
+template <int HD, bool HL>
+constexpr bool kWarpSlices = kScores && (HD == 256 || !HL);
+
 // HL (at most 4 query rows, NT = 1): the MMA's 8 columns carry the hi
 // parts of q (and of p) in columns 0-3 and the lo parts in columns 4-7, so
 // each k-step of q.k and each m-tile of p.v takes one MMA instead of two;
@@ -499,6 +519,7 @@ template <int FMT, int HD, int NT, bool HL>
 __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     decode_mma(const __grid_constant__ TmaMaps maps, DecodeArgs a) {
   static_assert(!HL || NT == 1, "hi/lo columns need a single 8-column row tile");
+  constexpr bool kSlices = kWarpSlices<HD, HL>;
   using C = Cfg<FMT, HD, NT>;
   constexpr int KS = HD / 16;   // k-steps of q.k, and m-tiles of p.v
   constexpr int RP = NT * 8;    // padded rows
@@ -723,6 +744,39 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     __syncwarp();
   };
 
+  // kSlices: each warp fetches its own slice of 16 cells of every stage, a copy a
+  // lane, behind a barrier of its own.
+  const uint32_t bar_own = kSlices ? bar_full + 8 * C::STAGES * warp : bar_full;
+  auto issue_slice = [&](int it, bool from_smem) {
+    constexpr int NC = C::NCH + C::VNCH + (C::KI8 ? 2 : 0);   // copies of a slice
+    const int s = it % C::STAGES, t = tile_of(it);
+    const int bsz = 1 << a.pool.bs_log2, at = warp * kCellsPerWarp;   // the slice in its tile
+    const int cell = c_begin + t * kTC + at;
+    // (the staged table has an entry a piece of up to 64 cells)
+    const int blk = from_smem ? (cell < c_end ? s_blk[t * n_pieces + (at >> pc_log2)] : -1) : block_of(a, bt, cell, c_end);
+    const bool there = blk >= 0 && blk < a.pool.n_blocks;
+    const uint32_t full = bar_own + 8 * s;
+    if (lane == 0)
+      mbar_expect_tx(full, (there ? kCellsPerWarp * (C::ROWB + C::VROWB + (C::KI8 ? (C::NG + C::VNS) * 2 : 0)) : 0) + a.extra_tx);
+    __syncwarp();
+    if (there && lane < NC) {
+      const int row = (blk * a.pool.n_kv + pool_h) * bsz + (cell & (bsz - 1)), c = lane;
+      const uint32_t st = sbase + s * C::STAGE_B;
+      if (c < C::NCH) {
+        tma_load_2d_hint(st + (uint32_t)(c * kTC + at) * C::SWB, &maps.k[c], 0, row, full, pol);
+      } else if (c < C::NCH + C::VNCH) {
+        const int sp = c - C::NCH;
+        tma_load_2d_hint(st + C::OFF_V + (uint32_t)(sp * kTC + at) * C::VSWB, &maps.v[sp], 0, row, full, pol);
+      } else if constexpr (C::KI8) {
+        constexpr uint32_t KB = kCellsPerWarp * C::NG * 2, VB = kCellsPerWarp * C::VNS * 2;
+        const uint32_t sc = sbase + C::SMEM_SC + (uint32_t)s * C::SC_STAGE_B;
+        if (c == NC - 2) bulk_load_hint(sc + (uint32_t)warp * KB, a.pool.ks + (size_t)row * C::NG, KB, full, pol);
+        else bulk_load_hint(sc + C::KSCALE_B + (uint32_t)warp * VB, a.pool.vs + (size_t)row * C::VNS, VB, full, pol);
+      }
+    }
+    __syncwarp();
+  };
+
   // Prologue.  Every small load (q, the split's block ids) is issued first,
   // into registers; only then does thread 0 start the first stages' bulk
   // copies.  Issued the other way round, these few latency-critical loads
@@ -763,7 +817,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
                 : -1;
   }
   bool lost = false;
-  if constexpr (kScores) {
+  if constexpr (kSlices) {
+    if (lane == 0) {
+      for (int s = 0; s < C::STAGES; ++s) mbar_init(bar_own + 8 * s, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    if (n_first > 0) issue_slice(0, false);
+  } else if constexpr (kScores) {
     if (warp == 0) {
       if (lane == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
@@ -830,14 +891,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     // (a cluster's empty splits go through the merge with nothing to add)
     if (n_tiles == 0 && !clustered) {
       // a split past the context: its slots tell the combine "no cells"
-      if (producer && n_first > 0) (void)mbar_wait(bar_full, 0, a.wait_limit);
+      if ((kSlices ? lane == 0 : producer) && n_first > 0) (void)mbar_wait(bar_own, 0, a.wait_limit);
       const size_t slot0 = (((size_t)b * a.n_kv + kvh) * a.nsplit + split) * a.R;
       if (threadIdx.x < a.R)
         *reinterpret_cast<float2*>(a.ws_ml + (slot0 + threadIdx.x) * 2) = make_float2(-INFINITY, 0.f);
       return;
     }
   }
-  if (kScores && warp == 0) {
+  if constexpr (kSlices) {
+    for (int it = 1; it < n_first; ++it) issue_slice(it, blk_in_smem);
+  } else if (kScores && warp == 0) {
     for (int it = 1; it < n_first; ++it) issue_warp(it, blk_in_smem);
   }
   if (!kScores && producer) {
@@ -1445,6 +1508,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   auto release = [&](int it) {
     // the last warp to let the stage go issues its refill
     __syncwarp();
+    if constexpr (kSlices) {   // (its own slice: every lane's reads are done)
+      if (it + C::STAGES < n_tiles) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        issue_slice(it + C::STAGES, blk_in_smem);
+      }
+      return;
+    }
     if constexpr (kScores) {
       const int s = it % C::STAGES;
       int prev = 0;
@@ -1495,7 +1565,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   float p_cur[NT][4];
   uint32_t vw[2][VSW];   // V scales of the tile whose p.v comes next
   if (n_tiles > 0) {
-    if (!mbar_wait(bar_full, 0, a.wait_limit)) {
+    if (!mbar_wait(bar_own, 0, a.wait_limit)) {
       lost = true;
     } else {
       nv_cur = slice_nvalid(0, blk_n);
@@ -1509,7 +1579,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
   int it = 0;
   for (; it + 1 < n_tiles && !lost; ++it) {
     const int sn = (it + 1) % C::STAGES;
-    if (!mbar_wait(bar_full + 8 * sn, ((it + 1) / C::STAGES) & 1, a.wait_limit)) {
+    if (!mbar_wait(bar_own + 8 * sn, ((it + 1) / C::STAGES) & 1, a.wait_limit)) {
       lost = true;
       break;
     }
@@ -1530,12 +1600,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, HD, NT>::MIN_CTAS)
     pv(it % C::STAGES, nv_cur, lo_all - (c_begin + tile_of(it) * kTC + cl), p_cur, vw);
     release(it);
   }
-  if (producer) {
-    // Every copy this CTA issued has landed before the CTA can exit (waits
-    // return at once in normal runs; they are bounded after a lost wait).
+  if (kSlices ? lane == 0 : producer) {
+    // Every copy this CTA issued (kSlices: this warp) has landed before the CTA
+    // can exit (waits return at once in normal runs; they are bounded after a
+    // lost wait).
     const int n_all = n_tiles > n_first ? n_tiles : n_first;
     for (int it = n_all > C::STAGES ? n_all - C::STAGES : 0; it < n_all; ++it)
-      (void)mbar_wait(bar_full + 8 * (it % C::STAGES), (it / C::STAGES) & 1, a.wait_limit);
+      (void)mbar_wait(bar_own + 8 * (it % C::STAGES), (it / C::STAGES) & 1, a.wait_limit);
   }
 
   // ---------------- merge the 4 warps, write the split's partial ----------------
@@ -1901,7 +1972,7 @@ cudaError_t launch_impl(const DecodePlan& p, const DecodeArgs& a, cudaStream_t s
   using C = Cfg<FMT, HD, NT>;
   if (ctas_per_sm_impl<FMT, HD, NT, HL>() <= 0) return cudaErrorInvalidConfiguration;
   const long long rows = (long long)a.pool.n_blocks * a.pool.n_kv << a.pool.bs_log2;
-  const int piece = 1 << (a.pool.bs_log2 < 6 ? a.pool.bs_log2 : 6);
+  const int piece = kWarpSlices<HD, HL> ? kCellsPerWarp : 1 << (a.pool.bs_log2 < 6 ? a.pool.bs_log2 : 6);
   TmaMaps maps;
   memset(&maps, 0, sizeof(maps));
   for (int sp = 0; sp < C::NCH; ++sp)
