@@ -690,8 +690,9 @@ typedef struct kvq_rotary {
  *   q_out      device fp32 [n_tok][n_q][head_dim], 16-byte aligned, not
  *              overlapping an input
  *
- * A token whose tok_seq is outside [0, n_seq) or whose tok_pos is negative
- * (padding) is skipped: its row of q_out stays as it was, nothing is
+ * Two tokens of one call must not name the same cell.  A token whose tok_seq
+ * is outside [0, n_seq) or whose tok_pos is negative (padding) is skipped: its
+ * row of q_out stays as it was, nothing is
  * appended.  Where only its block is out of range its q is written still.
  * Sums, angles and rotation are fp32 or better: an angle of up to 2^22
  * radians is reduced to within 2^-22 before its sine and cosine are taken, a

@@ -252,6 +252,9 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const __grid_con
     }
     return;
   }
+  // (waited for before the first store into a peer's shared memory: all of the
+  // cluster's CTAs run by then)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   // how many drafts stand
   if (warp == 0) {
     bool ok = false;
@@ -293,6 +296,7 @@ __global__ void __launch_bounds__(kVerThreads, 4) verify_kernel(const __grid_con
       if (lane == 0) s_tile[t] = total_of(c, kTile<E>);
     }
     __syncthreads();
+    if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 0) {
       unsigned long long v = 0;
       for (int t = lane; t < n_mine; t += 32) v += s_tile[t];
