@@ -396,6 +396,83 @@ __device__ __forceinline__ void store8(const ChunkArgs& a, size_t i, const float
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_any) + i) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// The merge of a cluster's key splits, scored.  Each CTA owns a share of the
+// columns: it gets their O of every split, and every row's (m, l), by remote
+// stores, which nobody waits for one by one, weighs and sums the slabs in the
+// splits' order and writes.  (Read from the peers, as the plain kernel does it,
+// split by split, 5 splits took 7.2 us of a CTA's 12.7 at head_dim 64, now about 3.)
+// The stages are free: no peer stores before the first barrier, which each CTA
+// passes with its copies and MMAs complete; nothing remote is touched behind the
+// second.
+template <int HD>
+__device__ __noinline__ void merge_pushed(unsigned char* smem, uint32_t sbase, uint32_t o_col, int n_split, bool soft,
+                                          bool valid, bool any, int row, int oc0, float m, float l,
+                                          const ChunkArgs& a, size_t orow) {
+  using namespace tcc;
+  using Lay = TcLayout<HD>;
+  constexpr int NCH = HD / 4;               // 16-byte chunks of a row
+  const int z0 = (int)blockIdx.z, half = (int)threadIdx.x >> 7;
+  const int most = (NCH + n_split - 1) / n_split;   // chunks a CTA owns at most
+  // slabs [split][chunk][row] from the start, (m, l) [split][row] at the end
+  constexpr int OFF_ML = Lay::OFF_BAR - kMaxKeySplits * BM * 8;
+  static_assert((NCH + kMaxKeySplits) * BM * 16 <= OFF_ML, "slabs and (m, l) fit");
+  cluster_sync_all();
+  if (soft) {
+    if (half == 0)   // (a lost wait: NaN through l)
+      for (int z = 0; z < n_split; ++z) st_dsmem_v2(sbase + OFF_ML + (z0 * BM + row) * 8, z, make_float2(m, l));
+#pragma unroll
+    for (int c1 = 0; c1 < HD / 2; c1 += 32) {
+      uint32_t ov[32];
+      if (any) {
+        tmem_ld32(o_col + oc0 + c1, ov);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) ov[e] = 0;
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const int ch = (oc0 + c1 + e) >> 2, z = ((ch + 1) * n_split - 1) / NCH;   // its owner
+        st_dsmem_v4(sbase + (uint32_t)(((z0 * most + ch - z * NCH / n_split) * BM + row) * 16), z,
+                    make_float4(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1]), __uint_as_float(ov[e + 2]),
+                                __uint_as_float(ov[e + 3])));
+      }
+    }
+  }
+  cluster_sync_all();
+  if (soft && valid) {
+    const float2* s_ml = reinterpret_cast<const float2*>(smem + OFF_ML) + row;
+    float w[kMaxKeySplits], M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int z = 0; z < kMaxKeySplits; ++z)
+      if (z < n_split) M = fmaxf(M, s_ml[z * BM].x);
+#pragma unroll
+    for (int z = 0; z < kMaxKeySplits; ++z) {
+      if (z < n_split) {
+        const float2 ml = s_ml[z * BM];
+        w[z] = fast_exp2(ml.x - M);
+        L += ml.y * w[z];
+      }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;   // (a row that sees no key: 0)
+    const int ch_b = z0 * NCH / n_split, ch_e = (z0 + 1) * NCH / n_split;
+    for (int ch = ch_b + half; ch < ch_e; ch += 2) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int z = 0; z < kMaxKeySplits; ++z) {
+        if (z < n_split) {
+          const float4 v = *reinterpret_cast<const float4*>(smem + ((z * most + ch - ch_b) * BM + row) * 16);
+          acc.x = fmaf(w[z], v.x, acc.x);
+          acc.y = fmaf(w[z], v.y, acc.y);
+          acc.z = fmaf(w[z], v.z, acc.z);
+          acc.w = fmaf(w[z], v.w, acc.w);
+        }
+      }
+      store4(a, orow + 4 * ch, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+  }
+}
+
 // LW: the lost-wait test's instantiation, whose waits take their poll limit
 // from the call and whose stages expect a.extra_tx bytes more than any copy
 // delivers; the ordinary one keeps the constant limit in its hot loops.
@@ -427,6 +504,35 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   const int row_tile = ascending ? (int)blockIdx.x / a.n_kv : kScores ? (int)blockIdx.x % n_row_tiles : (int)blockIdx.x;
   const int kvh = ascending ? (int)blockIdx.x - row_tile * a.n_kv
                   : kScores ? (int)blockIdx.x / n_row_tiles : (int)blockIdx.y;
+  auto set_up = [&]() {   // the barriers and the tensor memory
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(KFULL + i), 1);
+        mbar_init(bar(KEMPTY + i), 1);
+        mbar_init(bar(VFULL + i), 1);
+        mbar_init(bar(VEMPTY + i), 1);
+      }
+      for (int i = 0; i < 3; ++i) {
+        mbar_init(bar(SFULL + i), 1);
+        mbar_init(bar(PFULL + i), kSoftWarps * 32);
+        mbar_init(bar(SFREE + i), 1);
+      }
+      mbar_init(bar(ALLDONE), 1);
+      mbar_init(bar(SDRAIN), 1);
+      mbar_init(bar(PDRAIN), 1);
+      mbar_init(bar(QREADY), kSoftWarps * 32);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc(sbase + OFF_TSLOT, TMEM_COLS);
+  };
+  if constexpr (kScores) {
+    // A programmatic dependent of the previous kernel, nothing of which is read
+    // before this wait.  (Its own dependents follow as its CTAs end: let in
+    // earlier, a next chunk's clusters in SMs that were free made a chunk of 257
+    // tokens in 28 clusters of 5 take 15 us instead of 10.8; 11.2 without either.)
+    set_up();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
   const uint32_t wl = LW ? a.wait_limit : kDefaultWaitLimit;   // polls before a wait is lost
   const uint32_t extra_tx = LW ? a.extra_tx : 0u;
   // row tiles in descending order: the last ones (later tokens) see the
@@ -477,25 +583,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   const int j0 = tile0 + min(n_all, (int)blockIdx.z * per);     // this CTA's first key tile
   const int n_tiles = min(tile0 + n_all, j0 + per) - j0;         // and its count (0 possible)
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(KFULL + i), 1);
-      mbar_init(bar(KEMPTY + i), 1);
-      mbar_init(bar(VFULL + i), 1);
-      mbar_init(bar(VEMPTY + i), 1);
-    }
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(bar(SFULL + i), 1);
-      mbar_init(bar(PFULL + i), kSoftWarps * 32);
-      mbar_init(bar(SFREE + i), 1);
-    }
-    mbar_init(bar(ALLDONE), 1);
-    mbar_init(bar(SDRAIN), 1);
-    mbar_init(bar(PDRAIN), 1);
-    mbar_init(bar(QREADY), kSoftWarps * 32);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == kMmaWarp) tmem_alloc(sbase + OFF_TSLOT, TMEM_COLS);
+  if constexpr (!kScores) set_up();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -758,6 +846,8 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         }
       }
     }
+  } else if constexpr (kScores) {
+    merge_pushed<HD>(smem, sbase, tmem + lane_base + COL_O, n_split, soft, valid, n_tiles > 0, row, oc0, m, l, a, orow);
   } else {
     // Merge of the cluster's key splits through distributed shared memory
     // (the q and K stage areas are free now): (m, l) of every row first,
@@ -769,7 +859,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
     auto o_chunk = [&](int r, int ch) -> uint32_t {          // byte offset of chunk ch of row r
       return (uint32_t)(r * HD * 4) + ((uint32_t)(ch ^ (r & 7)) << 4);
     };
-    if (soft && (!kScores || warp < 4)) s_ml[row] = make_float2(m, lost ? nan : l);   // a lost wait: NaN through L
+    if (soft) s_ml[row] = make_float2(m, lost ? nan : l);   // a lost wait: NaN through L
     cluster_sync_all();
     if (soft) {
       float M = -INFINITY;
@@ -779,12 +869,9 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         const float mz = ld_dsmem_f32(smem_u32(&s_ml[row].x), z), lz = ld_dsmem_f32(smem_u32(&s_ml[row].y), z);
         L += lz * fast_exp2(mz - M);
       }
-      // this split's weight (rows that see no key: 0; unscored chunks have none)
-      const bool none = kScores && L == 0.f;
-      const float c = none ? 0.f : fast_exp2(m - M) / L;
+      const float c = fast_exp2(m - M) / L;   // this split's weight (rows that see no key: unused)
 #pragma unroll
-      for (int c1 = 0; c1 < OC; c1 += 32) {
-        const int c0 = oc0 + c1;
+      for (int c0 = 0; c0 < HD; c0 += 32) {
         uint32_t ov[32];
         if (n_tiles > 0) {
           tmem_ld32(tmem + lane_base + COL_O + c0, ov);
@@ -792,7 +879,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 r4 = n_tiles > 0 && !none
+          const float4 r4 = n_tiles > 0
               ? make_float4(__uint_as_float(ov[e]) * c, __uint_as_float(ov[e + 1]) * c,
                             __uint_as_float(ov[e + 2]) * c, __uint_as_float(ov[e + 3]) * c)
               : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -806,7 +893,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
       constexpr int NCH = HD / 4;
       const int z0 = (int)blockIdx.z;
       const int ch_b = z0 * NCH / n_split, ch_e = (z0 + 1) * NCH / n_split;
-      for (int ch = ch_b + (kScores ? warp >> 2 : 0); ch < ch_e; ch += kScores ? 2 : 1) {
+      for (int ch = ch_b; ch < ch_e; ++ch) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int z = 0; z < n_split; ++z) {
           const float4 v4 = ld_dsmem_v4(s_o + o_chunk(row, ch), z);
@@ -925,11 +1012,16 @@ cudaError_t launch_tc_kernel(const ChunkArgs& a, cudaStream_t s) {
     n_all = (int)min((long long)n_all, cells / Lay::BN + 2);
   }
   const int n_split = tc_key_splits<HD, LW>(row_tiles * a.n_kv, n_all);
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg =
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg =
       tc_config<HD>(kScores ? dim3((unsigned)(row_tiles * a.n_kv), 1, (unsigned)n_split)
                             : dim3((unsigned)row_tiles, (unsigned)a.n_kv, (unsigned)n_split),
                     n_split, s, attr);
+  if (kScores) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   return cudaLaunchKernelEx(&cfg, chunk_attn_tc<HD, LW>, maps, a);
 }
 

@@ -180,6 +180,19 @@ static __device__ __forceinline__ float ld_dsmem_f32(uint32_t smem_addr, int ran
   return v;
 }
 
+static __device__ __forceinline__ void st_dsmem_v2(uint32_t smem_addr, int rank, float2 v) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
+}
+
+static __device__ __forceinline__ void st_dsmem_v4(uint32_t smem_addr, int rank, float4 v) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr), "r"(rank));
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
 static __device__ __forceinline__ float4 ld_dsmem_v4(uint32_t smem_addr, int rank) {
   uint32_t remote;
   float4 v;
