@@ -203,15 +203,45 @@ __device__ __forceinline__ void pair_sync(int warp) {
 }
 
 struct Key {
-  int j0, n_tiles, P0, r0;   // the CTA's first key tile, its tiles, the cells before the chunk, its first row
+  int j0, n_tiles, P0;   // the CTA's first key tile, its tiles, the cells before the chunk
 };
+
+// A softmax thread's share of the CTA's q, 8 dims a step, neighbours of a row by
+// neighbouring lanes (row by row a thread, as the plain kernel does it, these loads
+// took 3.9 us of a CTA).  At head_dim 128 they go out before anything else is
+// known (4096 tokens with a window of 1024, heads of 128: 120.6 -> 116.4 us); 256
+// has no registers for it (2048 tokens 65.8 -> 68.3), 64 gains nothing.
+template <int HD>
+struct QLoads {
+  static constexpr bool kEarly = HD == 128;
+  static constexpr int CH = HD / 8, N = tcc::BM * CH / (tcc::kSoftWarps * 32);
+  float4 x0[N], x1[N];
+};
+
+template <int HD>
+__device__ __forceinline__ void load_q(const ChunkArgs& a, int r0, int kvh, QLoads<HD>& q) {
+  using Q = QLoads<HD>;
+  const int n_rows = a.T * a.G;
+#pragma unroll
+  for (int i = 0; i < Q::N; ++i) {
+    const int at = (int)threadIdx.x + i * tcc::kSoftWarps * 32, gr = r0 + at / Q::CH, c = at % Q::CH;
+    q.x0[i] = q.x1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (gr < n_rows) {
+      const int t = (int)fdiv((unsigned)gr, a.div_g);
+      const float4* src = reinterpret_cast<const float4*>(
+          a.q + ((size_t)t * a.n_q + (size_t)kvh * a.G + (gr - t * a.G)) * HD + 8 * c);
+      q.x0[i] = __ldg(src);
+      q.x1[i] = __ldg(src + 1);
+    }
+  }
+}
 
 // The softmax of a scored chunk: thread = (query row, half of the columns).
 // Returns whether a wait was lost; m (the same in a row's two threads) and l
 // (each its own columns') are left for the output.
 template <int HD>
 __device__ __forceinline__ bool softmax_scored(const ChunkArgs& a, unsigned char* smem, uint32_t sbase, uint32_t tmem,
-                                               const Key key, int row, int tok, int kvh, int gg, bool valid, uint32_t wl,
+                                               const Key key, QLoads<HD>& q, int r0, int row, int tok, int kvh, int gg, bool valid, uint32_t wl,
                                                float (*s_pair)[tcc::BM], int* s_flag, float& m, float& l) {
   using namespace tcc;
   using Lay = TcLayout<HD>;
@@ -225,24 +255,10 @@ __device__ __forceinline__ bool softmax_scored(const ChunkArgs& a, unsigned char
   const float slope =
       valid && a.slopes != nullptr ? 1.4426950408889634f * __ldg(a.slopes + kvh * a.G + gg) : 0.f;
   {
-    // q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand, 8 dims a step,
-    // neighbours of a row by neighbouring lanes (row by row a thread, as the plain
-    // kernel does it, these loads took 3.9 us of a CTA)
-    constexpr int CH = HD / 8, N = tcc::BM * CH / (kSoftWarps * 32);
-    const int n_rows = a.T * a.G;
-    float4 x0[N], x1[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = (int)threadIdx.x + i * kSoftWarps * 32, gr = key.r0 + at / CH, c = at % CH;
-      x0[i] = x1[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (gr < n_rows) {
-        const int t = (int)fdiv((unsigned)gr, a.div_g);
-        const float4* src = reinterpret_cast<const float4*>(
-            a.q + ((size_t)t * a.n_q + (size_t)kvh * a.G + (gr - t * a.G)) * HD + 8 * c);
-        x0[i] = __ldg(src);
-        x1[i] = __ldg(src + 1);
-      }
-    }
+    // q * sm_scale * log2(e) -> fp16 hi + lo rows of the A operand
+    constexpr int CH = HD / 8, N = QLoads<HD>::N;
+    if constexpr (!QLoads<HD>::kEarly) load_q<HD>(a, r0, kvh, q);
+    const float4 (&x0)[N] = q.x0, (&x1)[N] = q.x1;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int at = (int)threadIdx.x + i * kSoftWarps * 32, r = at / CH, c = at % CH;
@@ -544,7 +560,9 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
   const int t_last = min(a.T - 1, (min(r0 + BM, n_rows) - 1) / a.G);
   int n_all = (P0 + t_last + 1 + BN - 1) / BN;     // key tiles the CTA's rows see
   int tile0 = 0;                                   // and the first of them
+  QLoads<kScores ? HD : 64> q;
   if constexpr (kScores) {
+    if (QLoads<HD>::kEarly && warp < kSoftWarps) load_q<HD>(a, r0, kvh, q);
     // the union of what the tile's tokens see (windows and documents move
     // forward with the tokens, so it has no holes to speak of)
     __shared__ int s_seen[2][Lay::THREADS / 32];
@@ -698,7 +716,7 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
       (void)mbar_wait(bar(PDRAIN), 0, wl);
     }
   } else if constexpr (kScores) {
-    lost = softmax_scored<HD>(a, smem, sbase, tmem, Key{j0, n_tiles, P0, r0}, row, tok, kvh, gg, valid, wl, s_pair, s_flag, m, l);
+    lost = softmax_scored<HD>(a, smem, sbase, tmem, Key{j0, n_tiles, P0}, q, r0, row, tok, kvh, gg, valid, wl, s_pair, s_flag, m, l);
   } else {
     // ---------------- softmax warps: thread = query row ----------------
     const int lim = valid ? P0 + tok : -1;                  // last key this row sees
