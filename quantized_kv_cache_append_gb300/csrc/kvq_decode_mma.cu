@@ -12,7 +12,7 @@
 //               scales by bulk copies; an mbarrier per stage counts the
 //               bytes in.  Thread 0 issues the first stages; after that the
 //               warp that releases a stage last (a shared-memory counter)
-//               issues its refill.
+//               issues its refill (scored: or each warp its own, kWarpSlices).
 //   q.k         each warp owns 16 cells of every stage.  S^T = K . Q^T is a
 //               16-cell x 8-row mma.sync.m16n8k16 per 16 dims.  int8 K
 //               enters as the exact fp16 value 1152 + code, and 1152 * sum(q)
@@ -132,8 +132,12 @@ struct Cfg {
   // Scored, head_dim 256 of int8 keys: two stages where that is one more CTA an SM
   // (K8V4 with 8 rows: 3; int8 with 16: 2), since the instructions, not the
   // copies, bound them (2 x 98000 cells, 2 heads, 32 rows, blocks of 256: int8
-  // 160 us with 8 rows a CTA and 3 stages, 202 with 16 and 3, 144 with 16 and 2).
-  static constexpr int STAGES = kScores && HD == 256 && (V4 ? NT == 1 : KI8 && NT == 2) ? 2 : (SLAB_B + STAGE_B - 1) / STAGE_B > 3 ? (SLAB_B + STAGE_B - 1) / STAGE_B : 3;
+  // 118 us with 8 rows a CTA and 3 stages, 146 with 16 and 3, 101 with 16 and 2).
+  // FP16 of head_dim 128 with 16 rows: two stages and three CTAs likewise (16 ragged
+  // sequences, 12 or 16 rows 125 and 130 us -> 123 and 126, 32 rows of half the heads
+  // 130 -> 123; with 4 rows it loses, 99 -> 102).
+  static constexpr bool TWO = kScores && (HD == 256 ? (V4 ? NT == 1 : KI8 && NT == 2) : HD == 128 && !KI8 && NT == 2);
+  static constexpr int STAGES = TWO ? 2 : (SLAB_B + STAGE_B - 1) / STAGE_B > 3 ? (SLAB_B + STAGE_B - 1) / STAGE_B : 3;
   static constexpr int OFF_V = TILE_B;
   static constexpr int SMEM_SC = STAGES * STAGE_B;  // [STAGES]{K [64][NG], V [64][VNS]} fp16
   // q as fp16 hi / lo rows, padded by 16 bytes so ldmatrix rows hit distinct banks
@@ -501,8 +505,8 @@ __device__ __forceinline__ void merge_cluster(const DecodeArgs& a, unsigned char
 //                         (one choice for all block sizes; the larger ones decide)
 //   8 rows, head_dim 128, blocks of 64:  48.0, 48.0; 55.6, 55.6; 48.7, 50.0
 //                         blocks of 16:  51.8, 47.9; 66.5, 57.0; 53.8, 50.3
-//   16 rows, head_dim 128, blocks of 64: 143, 141; 134, 130; 151, 149
-//                         blocks of 16:  154, 140; 158, 133; 161, 149
+//   16 rows, head_dim 128, blocks of 64: 143, 141; 134, 130 (126 in two stages); 151, 149
+//                         blocks of 16:  154, 140; 158, 133 (127); 161, 149
 // Two sequences of 65536 to 131072 cells, head_dim 256, blocks of 64:
 //   32 rows:  117, 104; 181, 139; 124, 113       8 rows:  44.7, 41.8; 55, 53; 45.6, 42
 //   (blocks of 16: 145, 112; 239, 155; 151, 122           53.7, 43.5; 84, 58; 52, 45)
@@ -2089,8 +2093,8 @@ bool mma_decode_supported(int fmt, int hd, int rows) {
 int mma_rows_per_cta(int hd) { return 8 * (256 / hd); }
 // Scored: 16 at 256 too, twice the accumulators, but half of the widening and of
 // the copies a row (2 x 98000 cells, 2 heads, 32 rows of 256 dims, blocks of 16 /
-// 256: FP16 317 / 217 -> 219 / 173 us, int8 202 / 160 -> 164 / 144, K8V4 180 / 147 ->
-// 169 / 152).
+// 256: FP16 194 / 146 -> 155 / 131 us, int8 137 / 118 -> 112 / 101, K8V4 129 / 116 ->
+// 122 / 110).
 int scores_rows_per_cta(int hd) { return hd == 256 ? 16 : mma_rows_per_cta(hd); }
 
 int mma_cell_tile() { return kTC; }
