@@ -198,3 +198,50 @@ def test_lost_waits_give_nan_and_leave_the_context_usable(n_kv, G, hd, P, T):
     for dtype in TYPES:
         assert c.run(scores, dtype, lost=(3000, 16)).isnan().all()
     assert torch.equal(c.run(scores), want)
+
+
+@pytest.mark.parametrize("hd,tile", [(64, 128), (128, 128), (256, 64)])
+@pytest.mark.parametrize("splits", range(2, 9))
+def test_key_splits_merge(hd, tile, splits):
+    # as many key tiles as up to `splits` splits take; rows that see the keys of
+    # one split or of none beside rows that see them all; two heads of a key head
+    # whose scores lie far apart
+    rng = np.random.default_rng([hd, splits])
+    P, T = (4 * splits + 1) * tile - 5, 37
+    c = Case(rng, 1, 3, hd, P, T)
+    c.dq[:, 1] *= 6
+    c.q[:, 1] *= 6
+    pos = np.arange(P - T, P)
+    first = np.where(np.arange(T) % 4 == 1, pos - 20, np.where(np.arange(T) % 4 == 2, pos + 1, 0))
+    first[3] = pos[3]
+    for dtype in TYPES:
+        c.check(dtype, first=first)
+    c.check(cap=8.0, slopes=np.array([0.5, -0.01, 0.0], np.float32))
+
+
+def test_a_chunk_that_reads_the_one_before():
+    # each call's q is the output of the last: launched while it ends, it must not
+    # read before; the same one by one, in a row and captured
+    rng = np.random.default_rng(9)
+    for hd, P, T in ((64, 4000, 60), (128, 1000, 300), (256, 2000, 50)):
+        c = Case(rng, 2, 2, hd, P, T)
+        scores = kvq.make_scores(20.0, 600)
+        bufs = [c.dq] + [torch.zeros(T, 4, hd, device="cuda") for _ in range(6)]
+
+        def row(wait):
+            for a, b in zip(bufs, bufs[1:]):
+                assert kvq.kvq_chunk_attn_scored(c.dk, c.dv, 2, P, hd, scores, a, T, 4, c.sm * 8, b) == kvq.KVQ_OK
+                if wait:
+                    torch.cuda.synchronize()
+
+        row(True)
+        want = [b.clone() for b in bufs[1:]]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            row(False)
+        for f in (lambda: row(False), g.replay, g.replay):
+            for b in bufs[1:]:
+                b.zero_()
+            f()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(bufs[1:], want))
