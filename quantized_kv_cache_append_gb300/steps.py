@@ -17,9 +17,10 @@ class StepPlanner:
 
     plan(n_new) leaves the step's arrays in tok_seq, tok_pos, slots
     [max_tok], tok_start [n_seq + 1], ctx_start (the lengths before),
-    ctx_lens (the lengths after), block_table and info (tokens, blocks handed
-    out, blocks given back, status); the next plan overwrites them.  The
-    addresses stay the same, so a captured graph may hold whole steps."""
+    ctx_lens (the lengths after), block_table and plan_info (tokens, blocks
+    handed out, blocks given back, status); the next plan overwrites them.  trim
+    writes trim_info; info is that of the last call, plan_info or trim_info.
+    The addresses stay the same, so a captured graph may hold whole steps."""
 
     def __init__(self, n_seq: int, max_blocks: int, block_size: int, n_blocks: int, max_tok: int,
                  device="cuda"):
@@ -39,21 +40,24 @@ class StepPlanner:
         self.free_list = torch.arange(n_blocks - 1, -1, -1, dtype=torch.int32, device=device)
         self.tok_start = ints(n_seq + 1)
         self.tok_seq, self.tok_pos, self.slots = (ints(max_tok, fill=-1) for _ in range(3))
-        self.info = ints(4)
+        self.plan_info, self.trim_info = ints(4), ints(4)
+        self.info = self.plan_info
+        self._placed = torch.ones(1, dtype=torch.bool, device=device)   # whether the last plan was
+        self._drop = ints(n_seq)
 
     def _check(self, call: str, name: str, t) -> None:
-        if (t.shape != (self.n_seq,) or t.dtype != torch.int32 or not t.is_contiguous()
-                or t.device != self.info.device):
-            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: {name} must be a contiguous int32 [n_seq] on "
-                                        f"{self.info.device}")
-        if self.info.device.type != "cuda":
-            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: the planner is on {self.info.device}, not a GPU")
+        dev = self.plan_info.device
+        if t.shape != (self.n_seq,) or t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
+            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: {name} must be a contiguous int32 [n_seq] on {dev}")
+        if dev.type != "cuda":
+            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: the planner is on {dev}, not a GPU")
 
     def plan(self, n_new, stream=None) -> None:
         """n_new int32 [n_seq] on the device: tokens each sequence gets;
         negative: it ends and gives its blocks back.  A step that cannot be
-        placed changes nothing and says why in info[3]."""
+        placed changes nothing and says why in plan_info[3]."""
         self._check("plan", "n_new", n_new)
+        self.info = self.plan_info
         with torch.cuda.device(self.info.device), on_stream(stream):
             self._before.copy_(self._after)
             check(kvq_plan_step(self.ctx_start, n_new, self.n_seq, self.block_size, self.n_blocks,
@@ -64,12 +68,17 @@ class StepPlanner:
 
     def trim(self, n_drop, stream=None) -> None:
         """n_drop int32 [n_seq] on the device: cells taken back from the end of
-        each sequence (verify_draft's n_dropped).  ctx_lens shrink (ctx_start
-        are the lengths before), blocks go back; info: cells taken back, 0,
-        blocks given back, status.  The plan's token arrays stay as they are."""
+        each sequence (verify_draft's n_dropped, or more: a rollback).  ctx_lens
+        shrink (ctx_start are the lengths before), blocks go back; trim_info:
+        cells taken back, 0, blocks given back, status.  The plan's token arrays
+        stay as they are.  Behind a plan that could not be placed, whose tokens
+        are in no cell, nothing is taken back until another plan is placed."""
         self._check("trim", "n_drop", n_drop)
+        self.info = self.trim_info
         with torch.cuda.device(self.info.device), on_stream(stream):
             self._before.copy_(self._after)
-            check(kvq_trim_step(self.ctx_start, n_drop, self.n_seq, self.block_size, self.n_blocks,
+            torch.eq(self.plan_info[3:], 0, out=self._placed)
+            torch.mul(n_drop, self._placed, out=self._drop)
+            check(kvq_trim_step(self.ctx_start, self._drop, self.n_seq, self.block_size, self.n_blocks,
                                 self.block_table, self.max_blocks, self.free_list, self._count_in,
                                 self.ctx_lens, self.free_count, self.info, stream), "kvq_trim_step")
