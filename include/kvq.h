@@ -805,6 +805,10 @@ kvq_status kvq_chunk_attn_scored_lost_wait_test(const void *k16, const void *v16
  *   n_draft      device int32 [n_seq] or NULL (W - 1): drafts of each
  *                sequence, at most W - 1 (more count as W - 1); negative: the
  *                sequence takes no part: 0 accepted, tokens -1, 0 dropped
+ *                (a sequence the step gave no token, or whose plan was
+ *                refused, has to take no part: its drafts are in no cell).
+ *                Fewer drafts: a sequence's rows are the first of its W,
+ *                where the attention calls have its tokens in the last
  *   u            device fp32 [n_seq][W - 1], u_sample device fp32 [n_seq]:
  *                uniform in [0, 1)
  *   n_accepted   device int32 [n_seq]

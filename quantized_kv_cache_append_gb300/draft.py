@@ -11,9 +11,14 @@ from .pool import ELEMENT_TYPES, on_stream
 def verify_draft(target, draft, draft_tokens, u, u_sample, n_draft=None, out=None, stream=None):
     """target [n_seq][W][vocab], draft [n_seq][W - 1][vocab] (None: certain
     drafts) probabilities, draft_tokens int32 and u fp32 [n_seq][W - 1],
-    u_sample fp32 [n_seq], n_draft int32 [n_seq] (None: W - 1) -> (n_accepted
-    [n_seq], tokens [n_seq][W], n_dropped [n_seq]), int32; out: such a tuple
-    to write.  Rows may be wider than vocab (a padded array's view)."""
+    u_sample fp32 [n_seq], n_draft int32 [n_seq] -> (n_accepted [n_seq], tokens
+    [n_seq][W], n_dropped [n_seq]), int32; out: such a tuple to write.  Rows may
+    be wider than vocab (a padded array's view).
+
+    n_draft None says that every sequence of the batch has W - 1 drafts in its
+    cache.  Where some have fewer, or take no part in the step (negative), it has
+    to be given (StepPlanner.n_draft): n_dropped counts drafts, and a trim by it
+    takes that many cells."""
     n_seq, W, vocab = target.shape
     dev = target.device
 

@@ -66,6 +66,35 @@ class StepPlanner:
                                 self.tok_pos, self.slots, self.free_count, self.info, stream),
                   "kvq_plan_step")
 
+    def n_draft(self, out=None, stream=None):
+        """verify_draft's n_draft behind a plan whose tokens were each sequence's
+        last sampled one and its drafts: int32 [n_seq], the tokens placed less
+        one; negative, so that verify_draft passes the sequence over, where it got
+        none, ended, or the plan was not placed.  To be read before trim."""
+        if out is not None:
+            self._check("n_draft", "out", out)
+        with torch.cuda.device(self.plan_info.device), on_stream(stream):
+            return torch.sub(self.ctx_lens, self.ctx_start, out=out).sub_(1)
+
+    def window_rows(self, W: int, n_tok: int, stream=None):
+        """Where the plan's first n_tok tokens, which are packed, stand in arrays
+        of W rows a sequence: (attend, verify), int64 [n_tok].  The attention has a
+        sequence's tokens in the last rows of its window (row W - 1 is its last
+        cell), verify_draft its first in row 0; the two are the same where every
+        sequence got W tokens.  Row n_seq * W, behind the arrays, stands for
+        padding and for tokens that the window does not reach.  To be read before
+        trim."""
+        if W < 1 or not 0 <= n_tok <= self.max_tok:
+            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.window_rows: W = {W}, n_tok = {n_tok} of {self.max_tok}")
+        with torch.cuda.device(self.plan_info.device), on_stream(stream):
+            seq, pos = self.tok_seq[:n_tok].long(), self.tok_pos[:n_tok]
+            none = self.n_seq * W
+
+            def rows(at):
+                return torch.where((seq >= 0) & (at >= 0) & (at < W), seq * W + at, none)
+
+            return rows(W + pos - self.ctx_lens[seq]), rows(pos - self.ctx_start[seq])
+
     def trim(self, n_drop, stream=None) -> None:
         """n_drop int32 [n_seq] on the device: cells taken back from the end of
         each sequence (verify_draft's n_dropped, or more: a rollback).  ctx_lens
