@@ -45,6 +45,14 @@ def row_layout(fmt: int, head_dim: int):
     raise ValueError(f"unknown cache format {fmt}")
 
 
+def _held(settings, **arrays):
+    """For PagedPool._check: the tensors, in their order, that make_rotary or
+    make_scores put into `settings`, with what each has to be (raw addresses are
+    the caller's word)."""
+    held = getattr(settings, "held", ())
+    return {name: (t, *spec) for (name, spec), t in zip(arrays.items(), held) if isinstance(t, torch.Tensor)}
+
+
 class BlockBounds:
     """Bounds of a pool's keys, a block and KV head at a time: int8 codes
     [n_blocks][n_kv][2][hd] (lo, hi) and fp32 scales [n_blocks][n_kv][hd/64]."""
@@ -96,7 +104,8 @@ class PagedPool:
         `rotary` (make_rotary); returns q [n_tok][n_q][hd] normed and rotated,
         fp32.  The three may be views of one wider array (heads side by side,
         tokens evenly apart).  Padding tokens' rows of q_out stay as they were
-        (a q_out allocated here: unset)."""
+        (a q_out allocated here: unset).  The rotary's tensors are fp32 (a norm's
+        weights too, whatever type the model holds them in), pair_axis int32."""
         n_tok, n_q, hd = q.shape
         if q.dtype not in ELEMENT_TYPES or ELEMENT_TYPES[q.dtype] != rotary.type:
             raise KvqError(KVQ_ERR_ARG, f"append_rotary: q is {q.dtype}, which is not the rotary's type")
@@ -113,7 +122,10 @@ class PagedPool:
             self._check("append_rotary", tok_seq=(tok_seq, i32, (n_tok,)), tok_pos=(tok_pos, i32, (n_tok,)),
                         block_table=(block_table, i32, (None, None)),
                         positions=(positions, i32, (rotary.n_axes, n_tok)),
-                        q_out=(q_out, torch.float32, (n_tok, n_q, hd)))
+                        q_out=(q_out, torch.float32, (n_tok, n_q, hd)),
+                        **_held(rotary, inv_freq=(torch.float32, (rotary.rot_dim // 2,)),
+                                pair_axis=(i32, (rotary.rot_dim // 2,)), q_norm=(torch.float32, (hd,)),
+                                k_norm=(torch.float32, (hd,))))
             check(kvq_append_rotary(self.cache, rotary, q, k, v, stride(q), stride(k), stride(v), n_tok, n_q,
                                     tok_seq, tok_pos, positions, block_table, int(block_table.shape[0]),
                                     int(block_table.shape[1]), q_out, stream), "kvq_append_rotary")
@@ -147,13 +159,10 @@ class PagedPool:
             if workspace is None:
                 need = kvq_scored_workspace_bytes(self.cache, scores, n_seq, W, n_q, max_ctx)
                 workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-            slopes, first, last = getattr(scores, "held", (None, None, None))
-            held = {n: (t, dt, shape) for n, t, dt, shape in (("slopes", slopes, f32, (n_q,)),
-                                                             ("first", first, i32, (n_seq,)))
-                    if isinstance(t, torch.Tensor)}
             self._check("decode_scored", q=(q, f32, (n_seq, W, n_q, self.head_dim)),
                         ctx_lens=(ctx_lens, i32, (n_seq,)), block_table=(block_table, i32, (n_seq, None)),
-                        out=(out, f32, (n_seq, W, n_q, hd)), workspace=(workspace, torch.uint8, (None,)), **held)
+                        out=(out, f32, (n_seq, W, n_q, hd)), workspace=(workspace, torch.uint8, (None,)),
+                        **_held(scores, slopes=(f32, (n_q,)), first=(i32, (n_seq,))))
             check(kvq_decode_attn_scored(self.cache, scores, q, n_seq, W, n_q, ctx_lens, max_ctx, block_table,
                                          int(block_table.shape[1]), sm_scale, out, workspace,
                                          workspace.numel(), stream), "kvq_decode_attn_scored")
