@@ -11,8 +11,8 @@ import contextlib
 import torch
 
 from . import (KVQ_ERR_ARG, KVQ_F16, KVQ_GROUP, KVQ_K8V4, KVQ_Q4_BLOCK, KVQ_Q8, KVQ_T_BF16, KVQ_T_F16,
-               KVQ_T_F32, KvqError, check, kvq_append, kvq_append_rotary, kvq_bound_blocks, kvq_decode_attn_scored,
-               kvq_scored_workspace_bytes, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
+               KVQ_T_F32, KvqError, check, kvq_append, kvq_append_rotary, kvq_bound_blocks, kvq_chunk_attn_scored,
+               kvq_decode_attn_scored, kvq_scored_workspace_bytes, kvq_compact_f16, kvq_decode_attn, kvq_decode_workspace_bytes,
                kvq_select_blocks, kvq_sparse_decode_attn, kvq_sparse_workspace_bytes, make_cache)
 
 
@@ -178,6 +178,27 @@ class PagedPool:
             check(kvq_compact_f16(self.cache, block_table_row, n_cells, out_k, out_v, stream),
                   "kvq_compact_f16")
         return out_k, out_v
+
+    def chunk_scored(self, k16, v16, q, sm_scale: float, scores, out=None, out_dtype=torch.float32, stream=None):
+        """Attention of a prompt chunk's q [T][n_q][hd] fp32 over k16, v16
+        [n_kv][P][hd] (compact's, the chunk's cells the last T of them) with the
+        capped, biased or masked scores of make_scores (first, last: int32 [T]);
+        out [T][n_q][hd], of out_dtype (fp32, fp16 or bf16) if it is not given."""
+        T, n_q, hd = q.shape
+        P = k16.shape[1]
+        f16, i32 = torch.float16, torch.int32
+        if (out_dtype if out is None else out.dtype) not in ELEMENT_TYPES:
+            raise KvqError(KVQ_ERR_ARG, f"chunk_scored: output of {out_dtype if out is None else out.dtype}")
+        with self._on(stream):
+            if out is None:
+                out = torch.empty((T, n_q, hd), dtype=out_dtype, device=q.device)
+            self._check("chunk_scored", k16=(k16, f16, (self.n_kv, P, self.head_dim)),
+                        v16=(v16, f16, (self.n_kv, P, self.head_dim)), q=(q, torch.float32, (T, n_q, self.head_dim)),
+                        out=(out, out.dtype, (T, n_q, hd)),
+                        **_held(scores, slopes=(torch.float32, (n_q,)), first=(i32, (T,)), last=(i32, (T,))))
+            check(kvq_chunk_attn_scored(k16, v16, self.n_kv, P, hd, scores, q, T, n_q, sm_scale, out,
+                                        ELEMENT_TYPES[out.dtype], stream), "kvq_chunk_attn_scored")
+        return out
 
     def _check(self, where: str, **tensors) -> None:
         """Each given (tensor, dtype, shape) is contiguous on the pool's device;
