@@ -112,8 +112,13 @@ bool plan_decode(const kvq_cache* c, int n_seq, int W, int n_q, int max_ctx, Dec
   p->c_log2 = -1;
   p->batch_items = 0;
   p->off_base = 0;
-  if (kind == Decode::kScored && (long long)n_seq * (tiles + 1) < (1LL << 30))   // (summed in 32 bits)
+  if (kind == Decode::kScored && (long long)n_seq * (tiles + 1) < (1LL << 30)) {   // (summed in 32 bits)
+    // no more than the tiles there can be (one a split), and more than n_seq, which
+    // the choice on the device needs
+    const int most = n_seq * tiles > n_seq ? n_seq * tiles : n_seq + 1;
     p->batch_items = batch_items(capacity, c->n_kv_heads * p->n_rt, n_seq);
+    if (p->batch_items > most) p->batch_items = most;
+  }
   DecodePlan in_cluster = *p;
   if (lists) {
     // Splits of a row tile in one cluster of up to 8, merged there, if that
