@@ -398,18 +398,20 @@ __device__ __forceinline__ bool softmax_scored(const ChunkArgs& a, unsigned char
 
 // 8 output values of a row, at value index i (a multiple of 8)
 __device__ __forceinline__ void store8(const ChunkArgs& a, size_t i, const float (&v)[8]) {
-  if (!kScores || a.out_type == KVQ_T_F32) {
-    store4(a, i, make_float4(v[0], v[1], v[2], v[3]));
-    store4(a, i + 4, make_float4(v[4], v[5], v[6], v[7]));
-    return;
-  }
-  uint32_t u[4];
+  if constexpr (kScores) {
+    if (a.out_type != KVQ_T_F32) {
+      uint32_t u[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (a.out_type == KVQ_T_F16) u[e] = pack_half2(v[2 * e], v[2 * e + 1]);
-    else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+      for (int e = 0; e < 4; ++e) {
+        if (a.out_type == KVQ_T_F16) u[e] = pack_half2(v[2 * e], v[2 * e + 1]);
+        else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[e]) : "f"(v[2 * e + 1]), "f"(v[2 * e]));
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_any) + i) = make_uint4(u[0], u[1], u[2], u[3]);
+      return;
+    }
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out_any) + i) = make_uint4(u[0], u[1], u[2], u[3]);
+  store4(a, i, make_float4(v[0], v[1], v[2], v[3]));
+  store4(a, i + 4, make_float4(v[4], v[5], v[6], v[7]));
 }
 
 // The merge of a cluster's key splits, scored.  Each CTA owns a share of the
@@ -852,14 +854,14 @@ __global__ void __launch_bounds__(tcc::TcLayout<HD>::THREADS, 1)
               }
               store8(a, orow + c0 + e, v);
             }
-            continue;
-          }
+          } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            float4 r4 = make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
-                                    __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
-            if (lost) r4 = make_float4(nan, nan, nan, nan);
-            store4(a, orow + c0 + e, r4);
+            for (int e = 0; e < 32; e += 4) {
+              float4 r4 = make_float4(__uint_as_float(ov[e]) * inv, __uint_as_float(ov[e + 1]) * inv,
+                                      __uint_as_float(ov[e + 2]) * inv, __uint_as_float(ov[e + 3]) * inv);
+              if (lost) r4 = make_float4(nan, nan, nan, nan);
+              store4(a, orow + c0 + e, r4);
+            }
           }
         }
       }
