@@ -130,8 +130,8 @@ struct Cfg {
   // fp32, which takes a fourth stage for 32-row int8 HD 64 tiles)
   static constexpr int SLAB_B = kConsumerWarps * NT * 8 * HD * 4;
   // Scored, head_dim 256 of int8 keys: two stages where that is one more CTA an SM
-  // (K8V4 with 8 rows: 3; int8 with 16: 2), since the instructions, not the
-  // copies, bound them (2 x 98000 cells, 2 heads, 32 rows, blocks of 256: int8
+  // (K8V4 with 8 rows: 3; int8 with 16: 2), since warps that are ready, not
+  // copies under way, are what they lack (2 x 98000 cells, 2 heads, 32 rows, blocks of 256: int8
   // 118 us with 8 rows a CTA and 3 stages, 146 with 16 and 3, 101 with 16 and 2).
   // FP16 of head_dim 128 with 16 rows: two stages and three CTAs likewise (16 ragged
   // sequences, 12 or 16 rows 125 and 130 us -> 123 and 126, 32 rows of half the heads
