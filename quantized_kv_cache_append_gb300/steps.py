@@ -45,10 +45,14 @@ class StepPlanner:
         self._placed = torch.ones(1, dtype=torch.bool, device=device)   # whether the last plan was
         self._drop = ints(n_seq)
 
-    def _check(self, call: str, name: str, t) -> None:
+    def _check(self, call: str, **tensors) -> None:
+        """Each tensor (None: left out) is a contiguous int32 [n_seq] on the
+        planner's device, which is a GPU."""
         dev = self.plan_info.device
-        if t.shape != (self.n_seq,) or t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev:
-            raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: {name} must be a contiguous int32 [n_seq] on {dev}")
+        for name, t in tensors.items():
+            if t is not None and (t.shape != (self.n_seq,) or t.dtype != torch.int32 or not t.is_contiguous()
+                                  or t.device != dev):
+                raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: {name} must be a contiguous int32 [n_seq] on {dev}")
         if dev.type != "cuda":
             raise KvqError(KVQ_ERR_ARG, f"StepPlanner.{call}: the planner is on {dev}, not a GPU")
 
@@ -56,7 +60,7 @@ class StepPlanner:
         """n_new int32 [n_seq] on the device: tokens each sequence gets;
         negative: it ends and gives its blocks back.  A step that cannot be
         placed changes nothing and says why in plan_info[3]."""
-        self._check("plan", "n_new", n_new)
+        self._check("plan", n_new=n_new)
         self.info = self.plan_info
         with torch.cuda.device(self.info.device), on_stream(stream):
             self._before.copy_(self._after)
@@ -71,8 +75,7 @@ class StepPlanner:
         last sampled one and its drafts: int32 [n_seq], the tokens placed less
         one; negative, so that verify_draft passes the sequence over, where it got
         none, ended, or the plan was not placed.  To be read before trim."""
-        if out is not None:
-            self._check("n_draft", "out", out)
+        self._check("n_draft", out=out)
         with torch.cuda.device(self.plan_info.device), on_stream(stream):
             return torch.sub(self.ctx_lens, self.ctx_start, out=out).sub_(1)
 
@@ -84,6 +87,7 @@ class StepPlanner:
         sequence got W tokens.  Row n_seq * W, behind the arrays, stands for
         padding and for tokens that the window does not reach.  To be read before
         trim."""
+        self._check("window_rows")
         if W < 1 or not 0 <= n_tok <= self.max_tok:
             raise KvqError(KVQ_ERR_ARG, f"StepPlanner.window_rows: W = {W}, n_tok = {n_tok} of {self.max_tok}")
         with torch.cuda.device(self.plan_info.device), on_stream(stream):
@@ -102,7 +106,7 @@ class StepPlanner:
         cells taken back, 0, blocks given back, status.  The plan's token arrays
         stay as they are.  Behind a plan that could not be placed, whose tokens
         are in no cell, nothing is taken back until another plan is placed."""
-        self._check("trim", "n_drop", n_drop)
+        self._check("trim", n_drop=n_drop)
         self.info = self.trim_info
         with torch.cuda.device(self.info.device), on_stream(stream):
             self._before.copy_(self._after)
