@@ -855,8 +855,11 @@ kvq_status kvq_verify_draft(const void *target, const void *draft, int type, int
  *
  * A step with a broken argument changes nothing (ctx_out = ctx_in, info 0, 0,
  * 0, status): KVQ_PLAN_ROW for a length below 0 or beyond its row or an
- * n_drop outside [0, ctx_in], KVQ_PLAN_LIST as in kvq_plan_step.  Limits,
- * overlap rules and errors as there.  One launch, no workspace.
+ * n_drop outside [0, ctx_in], KVQ_PLAN_LIST as in kvq_plan_step.  The call
+ * knows nothing of the plan before it: the tokens of a refused plan are in no
+ * cell, and n_drop has to be 0 for them (kvq_verify_draft's n_dropped is, with
+ * n_draft negative).  Limits, overlap rules and errors as there.  One launch, no
+ * workspace.
  */
 kvq_status kvq_trim_step(const int32_t *ctx_in, const int32_t *n_drop, int n_seq, int block_size,
                          int n_blocks, const int32_t *block_table, int max_blocks_per_seq,
